@@ -162,10 +162,10 @@ def work(case):
 # ------------------------------------------------------------------ inputs
 def _quantise(x):
     """E4M3 codes (as bytes) and E8M0 bytes of rows x [..., dim] in 32 bits: the scale is the
-    smallest power of two 2^e with max|x| <= 448 * 2^e (e in -124..15; 1 for a row of zeros)."""
+    smallest power of two 2^e with max|x| <= 448 * 2^e (e in -124..7; 1 for a row of zeros)."""
     amax = x.abs().amax(-1)
     mant, e = torch.frexp(amax / 448)  # amax / 448 = mant * 2^e with mant in [0.5, 1)
-    e = torch.where(mant == 0.5, e - 1, e).clamp(-124, 15)
+    e = torch.where(mant == 0.5, e - 1, e).clamp(-124, 7)
     e = torch.where(amax == 0, torch.zeros_like(e), e)
     codes = torch.ldexp(x, -e[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
     return codes.view(torch.uint8), (e + 127).to(torch.uint8)
@@ -455,7 +455,7 @@ def _exact_rows(y):
     some = top > 0
     e[some] = torch.ceil(torch.log2(top[some] / 448))
     e = torch.where(some & (top > 448 * torch.exp2(e)), e + 1, torch.where(some & (top <= 448 * torch.exp2(e - 1)), e - 1, e))
-    e = e.clamp(-124, 15)
+    e = e.clamp(-124, 7)
     return _nearest_codes(y * torch.exp2(-e)[..., None]), (e + 127).to(torch.uint8)
 
 
