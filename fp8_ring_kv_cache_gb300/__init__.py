@@ -30,3 +30,7 @@ from ._binding import (  # noqa: F401
     rc_cache_window_shift, rc_tile_kinds,
     rc_status_string,
 )
+from ._paged import (  # noqa: F401
+    RC_PAGED_WORKSPACE_BYTES, RC_ROPE_SHARED_FREQS, PagedBatch, PagedKVCache, RopeAxes, rc_paged_set_wait_limit,
+    rc_rope_axes,
+)

@@ -16,11 +16,10 @@
 #include <new>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "rc.h"
 #include "rc_internal.h"
 #include "rc_layout.h"
+#include "rc_nvtx.h"
 
 using namespace rc;
 
@@ -176,34 +175,20 @@ void refresh_uniform(rc_cache* h, int layer) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// A named NVTX range around each entry point that enqueues work, so that a
-// timeline tool (Nsight Systems, or ncu --nvtx --nvtx-include) shows which
-// call launched which kernels; with no tool attached the calls do nothing.
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange&) = delete;
-    NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
 // Host-side fault injection for the failure-path tests, read from the
 // environment at each use: RC_FAULT_INJECT=alloc:K makes the K-th allocation
-// (1-based; device or pinned) of an rc_cache_create fail, RC_FAULT_INJECT=launch
-// makes every entry point that launches kernels fail with RC_ERR_CUDA after its
-// argument checks and before it changes anything.  Unset: nothing is injected.
+// (1-based; device or pinned) of an rc_cache_create fail (launch_fault, the
+// other form, is shared with the paged calls).  Unset: nothing is injected.
 struct FaultPlan {
     int alloc_at = 0;
-    bool launch = false;
 };
 FaultPlan fault_plan() {
     FaultPlan f;
     const char* e = std::getenv("RC_FAULT_INJECT");
     if (e == nullptr) return f;
     if (std::strncmp(e, "alloc:", 6) == 0) f.alloc_at = std::atoi(e + 6);
-    if (std::strcmp(e, "launch") == 0) f.launch = true;
     return f;
 }
-bool launch_fault() { return fault_plan().launch; }
 
 bool is_arith(const int64_t* p, int n) {
     for (int t = 1; t < n; ++t)

@@ -1,0 +1,203 @@
+// rc_paged.cuh -- what the kernels over the paged cache share: parameter
+// blocks, the sequence and page lookups (every index read from device memory
+// is checked here before it is used), and the decode of E4M3 codes with E8M0
+// scales to bf16.
+#pragma once
+#include "rc.h"
+#include "rc_device.cuh"
+#include "rc_internal.h"
+
+namespace rc {
+
+// Frequencies of the dimension pairs in turns, 64-bit fixed point.
+struct RopePlanDev {
+    uint64_t turns[kMaxHalfDim];
+    uint8_t axis[kMaxHalfDim];
+};
+
+struct PagedParams {
+    uint8_t* kcodes;
+    uint8_t* vcodes;
+    uint8_t* kscale;
+    uint8_t* vscale;
+    const int32_t* page_table;
+    const int32_t* kv_len;
+    const int32_t* q_start;
+    int* status;
+    int pages, kv_heads, page_shift;  // tokens of a page = 1 << page_shift (4 .. 7)
+    int seqs, table_pages, tokens, max_new, max_kv;
+};
+
+// Device status word of the paged calls.
+constexpr int kDevBadMeta = 301;
+
+__device__ __forceinline__ void flag_meta(int* status) { atomicCAS(status, 0, kDevBadMeta); }
+
+struct Seq {
+    int q0, n, kv;  // first row, new tokens, cached tokens (new ones included)
+};
+
+// Sequence s as the metadata gives it; empty (and flagged) if it is out of the
+// bounds that the host was told.
+__device__ __forceinline__ Seq load_seq(const PagedParams& p, int s) {
+    Seq q;
+    q.kv = __ldg(p.kv_len + s);
+    q.q0 = __ldg(p.q_start + s);
+    const int end = __ldg(p.q_start + s + 1);
+    q.n = end - q.q0;
+    if (q.kv < 0 || q.kv > p.max_kv || q.q0 < 0 || end < q.q0 || end > p.tokens || q.n > p.max_new) {
+        flag_meta(p.status);
+        q.q0 = q.n = q.kv = 0;
+    }
+    return q;
+}
+
+// Page of tokens [i P, i P + P) of sequence s, or -1 (flagged) if the table
+// holds no page of the pool.  i P < kv_len <= table_pages P by load_seq.
+__device__ __forceinline__ int load_page(const PagedParams& p, int s, int i) {
+    const int page = __ldg(p.page_table + static_cast<size_t>(s) * p.table_pages + i);
+    if (page < 0 || page >= p.pages) {
+        flag_meta(p.status);
+        return -1;
+    }
+    return page;
+}
+
+// (cos, sin) of position * frequency: the product modulo one turn is exact in
+// 64-bit integers; the nearest quarter turn is taken off as an integer, so
+// what is left (at most an eighth) converts to fp32 with a relative error of
+// 2^-24 before sincospi sees it.
+__device__ __forceinline__ float2 turn_cos_sin(int pos, uint64_t turns) {
+    const uint32_t frac = static_cast<uint32_t>((static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns) >> 32);
+    const uint32_t quad = (frac + 0x20000000u) >> 30;
+    const int32_t rest = static_cast<int32_t>(frac - (quad << 30));
+    float s, c;
+    sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &s, &c);  // half turns: rest / 2^31
+    const bool odd = quad & 1u;
+    const float cc = odd ? s : c, ss = odd ? c : s;
+    return make_float2((quad == 1u || quad == 2u) ? -cc : cc, (quad & 2u) ? -ss : ss);
+}
+
+// ---------------------------------------------------------------- decode
+// An E4M3 byte s eeee mmm put at s 0000 eeee mmm 0000 of a bf16 word is its
+// value times 2^-120, subnormals included (both formats are then subnormal or
+// normal together); one bf16 multiply by 2^120 times the scale, 2^(b - 7) for
+// an E8M0 byte b, makes it exact.  A word of four codes c0..c3 (c0 in the low
+// byte) gives the pairs (c0, c2) and (c1, c3): two shifts and masks each,
+// where neighbouring codes would need a byte permute more.
+__device__ __forceinline__ uint32_t codes02(uint32_t w) {
+    return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u);
+}
+__device__ __forceinline__ uint32_t codes13(uint32_t w) {
+    return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
+}
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// bf16 factor 2^(b + 120 - 127) of scale byte b, in both halves; bytes over
+// 134 (255: a row that is not finite) give infinity, which makes a zero code
+// NaN and any other code infinite.
+__device__ __forceinline__ uint32_t scale_factor(uint32_t b) {
+    const uint32_t f = min(b + 120u, 255u) << 7;
+    return f | (f << 16);
+}
+// The factors of scale bytes (0, 2) and (1, 3) of a word.
+__device__ __forceinline__ uint32_t scale_factor2(uint32_t two) {  // bytes in bits 0..7 and 16..23
+    return __vminu2(two + 0x00780078u, 0x00ff00ffu) << 7;
+}
+__device__ __forceinline__ uint32_t factors02(uint32_t w) { return scale_factor2(w & 0x00ff00ffu); }
+__device__ __forceinline__ uint32_t factors13(uint32_t w) { return scale_factor2((w >> 8) & 0x00ff00ffu); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// E8M0 byte of a row's scale from its largest magnitude: the smallest e with
+// amax <= 448 * 2^e = 1.75 * 2^(e + 8), cut to -124 .. 7; 0 for a row of zeros.
+__device__ __forceinline__ int scale_exponent(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    const int k = static_cast<int>(u >> 23) - 127;
+    const int e = k - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return amax == 0.f ? 0 : max(-124, min(7, e));
+}
+
+// D (+)= A B, A 16 x 16 row-major fragment, B 16 x 8, fp32 accumulators.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct PagedWriteParams {
+    PagedParams g;
+    RopePlanDev rope;
+    const __nv_bfloat16* K;
+    const __nv_bfloat16* V;
+    const int32_t* pos;
+    int64_t k_stride, v_stride, pos_stride;
+};
+
+struct PagedAttnParams {
+    PagedParams g;
+    const __nv_bfloat16* q;
+    int64_t q_stride;
+    __nv_bfloat16* out;
+    int64_t out_stride;
+    float* lse;        // may be nullptr
+    int heads, group;  // query heads, query heads of one KV head
+    int causal;
+    float sm_log2;     // log2(e) / sqrt(head_dim)
+    int split_tokens;  // cached tokens of one split (a multiple of 256)
+    int splits;        // splits of a sequence of max_kv tokens
+    int row_tiles;     // row tiles of a sequence of max_new tokens
+    float* part;       // workspace: partial results
+    int* counters;     // workspace: arrivals per row tile, all zero between calls
+    uint64_t wait_ns;
+};
+
+struct PagedScoreParams {
+    PagedParams g;
+    const __nv_bfloat16* q;
+    int64_t q_stride;
+    const float* lse;
+    const float* scores;
+    float* out;
+    int64_t score_stride;
+    int heads, group, causal;
+    float sm_log2;
+    uint64_t wait_ns;
+};
+
+struct PagedEvictParams {
+    PagedParams g;
+    const float* scores;
+    int64_t score_stride;
+    int keep, recent, dst_pages;
+    const int32_t* dst_table;
+    int32_t* kept;
+    int32_t* kv_len_out;
+    float* scores_out;  // may be nullptr
+};
+
+struct RopeAxesParams {
+    RopePlanDev rope;
+    const void* x;
+    void* out;
+    int64_t x_stride, out_stride, pos_stride, n;
+    const int32_t* pos;
+    int heads, inverse;
+};
+
+cudaError_t launch_rope_axes(const RopeAxesParams& p, int D, int dtype, cudaStream_t s);
+cudaError_t launch_paged_write(const PagedWriteParams& p, int D, cudaStream_t s);
+cudaError_t launch_paged_attention(PagedAttnParams& p, int D, size_t part_floats, int max_counters, cudaStream_t s);
+cudaError_t launch_paged_scores(const PagedScoreParams& p, int D, cudaStream_t s);
+cudaError_t launch_paged_evict(const PagedEvictParams& p, int D, cudaStream_t s);
+
+}  // namespace rc

@@ -1,0 +1,352 @@
+// rc_paged_attn.cu -- attention of each sequence's new tokens over its pages.
+//
+// paged_rows_kernel, for few query rows (a KV head's rows are its sequence's
+// new tokens x the query heads that share it): bound by reading the codes, so
+// the warps read them straight into the registers where the matrix
+// instructions want them, with no shared memory and no barrier on the way.
+// A block has one (sequence, KV head, tile of 16 rows, split of the cached
+// tokens); a warp takes 64 cached tokens at a time:
+//   S = Q K^T   mma m16n8k16 in bf16: a 16-byte piece of a K row is 16 of the
+//               summed dims for its token; which dims of the product they are
+//               is free as long as Q is held in the same order
+//   P = exp2(S - max), online; P's accumulator layout is the A operand of
+//   O += P V    whose B operand is a 16-byte piece of a V row: 16 tokens of
+//               one dim.  The tokens of S's columns are chosen to match.
+// The warps' (max, sum, O) are joined through shared memory; with several
+// splits they go to the workspace, and the block that arrives last at its row
+// tile's counter joins them in split order, so results do not depend on timing.
+#include <algorithm>
+
+#include "rc_paged.cuh"
+
+namespace rc {
+
+namespace {
+
+constexpr int kRowsWarps = 4;
+constexpr int kRowsThreads = kRowsWarps * 32;
+constexpr int kRowTile = 16;
+constexpr int kChunk = 64;  // cached tokens of a warp's step
+
+// One split's result for a row tile in the workspace: O [16][D], then max and
+// sum [16] each.
+template <int D>
+constexpr int part_floats() {
+    return kRowTile * D + 2 * kRowTile;
+}
+
+// Weight of a partial whose running max is m against the joint max M (both in
+// log2 units; -inf: the partial saw nothing).
+__device__ __forceinline__ float join_weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
+
+template <int D>
+__global__ void __launch_bounds__(kRowsThreads) paged_rows_kernel(PagedAttnParams p) {
+    constexpr int CH = D / 64;  // 16-byte pieces of a K row that a lane reads
+    constexpr int NT = D / 8;   // n tiles of O
+    __shared__ __align__(16) float so[kRowsWarps][kRowTile][D + 4];
+    __shared__ float sm[kRowsWarps][kRowTile], sl[kRowsWarps][kRowTile];
+    __shared__ int last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int split = blockIdx.x, h = blockIdx.y % p.g.kv_heads, tile = blockIdx.y / p.g.kv_heads, s = blockIdx.z;
+    const Seq q = load_seq(p.g, s);
+    const int rows = q.n * p.group;
+    if (tile * kRowTile >= rows) return;
+    // tokens that the tile's last row sees
+    const int last_new = min(q.n - 1, (tile * kRowTile + kRowTile - 1) / p.group);
+    const int seen = p.causal ? max(0, q.kv - q.n + last_new + 1) : q.kv;
+    const int nsplit = max(1, (seen + p.split_tokens - 1) / p.split_tokens);
+    if (split >= nsplit) return;
+    const int j0 = split * p.split_tokens, j1 = min(seen, j0 + p.split_tokens);
+
+    // rows r0 = g and r1 = g + 8 of the tile: token, query head, tokens seen
+    int limit[2];
+    const __nv_bfloat16* qrow[2];
+    bool live[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = tile * kRowTile + g + 8 * i;
+        live[i] = r < rows;
+        const int tok = live[i] ? r / p.group : 0, head = h * p.group + (live[i] ? r - tok * p.group : 0);
+        qrow[i] = p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D;
+        limit[i] = !live[i] ? 1 << 30 : p.causal ? max(0, q.kv - q.n + tok + 1) : q.kv;
+    }
+    // Q fragments: product c * 4 + i of the lane holds dims 16 (t + 4 c) + 4 i + {0, 2} and + {1, 3}
+    uint32_t qa[CH * 4][4];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (live[r]) {
+                a = *reinterpret_cast<const uint4*>(qrow[r] + 16 * (t + 4 * c));
+                b = *reinterpret_cast<const uint4*>(qrow[r] + 16 * (t + 4 * c) + 8);
+            }
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                qa[c * 4 + i][r] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);      // dims 0, 2
+                qa[c * 4 + i][2 + r] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);  // dims 1, 3
+            }
+        }
+
+    float o[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    const int P = 1 << p.g.page_shift;
+
+    for (int jc = j0 + warp * kChunk; jc < j1; jc += kRowsWarps * kChunk) {
+        // The lane reads K rows of the 16-token block g >> 1 and V pieces of
+        // block t.  A block behind the sequence's end, or on a bad page, is
+        // read from page 0 instead and masked (K) or given the factor 0 (V).
+        const int kblk = jc + 16 * (g >> 1), vblk = jc + 16 * t;
+        const int kpage = kblk < q.kv ? load_page(p.g, s, kblk >> p.g.page_shift) : 0;
+        const int vpage = vblk < q.kv ? load_page(p.g, s, vblk >> p.g.page_shift) : 0;
+        const bool vok = vblk < q.kv && vpage >= 0;
+        const size_t kph = static_cast<size_t>(max(kpage, 0)) * p.g.kv_heads + h;
+        const size_t vph = static_cast<size_t>(max(vpage, 0)) * p.g.kv_heads + h;
+        const int koff = kblk & (P - 1), voff = vblk & (P - 1);
+        const uint8_t* kp = p.g.kcodes + (kph * P + koff + 2 * (g & 1)) * D + 16 * t;
+        const uint8_t* ksp = p.g.kscale + kph * P + koff + 2 * (g & 1);
+        const uint8_t* vp = p.g.vcodes + (vph * D + g) * P + voff;
+
+        // S: column 2t + b of n tile (i, ab) is token 16 t + 4 i + ab + 2 b, so
+        // the lane's K row for it is token 16 (g >> 1) + 4 i + ab + 2 (g & 1)
+        float sc[8][4];
+        uint4 kw[8][CH];
+        uint32_t ks[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int row = 4 * (n >> 1) + (n & 1);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) kw[n][c] = ldg_nc_na_v4(kp + row * D + 64 * c);
+            ks[n] = __ldg(ksp + row);
+        }
+        const uint4 vsw = __ldg(reinterpret_cast<const uint4*>(p.g.vscale + vph * P + voff));
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const uint32_t f = kpage >= 0 ? scale_factor(ks[n]) : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const uint32_t w[4] = {kw[n][c].x, kw[n][c].y, kw[n][c].z, kw[n][c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_bf16(sc[n], qa[c * 4 + i], bf2_mul(codes02(w[i]), f), bf2_mul(codes13(w[i]), f));
+            }
+        }
+        // V pieces on their way while the softmax runs
+        uint4 vw[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) vw[n] = ldg_nc_na_v4(vp + static_cast<size_t>(8 * n) * P);
+
+        // softmax: rows g (i = 0) and g + 8 (i = 1)
+        const int room = min(min(limit[0], limit[1]), j1) - jc;
+        const bool full = __all_sync(0xffffffffu, room >= kChunk);
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i >> 1, b = i & 1;
+                const int j = jc + 16 * t + 4 * (n >> 1) + (n & 1) + 2 * b;
+                float x = sc[n][i] * p.sm_log2;
+                if (!full && (j >= limit[r] || j >= j1)) x = -INFINITY;
+                sc[n][i] = x;
+                mx[r] = fmaxf(mx[r], x);
+            }
+        float alpha[2], base[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            const float m_new = fmaxf(m_run[r], mx[r]);
+            base[r] = m_new == -INFINITY ? 0.f : m_new;
+            alpha[r] = ex2(m_run[r] - base[r]);  // 0 while nothing was seen
+            m_run[r] = m_new;
+        }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sc[n][i] = ex2(sc[n][i] - base[i >> 1]);
+                sum[i >> 1] += sc[n][i];
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) l_run[r] = l_run[r] * alpha[r] + sum[r];
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                o[n][0] *= alpha[0];
+                o[n][1] *= alpha[0];
+                o[n][2] *= alpha[1];
+                o[n][3] *= alpha[1];
+            }
+        }
+        // the V pieces' 16 tokens: factors by word, 0 for tokens the sequence does not have
+        uint32_t vf[8];
+        const uint32_t vs[4] = {vsw.x, vsw.y, vsw.z, vsw.w};
+        // A token whose V is not a number must reach the rows that see it and
+        // no other, so that is moved from V (0 x NaN would reach every row)
+        // into the weights; they are of the same 16 tokens as the V pieces.
+        uint32_t nans = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) nans |= __vcmpgtu4(vs[i], 0x86868686u);
+        if (__any_sync(0xffffffffu, nans != 0)) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int byte = (n & 1) + 2 * (i & 1);
+                    const int j = jc + 16 * t + 4 * (n >> 1) + byte;
+                    if (((vs[n >> 1] >> (8 * byte)) & 0xffu) > 134u && j < limit[i >> 1] && j < j1)
+                        sc[n][i] = __uint_as_float(0x7fc00000u);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t good = vs[i] & ~__vcmpgtu4(vs[i], 0x86868686u);
+            vf[2 * i] = factors02(good);
+            vf[2 * i + 1] = factors13(good);
+            if (!full || !vok) {
+                const int left = vok ? q.kv - (vblk + 4 * i) : 0;  // tokens of the word that exist
+                vf[2 * i] &= (left > 0 ? 0xffffu : 0u) | (left > 2 ? 0xffff0000u : 0u);
+                vf[2 * i + 1] &= (left > 1 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // products over tokens 16 t + 4 i + {0, 2} (n tile (i, 0)) and + {1, 3} (n tile (i, 1))
+            const uint32_t pa[4] = {pack_bf16(sc[2 * i][0], sc[2 * i][1]), pack_bf16(sc[2 * i][2], sc[2 * i][3]),
+                                    pack_bf16(sc[2 * i + 1][0], sc[2 * i + 1][1]),
+                                    pack_bf16(sc[2 * i + 1][2], sc[2 * i + 1][3])};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint32_t w = i == 0 ? vw[n].x : i == 1 ? vw[n].y : i == 2 ? vw[n].z : vw[n].w;
+                mma_bf16(o[n], pa, bf2_mul(codes02(w), vf[2 * i]), bf2_mul(codes13(w), vf[2 * i + 1]));
+            }
+        }
+    }
+
+    // ---- join the warps
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
+        l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+        if (t == 0) {
+            sm[warp][g + 8 * r] = m_run[r];
+            sl[warp][g + 8 * r] = l_run[r];
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<float2*>(&so[warp][g + 8 * r][8 * n + 2 * t]) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+    }
+    __syncthreads();
+    const int rows_here = min(kRowTile, rows - tile * kRowTile);
+    const int slot = (s * p.row_tiles + tile) * p.g.kv_heads + h;
+    float* part = p.part + static_cast<size_t>(slot) * p.splits * part_floats<D>();
+    auto store_out = [&](int r, int d, float4 v, float M, float L) {
+        const int rr = tile * kRowTile + r, tok = rr / p.group, head = h * p.group + rr - tok * p.group;
+        const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // a sum that is not a number stays one
+        *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q.q0 + tok) * p.out_stride +
+                                  static_cast<int64_t>(head) * D + d) =
+            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+        if (d == 0 && p.lse != nullptr)
+            p.lse[static_cast<int64_t>(q.q0 + tok) * p.heads + head] =
+                L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    };
+    for (int i = tid; i < rows_here * (D / 4); i += kRowsThreads) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm[w][r]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowsWarps; ++w) {
+            const float f = join_weight(sm[w][r], M);
+            const float4 v = *reinterpret_cast<const float4*>(&so[w][r][d]);
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+            L += f * sl[w][r];
+        }
+        if (nsplit == 1) {
+            store_out(r, d, acc, M, L);
+        } else {
+            float* mine = part + static_cast<size_t>(split) * part_floats<D>();
+            *reinterpret_cast<float4*>(mine + r * D + d) = acc;
+            if (d == 0) {
+                mine[kRowTile * D + r] = M;
+                mine[kRowTile * D + kRowTile + r] = L;
+            }
+        }
+    }
+    if (nsplit == 1) return;
+    // ---- join the splits: the last block to arrive
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) last = atomicAdd(p.counters + slot, 1) == nsplit - 1;
+    __syncthreads();
+    if (!last) return;
+    if (tid == 0) p.counters[slot] = 0;
+    __threadfence();
+    for (int i = tid; i < rows_here * (D / 4); i += kRowsThreads) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        float M = -INFINITY;
+        for (int k = 0; k < nsplit; ++k)
+            M = fmaxf(M, __ldcg(part + static_cast<size_t>(k) * part_floats<D>() + kRowTile * D + r));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
+        for (int k = 0; k < nsplit; ++k) {
+            const float* b = part + static_cast<size_t>(k) * part_floats<D>();
+            const float f = join_weight(__ldcg(b + kRowTile * D + r), M);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(b + r * D + d));
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+            L += f * __ldcg(b + kRowTile * D + kRowTile + r);
+        }
+        store_out(r, d, acc, M, L);
+    }
+}
+
+template <int D>
+cudaError_t launch_rows(PagedAttnParams& p, size_t part_floats_max, int max_counters, cudaStream_t s) {
+    const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
+    p.row_tiles = static_cast<int>((rows + kRowTile - 1) / kRowTile);
+    const int64_t slots = static_cast<int64_t>(p.g.seqs) * p.row_tiles * p.g.kv_heads;
+    if (static_cast<int64_t>(p.row_tiles) * p.g.kv_heads > 65535) return cudaErrorInvalidValue;
+    // Splits: enough blocks for several on each of the 152 SMs, at least one
+    // step of every warp each, at most 32 (the last block reads them all), and
+    // as many as the workspace holds.
+    const int step = kRowsWarps * kChunk;
+    int64_t want = (152 * 12 + slots - 1) / slots;
+    want = std::min<int64_t>(want, 32);
+    want = std::min<int64_t>(want, (p.g.max_kv + step - 1) / step);
+    want = std::min<int64_t>(want, static_cast<int64_t>(part_floats_max / (slots * part_floats<D>())));
+    if (slots > max_counters || want < 1) want = 1;
+    const int per = static_cast<int>((p.g.max_kv + want - 1) / want);
+    p.split_tokens = std::max(step, (per + step - 1) / step * step);
+    p.splits = std::max(1, (p.g.max_kv + p.split_tokens - 1) / p.split_tokens);
+    dim3 grid(p.splits, p.row_tiles * p.g.kv_heads, p.g.seqs);
+    paged_rows_kernel<D><<<grid, kRowsThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attention(PagedAttnParams& p, int D, size_t part_floats_max, int max_counters,
+                                   cudaStream_t s) {
+    return D == 128 ? launch_rows<128>(p, part_floats_max, max_counters, s)
+                    : launch_rows<64>(p, part_floats_max, max_counters, s);
+}
+
+}  // namespace rc

@@ -354,6 +354,191 @@ int rc_ring_write_noalloc(const rc_ring_view *ring, const void *K_bf16, const vo
                           const int64_t *positions, int n, int64_t delta_total,
                           int32_t group, double rope_base, void *stream);
 
+/* ---- positions with several axes ---------------------------------------- */
+/*
+ * Rotary positions for tokens that have a place on several axes (time, height,
+ * width of a video; one axis for text).  The head_dim / 2 dimension pairs
+ * (2i, 2i + 1) are divided among the axes in order: the first sections[0] pairs
+ * turn by the token's position on axis 0, the next sections[1] by axis 1, and
+ * so on.  Pair number r of an axis with w pairs has the frequency
+ * base^(-r / w) (an axis is a rotary embedding of its own, of 2 w dims); with
+ * RC_ROPE_SHARED_FREQS pair i of the head keeps base^(-2i / head_dim) whatever
+ * its axis.  One axis with head_dim / 2 pairs is the RoPE of rc_cache_write.
+ *
+ * A plan holds each pair's axis and its frequency in turns as a 64-bit fixed
+ * point fraction, so that position * frequency mod 1 turn is exact integer
+ * arithmetic at every int32 position.  It is plain host data: fill it once,
+ * keep it by value, pass it to any number of calls.
+ */
+#define RC_ROPE_SHARED_FREQS 1u
+#define RC_ROPE_MAX_AXES 4
+
+typedef struct rc_rope_plan {
+    int head_dim;        /* 64 or 128 */
+    int axes;            /* 1 .. RC_ROPE_MAX_AXES */
+    uint64_t turns[64];  /* pair i: round(frequency / 2 pi * 2^64) */
+    uint8_t axis[64];    /* pair i: its axis */
+} rc_rope_plan;
+
+/*
+ * Fill *plan.  Host only.  Errors: RC_ERR_ARG for a NULL pointer, axes outside
+ * 1 .. 4, a section < 0, sections that do not add up to head_dim / 2, base
+ * not in (1, 1e9], unknown flags; RC_ERR_UNSUPPORTED for head_dim other than 64 or 128.
+ */
+int rc_rope_plan_init(rc_rope_plan *plan, int head_dim, int axes, const int *sections, double base,
+                      unsigned flags);
+
+#define RC_BF16 0
+#define RC_F32 1
+
+/*
+ * out[t][h] = x[t][h] turned at token t's positions (inverse = 0), or turned
+ * back (inverse = 1: also the gradient of the turn, dx from dout).  x, out:
+ * device [n][heads][head_dim] of dtype RC_BF16 or RC_F32, tokens x_stride /
+ * out_stride elements apart (>= heads * head_dim, a multiple of 16 bytes), so
+ * a slice of a fused projection's rows can be passed.  out may be x (the same
+ * address and stride); other overlaps are not supported.  positions: device
+ * int32 [axes][n], axes pos_stride elements apart (>= n).  The arithmetic is
+ * fp32, rounded once to dtype.  n = 0 does nothing.
+ * Errors: RC_ERR_ARG (NULL or unaligned pointers, n < 0, heads < 1, a stride
+ * too small or unaligned, a plan that rc_rope_plan_init did not fill).
+ */
+int rc_rope_axes(const rc_rope_plan *plan, const void *x, int64_t x_stride, void *out, int64_t out_stride,
+                 int dtype, int64_t n, int heads, const int32_t *positions, int64_t pos_stride, int inverse,
+                 void *stream);
+
+/* ---- the paged cache ------------------------------------------------------ */
+/*
+ * One layer's FP8 cache for many sequences, in pages the CALLER owns (as with
+ * rc_ring_write_noalloc, nothing here allocates): any page can serve any
+ * sequence, and sequences may share pages they only read.
+ *
+ * Pages (P = page_tokens: 16, 32, 64 or 128), device memory, 16-byte aligned:
+ *   kcodes [pages][kv_heads][P][head_dim]  E4M3 codes
+ *   vcodes [pages][kv_heads][head_dim][P]  E4M3 codes (V transposed)
+ *   kscale, vscale [pages][kv_heads][P]    E8M0: byte b stands for 2^(b - 127)
+ * Each token and head has one scale for K and one for V: the smallest power of
+ * two s with max |x| <= 448 s (s = 1 for a row of zeros; s between 2^-124 and
+ * 2^7, so magnitudes over 57,344 saturate).  Code times scale is then an exact
+ * bf16 number.  A row that holds an infinity or a NaN gets scale byte 255 and
+ * zero codes, which read as NaN.  Scale bytes 135 .. 254 are not produced and
+ * read as infinity.
+ *
+ * Metadata of a call (rc_paged_batch), device int32, read when the kernels run,
+ * so a captured graph follows the values that are there at each replay:
+ *   page_table [seqs][table_pages]  entry i of a row: the page of the
+ *       sequence's tokens [i P, i P + P); entries past its length are not read
+ *   kv_len [seqs]   tokens of the sequence in the cache, its new ones included
+ *   q_start [seqs + 1]  sequence s owns rows q_start[s] .. q_start[s + 1] - 1
+ *       of the token-major tensors; its n new tokens are the last n of its
+ *       kv_len.  Rows outside every sequence are not touched.
+ * max_new and max_kv (host) bound every sequence's n and kv_len; tokens (host) is the
+ * row count of the tensors.  Metadata out of these bounds (or a page id that
+ * is not one of the pool's) is found on the device: the sequence (or page) is
+ * left out, nothing is read or written out of bounds, and rc_paged_status
+ * reports RC_ERR_ARG; that call's results are not valid.
+ *
+ * workspace: device memory of RC_PAGED_WORKSPACE_BYTES, 256-byte aligned,
+ * zeroed once by the caller before its first use.  It holds the status word
+ * and the partial results of split calls; each call leaves it ready for the
+ * next.  Calls that share a workspace (captured graphs included) must not run
+ * at the same time: issue them on one stream, or give each stream its own.
+ * Every call only launches kernels on `stream`, on the device that is current
+ * (which must be the stream's and the pointers'), and can be captured into a
+ * graph once it has been called directly, and a graph replayed any number of
+ * times.
+ */
+#define RC_PAGED_WORKSPACE_BYTES ((size_t)64 << 20)
+
+typedef struct rc_paged_view {
+    uint8_t *kcodes;
+    uint8_t *vcodes;
+    uint8_t *kscale;
+    uint8_t *vscale;
+    void *workspace;
+    int pages;       /* >= 1 */
+    int kv_heads;    /* 1 .. 1024 */
+    int head_dim;    /* 64 or 128 */
+    int page_tokens; /* 16, 32, 64 or 128 */
+} rc_paged_view;
+
+typedef struct rc_paged_batch {
+    const int32_t *page_table;
+    const int32_t *kv_len;
+    const int32_t *q_start; /* not read by rc_paged_evict */
+    int seqs;               /* 1 .. 65535 */
+    int table_pages;        /* row length of page_table */
+    int tokens;             /* rows of K, V, Q, out (>= 0) */
+    int max_new;            /* >= 0 */
+    int max_kv;             /* 0 .. table_pages * page_tokens, at most 2^24 */
+} rc_paged_batch;
+
+/*
+ * Write each sequence's new tokens into its pages: K turned at the tokens'
+ * positions (as rc_rope_axes, unrounded), K and V quantised as above.  K, V:
+ * device bf16 [tokens][kv_heads][head_dim], tokens k_stride / v_stride elements
+ * apart; positions: device int32 [axes][tokens], axes pos_stride apart.  The
+ * pages must already be in page_table.  Two sequences must not write to one page.
+ * A sequence whose n is larger than its kv_len is left out (RC_ERR_ARG later).
+ */
+int rc_paged_write(const rc_paged_view *view, const rc_paged_batch *batch, const void *K_bf16, int64_t k_stride,
+                   const void *V_bf16, int64_t v_stride, const int32_t *positions, int64_t pos_stride,
+                   const rc_rope_plan *plan, void *stream);
+
+/*
+ * out = softmax(q . k / sqrt(head_dim)) v over the sequence's cached tokens, for
+ * each of its new tokens and each of `heads` query heads; query head g reads
+ * KV head g / (heads / kv_heads).  With causal != 0 new token i sees tokens
+ * 0 .. kv_len - n + i, else all kv_len.  Q is bf16, already turned
+ * (rc_rope_axes), [tokens][heads][head_dim]; out is bf16 of the same layout;
+ * lse (may be NULL) is fp32 [tokens][heads], the natural logarithm of the sum
+ * of exp(scores).  A query that sees nothing gets zeros and lse = -infinity.
+ * heads must be a multiple of kv_heads.
+ */
+int rc_paged_attend(const rc_paged_view *view, const rc_paged_batch *batch, const void *Q_bf16, int64_t q_stride,
+                    int heads, void *out_bf16, int64_t out_stride, float *lse, int causal, void *stream);
+
+/*
+ * The attention weight that each cached token received from the new tokens'
+ * queries: out[s][h][j] = scores[s][h][j] + sum over the queries of KV head h
+ * that see token j of exp(q . k_j / sqrt(head_dim) - lse).  lse as
+ * rc_paged_attend gives it; a row whose lse is -infinity adds nothing.
+ * scores, out: device fp32 [seqs][kv_heads][score_stride], score_stride >=
+ * max_kv; out may be scores.  Entries kv_len .. max_kv - 1 are copied
+ * unchanged, entries past max_kv not touched.  Every entry is summed in one fixed order: the
+ * same inputs give the same bits.
+ */
+int rc_paged_accumulate(const rc_paged_view *view, const rc_paged_batch *batch, const void *Q_bf16, int64_t q_stride,
+                        int heads, const float *lse, const float *scores, float *out, int64_t score_stride,
+                        int causal, void *stream);
+
+/*
+ * Cut each sequence, per KV head, to at most `keep` tokens: its last `recent`
+ * tokens and, of the others, those with the largest scores (equal scores: the
+ * lower index first; -0 equals +0; a NaN counts as the largest).  The kept tokens' codes and scales
+ * are copied, in order, to the pages of dst_table [seqs][dst_pages] (token i of
+ * the result in page i / P, place i % P); a sequence of at most `keep` tokens
+ * is copied whole.  The source pages are only read, so they may be shared;
+ * no destination page may be a source page or appear twice.
+ *   kept [seqs][kv_heads][keep]: the kept tokens' old indices, ascending; -1 past the end
+ *   kv_len_out [seqs]: min(kv_len, keep)
+ *   scores_out (may be NULL) [seqs][kv_heads][keep]: the kept tokens' scores; 0 past the end
+ * Errors: RC_ERR_ARG also for keep < 1, recent outside 0 .. keep, or
+ * min(keep, max_kv) tokens that do not fit dst_pages pages.
+ */
+int rc_paged_evict(const rc_paged_view *view, const rc_paged_batch *batch, const float *scores, int64_t score_stride,
+                   int keep, int recent, const int32_t *dst_table, int dst_pages, int32_t *kept, int32_t *kv_len_out,
+                   float *scores_out, void *stream);
+
+/* Synchronise `stream` and report what the calls on this workspace found:
+   RC_OK, RC_ERR_ARG (bad metadata, see above), RC_ERR_TIMEOUT (a kernel gave
+   up a bounded wait) or RC_ERR_CUDA.  The status word is cleared. */
+int rc_paged_status(const rc_paged_view *view, void *stream);
+
+/* Test support: the longest one wait of a later paged call may take, in ns
+   (default 2 s; process-wide; as rc_cache_set_wait_limit). */
+int rc_paged_set_wait_limit(uint64_t ns);
+
 /* Number of occupied slots of `layer`, or a negative status. */
 int rc_cache_occupancy(const rc_cache *h, int layer);
 
