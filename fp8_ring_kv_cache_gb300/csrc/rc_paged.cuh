@@ -197,6 +197,7 @@ struct RopeAxesParams {
 cudaError_t launch_rope_axes(const RopeAxesParams& p, int D, int dtype, cudaStream_t s);
 cudaError_t launch_paged_write(const PagedWriteParams& p, int D, cudaStream_t s);
 cudaError_t launch_paged_attention(PagedAttnParams& p, int D, size_t part_floats, int max_counters, cudaStream_t s);
+cudaError_t launch_paged_tc(PagedAttnParams& p, int D, size_t part_floats, cudaStream_t s);
 cudaError_t launch_paged_scores(const PagedScoreParams& p, int D, cudaStream_t s);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int D, cudaStream_t s);
 

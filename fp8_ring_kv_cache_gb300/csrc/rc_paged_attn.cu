@@ -345,6 +345,9 @@ cudaError_t launch_rows(PagedAttnParams& p, size_t part_floats_max, int max_coun
 
 cudaError_t launch_paged_attention(PagedAttnParams& p, int D, size_t part_floats_max, int max_counters,
                                    cudaStream_t s) {
+    // up to one row tile per KV head the reading of the codes is what counts;
+    // with more rows each tile would read them again
+    if (static_cast<int64_t>(p.g.max_new) * p.group > kRowTile) return launch_paged_tc(p, D, part_floats_max, s);
     return D == 128 ? launch_rows<128>(p, part_floats_max, max_counters, s)
                     : launch_rows<64>(p, part_floats_max, max_counters, s);
 }

@@ -1,0 +1,663 @@
+// rc_paged_tc.cu -- attention of many query rows over the pages, on the
+// tensor cores (tcgen05).
+//
+// A block has up to 256 query rows of one KV head (a sequence's new tokens x
+// the query heads that share it), 16 warps:
+//   warp 0        issues the matrix products (one lane) and owns TMEM
+//   warps 4..7    softmax group 0, warps 8..11 softmax group 1 (a row a thread)
+//   warps 12..15  converters: read the codes of 128 cached tokens from their
+//                 pages (half a tile ahead, in registers), make them bf16 and
+//                 write the K and V tiles in the swizzled layout of a K-major
+//                 operand, two buffers each
+// Scales are powers of two, so the bf16 tiles are exact, S = Q K^T needs no
+// factor per column, and both products run at the bf16 rate:
+//   S_i = Q_i K_j^T into TMEM; softmax of a row by its thread: P to bf16, over
+//   S in TMEM; O_i += P_i V_j with P read from TMEM.
+// The work is a chain of units: unit u is (KV tile, group u & 1).  With more
+// than 128 rows group i has rows [128 i, 128 i + 128) and both groups take
+// each KV tile; with fewer both groups have the same rows and take the KV tiles
+// in turn, and their results are joined at the end.  Either way the products of
+// one group run while the other is in softmax.  After P of unit u: O += P V of
+// unit u, then S of unit u + 2, which overwrites P's place.
+// A code word gives the pairs (0, 2) and (1, 3) of its four values cheapest:
+// that order is kept along the summed dims (Q is stored in it) and along the
+// cached tokens (P is packed in it).
+#include <algorithm>
+
+#include "rc_paged.cuh"
+
+namespace rc {
+
+namespace {
+
+constexpr int kTcThreads = 512;
+constexpr int kTileM = 128, kTileN = 128;
+constexpr int kRowsTc = 2 * kTileM;
+constexpr int kWgSoftmax0 = 1, kWgConvert = 3;
+constexpr uint32_t kTcTmem = 512;
+
+enum : int {
+    T_K_FULL = 0,   // [2] the converters wrote the K tile
+    T_K_EMPTY = 2,  // [2] its products have finished
+    T_V_FULL = 4,
+    T_V_EMPTY = 6,
+    T_S_FULL = 8,  // [2] scores of group i in TMEM
+    T_O_DONE = 10,
+    T_DRAIN = 11,
+    T_COUNT = 12
+};
+// Named barriers: group i with the product warp (P in TMEM; the group's
+// checker lane has seen V of this unit and K of unit u + 2), and the two
+// groups at the end.
+constexpr int kNbUnit = 1;  // [2]
+constexpr int kNbJoin = 3;
+constexpr int kNbUnitThreads = 128 + 32;
+
+template <int D>
+struct TcLayout {
+    static constexpr uint32_t kTile = kTileN * D * 2;  // bytes of a bf16 tile (Q_i, K or V)
+    static constexpr uint32_t kQ = 0;                  // [2][D/64][128][128 B]
+    static constexpr uint32_t kK = 2 * kTile;          // [2 buffers]
+    static constexpr uint32_t kV = kK + 2 * kTile;     // [2 buffers][2 halves][D][128 B]
+    static constexpr uint32_t kScale = kV + 2 * kTile; // V scale bytes of the last four KV tiles
+    static constexpr uint32_t kBar = kScale + 4 * kTileN;
+    static constexpr uint32_t kMisc = kBar + 8 * T_COUNT;  // [0] tmem, [1] abort, [4..7] KV tile holds a V that is not a number
+    static constexpr uint32_t kTotal = kMisc + 64;
+    static constexpr uint32_t kAlloc = kTotal + 1024;
+};
+
+// A split's result for a row tile: O [256][D] (joined weights, not divided),
+// then max and sum [256] each.
+template <int D>
+constexpr int tc_part_floats() {
+    return kRowsTc * D + 2 * kRowsTc;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Cached tokens that the rows of a tile see, and how they are split.
+struct TileWork {
+    int rows;    // rows of the sequence's KV head
+    int seen;    // tokens that the tile's last row sees
+    int nsplit;  // splits with work (at least 1)
+};
+__device__ __forceinline__ TileWork tile_work(const PagedAttnParams& p, const Seq& q, int tile) {
+    TileWork w;
+    w.rows = q.n * p.group;
+    const int last_new = min(q.n - 1, (tile * kRowsTc + kRowsTc - 1) / p.group);
+    w.seen = p.causal ? max(0, q.kv - q.n + last_new + 1) : q.kv;
+    w.nsplit = max(1, (w.seen + p.split_tokens - 1) / p.split_tokens);
+    return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams p) {
+    using Lay = TcLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(smem + Lay::kMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+
+    // the last tiles, which see the most when causal, come first
+    int b = blockIdx.x;
+    const int h = b % p.g.kv_heads;
+    b /= p.g.kv_heads;
+    const int s = b % p.g.seqs, tile = p.row_tiles - 1 - b / p.g.seqs, split = blockIdx.y;
+    const Seq q = load_seq(p.g, s);
+    const TileWork tw = tile_work(p, q, tile);
+    const int row0 = tile * kRowsTc;
+    if (row0 >= tw.rows || split >= tw.nsplit) return;
+    const int j0 = split * p.split_tokens, j1 = min(tw.seen, j0 + p.split_tokens);
+    const int rows_here = min(kRowsTc, tw.rows - row0);
+    const bool two = rows_here > kTileM;              // two row tiles; else one, KV tiles in turn
+    const int T = (j1 - j0 + kTileN - 1) / kTileN;    // KV tiles
+    const int U = two ? 2 * T : T;                    // units
+    AbortState ab{reinterpret_cast<volatile uint32_t*>(&misc[1]), p.g.status, p.wait_ns};
+    auto tile_of = [&](int u) { return two ? u >> 1 : u; };
+
+    // ------------------------------------------------------------ set-up
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[T_K_FULL + i], 4);
+            mbar_init(&bars[T_K_EMPTY + i], 1);
+            mbar_init(&bars[T_V_FULL + i], 4);
+            mbar_init(&bars[T_V_EMPTY + i], 1);
+            mbar_init(&bars[T_S_FULL + i], 1);
+        }
+        mbar_init(&bars[T_O_DONE], 1);
+        mbar_init(&bars[T_DRAIN], 1);
+        misc[1] = 0u;
+        for (int i = 4; i < 8; ++i) misc[i] = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&misc[0], kTcTmem);
+        tmem_relinquish();
+    }
+    // Q rows, 8 dims a piece, in the order (0, 2), (1, 3) of each four
+    {
+        constexpr int kPieces = D / 8;
+        const int total = (two ? kRowsTc : kTileM) * kPieces;
+        for (int u = tid; u < total; u += kTcThreads) {
+            const int r = u / kPieces, c = u % kPieces;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < rows_here) {
+                const int rr = row0 + r, tok = rr / p.group, head = h * p.group + rr - tok * p.group;
+                w = ldg_nc_na_v4(p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D +
+                                 8 * c);
+            }
+            *reinterpret_cast<uint4*>(smem + Lay::kQ + (r >> 7) * Lay::kTile + bktile_off(r & 127, 8 * c)) =
+                make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632),
+                           __byte_perm(w.z, w.w, 0x5410), __byte_perm(w.z, w.w, 0x7632));
+        }
+        fence_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+
+    if (wg == 0) {
+        regs_dec<56>();
+        if (warp == 0 && U > 0) {
+            // -------------------------------------------------------- products
+            // Operand descriptors differ from a base only in the start address
+            // (16-byte units, no carry below 256 KB), so one add moves them.
+            const uint32_t idesc_qk = instr_desc(kFmtBF16, kFmtBF16, 128, 128);
+            const uint32_t idesc_pv = instr_desc(kFmtBF16, kFmtBF16, 128, D);
+            const uint64_t dq0 = smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2);
+            const uint64_t dk0 = smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2);
+            const uint64_t dv0 = smem_desc(smem_u32(smem + Lay::kV), 16, 1024, 2);
+            auto issue_qk = [&](int u) {
+                const int i = u & 1, j = tile_of(u);
+                const uint64_t qa = dq0 + ((two && i) ? Lay::kTile >> 4 : 0u);
+                const uint64_t kb = dk0 + ((j & 1) ? Lay::kTile >> 4 : 0u);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_f16_ss(tmem + 128u * i, qa + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                               kb + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), idesc_qk, k != 0);
+                mma_commit(&bars[T_S_FULL + i]);
+                if (!two || i == 1) mma_commit(&bars[T_K_EMPTY + (j & 1)]);
+            };
+            auto issue_pv = [&](int u) {
+                const int i = u & 1, j = tile_of(u);
+                const uint64_t vb = dv0 + ((j & 1) ? Lay::kTile >> 4 : 0u);
+#pragma unroll
+                for (int k = 0; k < kTileN / 16; ++k)
+                    mma_f16_ts(tmem + 256u + static_cast<uint32_t>(D) * i, tmem + 128u * i + 8 * k,
+                               vb + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), idesc_pv, (u > 1 || k > 0) ? 1u : 0u);
+                if (!two || i == 1) mma_commit(&bars[T_V_EMPTY + (j & 1)]);
+            };
+            const bool leader = lane == 0;
+            bool ok = true;
+            for (int u = 0; u < 2 && u < U; ++u) {
+                const int j = tile_of(u);
+                bool r = true;
+                if (leader && ok) r = mbar_wait(&bars[T_K_FULL + (j & 1)], 0, ab, kDevTimeoutMma);
+                ok = ok && __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+                if (ok && leader) {
+                    tc_fence_after();
+                    issue_qk(u);
+                }
+            }
+            // every unit passes its rendezvous, also after an abort, so no partner is left waiting
+            for (int u = 0; u < U; ++u) {
+                ok = named_barrier_and(kNbUnit + (u & 1), kNbUnitThreads, ok);
+                if (ok && leader) {
+                    tc_fence_after();
+                    issue_pv(u);
+                    if (u + 2 < U) issue_qk(u + 2);
+                    if (u + 1 == U) mma_commit(&bars[T_O_DONE]);
+                }
+            }
+            if (leader) {
+                // every product has finished before the tensor memory is released
+                mma_commit(&bars[T_DRAIN]);
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(&bars[T_DRAIN], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+                }
+            }
+        }
+    } else if (wg != kWgConvert) {
+        // ------------------------------------------------------------ softmax
+        regs_inc<184>();
+        const int i = wg - kWgSoftmax0;
+        const int quad = warp & 3, r = quad * 32 + lane;  // TMEM lane quadrant; row within the group's tile
+        const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t s_tm = tmem + lane_off + 128u * i;
+        const uint32_t o_tm = tmem + lane_off + 256u + static_cast<uint32_t>(D) * i;
+        const int rr = row0 + (two ? kTileM * i : 0) + r;  // row of the KV head
+        const bool live = rr < tw.rows;
+        const int tok = live ? rr / p.group : 0, head = h * p.group + (live ? rr - tok * p.group : 0);
+        // tokens the row sees, counted from j0; rows past the end see all (nothing of theirs is stored)
+        const int limit = (!live || !p.causal ? j1 : min(j1, max(0, q.kv - q.n + tok + 1))) - j0;
+        const float a = p.sm_log2;
+        const float2 a2 = make_float2(a, a);
+        float m_run = -INFINITY, l_run = 0.f;
+        bool poison = false;  // a token whose V is not a number is seen
+        bool ok = true;
+        const bool checker = quad == 0 && lane == 0;
+
+        auto unit = [&](int u) -> bool {
+            const int j = tile_of(u);
+            // V of this unit and K of unit u + 2, tested now and looked at after the softmax
+            const int jk = tile_of(u + 2);
+            const bool want_k = u + 2 < U;
+            bool vk = true;
+            if (checker) {
+                vk = mbar_test(&bars[T_V_FULL + (j & 1)], (j >> 1) & 1);
+                if (want_k) vk = mbar_test(&bars[T_K_FULL + (jk & 1)], (jk >> 1) & 1) && vk;
+            }
+            if (!warp_wait(&bars[T_S_FULL + i], (u >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
+            tc_fence_after();
+            const int room = limit - j * kTileN;  // columns the row sees
+            uint32_t v0[32], v1[32], v2[32], v3[32];
+            tmem_ld32_async(s_tm, v0);
+            tmem_ld32_async(s_tm + 32, v1);
+            tmem_ld32_async(s_tm + 64, v2);
+            tmem_ld32_async(s_tm + 96, v3);
+            tmem_wait_ld_dep(v0);
+            reg_fence(v1);
+            reg_fence(v2);
+            reg_fence(v3);
+            if (!__all_sync(0xffffffffu, room >= kTileN)) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    if (k >= room) v0[k] = 0xff800000u;
+                    if (k + 32 >= room) v1[k] = 0xff800000u;
+                    if (k + 64 >= room) v2[k] = 0xff800000u;
+                    if (k + 96 >= room) v3[k] = 0xff800000u;
+                }
+            }
+            auto chunk_max = [](const uint32_t (&v)[32]) {
+                float t[11];
+#pragma unroll
+                for (int k = 0; k < 10; ++k)
+                    t[k] = max3(__uint_as_float(v[3 * k]), __uint_as_float(v[3 * k + 1]), __uint_as_float(v[3 * k + 2]));
+                t[10] = fmaxf(__uint_as_float(v[30]), __uint_as_float(v[31]));
+                const float u0 = max3(t[0], t[1], t[2]), u1 = max3(t[3], t[4], t[5]);
+                const float u2 = max3(t[6], t[7], t[8]), u3 = max3(t[9], t[10], u0);
+                return max3(u1, u2, u3);
+            };
+            const float m_tile = fmaxf(fmaxf(chunk_max(v0), chunk_max(v1)), fmaxf(chunk_max(v2), chunk_max(v3))) * a;
+            // the running max moves only when a tile raises it by more than
+            // 2^8 of weight: bf16 and fp32 hold the larger weights as well
+            const bool bump = (m_run == -INFINITY) || (m_tile > m_run + 8.f);
+            const float m_new = bump ? fmaxf(m_run, m_tile) : m_run;
+            const float base = (m_new == -INFINITY) ? 0.f : m_new;
+            const float alpha = bump ? ex2(m_run - base) : 1.f;
+            const float2 n2 = make_float2(-base, -base);
+            float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
+            auto p_chunk = [&](const uint32_t (&v)[32], uint32_t* pk) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float2 x0 = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), a2, n2);
+                    const float2 x1 = fma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), a2, n2);
+                    const float2 q0 = make_float2(ex2(x0.x), ex2(x0.y));
+                    const float2 q1 = make_float2(ex2(x1.x), ex2(x1.y));
+                    ls0 = add2(ls0, q0);
+                    ls1 = add2(ls1, q1);
+                    pk[k / 2] = pack_bf16(q0.x, q1.x);      // tokens 0, 2
+                    pk[k / 2 + 1] = pack_bf16(q0.y, q1.y);  // tokens 1, 3
+                }
+            };
+            uint32_t pa[32], pb[32];
+            p_chunk(v0, pa);
+            p_chunk(v1, pa + 16);
+            tmem_st32(s_tm, pa);
+            p_chunk(v2, pb);
+            p_chunk(v3, pb + 16);
+            tmem_st32(s_tm + 32, pb);
+            if (misc[4 + (j & 3)] != 0u) {
+                const uint8_t* vs = smem + Lay::kScale + (j & 3) * kTileN;
+                for (int k = 0; k < kTileN; ++k) poison |= vs[k] > 134 && k < room;
+            }
+            tmem_st_wait();
+            // rescale the running output when the max moved (the product of
+            // unit u - 2 has finished: S of this unit came after it)
+            if (__any_sync(0xffffffffu, u > 1 && alpha != 1.f)) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(o_tm + 32 * c, v);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                    tmem_st32(o_tm + 32 * c, v);
+                }
+                tmem_st_wait();
+            }
+            l_run = l_run * alpha + ((ls0.x + ls0.y) + (ls1.x + ls1.y));
+            m_run = m_new;
+            if (checker && !vk) {
+                if (!mbar_wait(&bars[T_V_FULL + (j & 1)], (j >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
+                if (want_k && !mbar_wait(&bars[T_K_FULL + (jk & 1)], (jk >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
+            }
+            return true;
+        };
+        for (int u = i; u < U; u += 2) {
+            if (ok) ok = unit(u);
+            tc_fence_before();
+            __syncwarp();
+            ok = named_barrier_and(kNbUnit + i, kNbUnitThreads, ok);
+        }
+        // ------------------------------------------------------------ epilogue
+        if (ok && U > 0) ok = warp_wait(&bars[T_O_DONE], 0, ab, kDevTimeoutEpilogue);
+        tc_fence_after();
+        // With one row tile the groups' results are joined: group 1 leaves its
+        // max, sum and O in shared memory (the K and V buffers, free once every
+        // product has finished).
+        float scale = 1.f, other = 0.f;
+        const float* theirs = reinterpret_cast<const float*>(smem + Lay::kK) + quad * 32 * 36;
+        if (!two) {
+            float* ml = reinterpret_cast<float*>(smem + Lay::kV + Lay::kTile);  // [128] max, [128] sum, [128] poison
+            if (i == 1) {
+                ml[r] = m_run;
+                ml[128 + r] = l_run;
+                ml[256 + r] = poison ? 1.f : 0.f;
+                if (U > 1 && ok) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(o_tm + 32 * c, v);
+                        float* dst = reinterpret_cast<float*>(smem + Lay::kK) + c * (128 * 36) + quad * 32 * 36 + lane * 36;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<uint4*>(dst + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    }
+                }
+            }
+            ok = named_barrier_and(kNbJoin, 256, ok);
+            if (i == 0) {
+                const float m1 = ml[r], l1 = ml[128 + r];
+                const float M = fmaxf(m_run, m1);
+                scale = m_run == -INFINITY ? 0.f : ex2(m_run - M);
+                other = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+                l_run = l_run * scale + l1 * other;
+                m_run = M;
+                poison |= ml[256 + r] != 0.f;
+            }
+        }
+        if (ok && (two || i == 0)) {
+            const bool last = tw.nsplit == 1;
+            const float inv = !last ? 1.f : (l_run > 0.f || l_run != l_run) ? 1.f / l_run : 0.f;
+            const float f = poison ? __uint_as_float(0x7fc00000u) : scale * inv;
+            const float g = other * inv;
+            const int slot = (s * p.row_tiles + tile) * p.g.kv_heads + h;
+            float* part = p.part + (static_cast<size_t>(slot) * p.splits + split) * tc_part_floats<D>();
+            const int tr = (two ? kTileM * i : 0) + r;  // row of the 256
+            if (live) {
+                if (!last) {
+                    part[kRowsTc * D + tr] = m_run;
+                    part[kRowsTc * D + kRowsTc + tr] = l_run;
+                } else if (p.lse != nullptr) {
+                    p.lse[static_cast<int64_t>(q.q0 + tok) * p.heads + head] =
+                        l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
+                }
+            }
+            // Rows go out through shared memory (the Q image, which no product
+            // reads any more), so that a store instruction covers whole lines.
+            float* stage = reinterpret_cast<float*>(smem + Lay::kQ) + (i * 4 + quad) * (32 * 36);
+            const int wrow = row0 + (two ? kTileM * i : 0) + quad * 32;  // the warp's first row
+            const bool both = !two && U > 1;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                if (U > 0) tmem_ld32(o_tm + 32 * c, v);
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (U > 0)
+                        x = make_float4(__uint_as_float(v[k]) * f, __uint_as_float(v[k + 1]) * f,
+                                        __uint_as_float(v[k + 2]) * f, __uint_as_float(v[k + 3]) * f);
+                    if (both) {
+                        const float4 y = *reinterpret_cast<const float4*>(theirs + c * (128 * 36) + lane * 36 + k);
+                        x = make_float4(fmaf(y.x, g, x.x), fmaf(y.y, g, x.y), fmaf(y.z, g, x.z), fmaf(y.w, g, x.w));
+                    }
+                    *reinterpret_cast<float4*>(stage + lane * 36 + k) = x;
+                }
+                __syncwarp();
+                if (last) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int ro = 8 * k + (lane >> 2), e = 8 * (lane & 3);
+                        const int row = wrow + ro;
+                        const float4 x = *reinterpret_cast<const float4*>(stage + ro * 36 + e);
+                        const float4 y = *reinterpret_cast<const float4*>(stage + ro * 36 + e + 4);
+                        if (row < tw.rows) {
+                            const int t2 = row / p.group, h2 = h * p.group + row - t2 * p.group;
+                            *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(q.q0 + t2) * p.out_stride +
+                                                      static_cast<int64_t>(h2) * D + 32 * c + e) =
+                                make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y),
+                                           pack_bf16(y.z, y.w));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int ro = 4 * k + (lane >> 3), e = 4 * (lane & 7);
+                        if (wrow + ro < tw.rows)
+                            *reinterpret_cast<float4*>(part + static_cast<size_t>(wrow + ro - row0) * D + 32 * c + e) =
+                                *reinterpret_cast<const float4*>(stage + ro * 36 + e);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ converters
+        // Thread ct: of K, the piece of 16 dims ct % KP of the rows ct / KP +
+        // k 128 / KP; of V, the 16 tokens (ct % 8) 16 .. of the dims ct / 8 + 16 k.
+        // Lane l < 8 of each warp looks up the page of the tile's tokens 16 l ..
+        regs_dec<88>();
+        constexpr int KP = D / 16, KU = KP, VU = D / 16;  // pieces of a K row; pieces of a thread
+        const int ct = tid - kWgConvert * 128;
+        const int P = 1 << p.g.page_shift;
+        bool ok = true;
+        // page of the tile's tokens [16 (ct % 8), + 16); -1: none (bad page or behind the end)
+        auto page_at = [&](int j) {
+            const int t = j0 + j * kTileN + 16 * (ct & 7);
+            return j < T && t < q.kv ? load_page(p.g, s, t >> p.g.page_shift) : -1;
+        };
+        uint4 kr[KU], vr[VU];
+        uint32_t ks[KU];
+        uint4 vs;
+        auto fetch_k = [&](int j, int page) {
+#pragma unroll
+            for (int k = 0; k < KU; ++k) {
+                const int row = ct / KP + k * (128 / KP);
+                const int pg = __shfl_sync(0xffffffffu, page, row >> 4);
+                kr[k] = make_uint4(0, 0, 0, 0);
+                ks[k] = 0;
+                if (pg >= 0) {
+                    const size_t at = (static_cast<size_t>(pg) * p.g.kv_heads + h) * P + ((j0 + j * kTileN + row) & (P - 1));
+                    kr[k] = ldg_nc_na_v4(p.g.kcodes + at * D + 16 * (ct % KP));
+                    ks[k] = __ldg(p.g.kscale + at);
+                }
+            }
+        };
+        auto fetch_v = [&](int j, int page) {
+            const size_t ph = static_cast<size_t>(max(page, 0)) * p.g.kv_heads + h;
+            const int off = (j0 + j * kTileN + 16 * (ct & 7)) & (P - 1);
+#pragma unroll
+            for (int k = 0; k < VU; ++k) {
+                vr[k] = make_uint4(0, 0, 0, 0);
+                if (page >= 0) vr[k] = ldg_nc_na_v4(p.g.vcodes + (ph * D + (ct >> 3) + 16 * k) * P + off);
+            }
+        };
+        auto fetch_vs = [&](int j, int page) {
+            vs = make_uint4(0, 0, 0, 0);
+            if (page >= 0) {
+                const size_t ph = static_cast<size_t>(page) * p.g.kv_heads + h;
+                vs = __ldg(reinterpret_cast<const uint4*>(p.g.vscale + ph * P + ((j0 + j * kTileN + 16 * (ct & 7)) & (P - 1))));
+                // tokens behind the sequence's end: byte 0, with which any code is 0 or next to it
+                const int left = q.kv - (j0 + j * kTileN + 16 * (ct & 7));
+                if (left < 16) {
+                    uint32_t* w = &vs.x;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int n = left - 4 * k;
+                        w[k] = n <= 0 ? 0u : n < 4 ? w[k] & ((1u << (8 * n)) - 1u) : w[k];
+                    }
+                }
+            }
+        };
+        // the four values pairs of 16 codes, as bf16
+        auto put = [&](uint8_t* lo, uint8_t* hi, const uint4& w, const uint32_t (&f)[8]) {
+            *reinterpret_cast<uint4*>(lo) = make_uint4(bf2_mul(codes02(w.x), f[0]), bf2_mul(codes13(w.x), f[1]),
+                                                       bf2_mul(codes02(w.y), f[2]), bf2_mul(codes13(w.y), f[3]));
+            *reinterpret_cast<uint4*>(hi) = make_uint4(bf2_mul(codes02(w.z), f[4]), bf2_mul(codes13(w.z), f[5]),
+                                                       bf2_mul(codes02(w.w), f[6]), bf2_mul(codes13(w.w), f[7]));
+        };
+        int page = page_at(0);
+        if (T > 0) {
+            fetch_k(0, page);
+            fetch_vs(0, page);
+            fetch_v(0, page);
+        }
+        for (int j = 0; j < T; ++j) {
+            const int st = j & 1;
+            const int next = page_at(j + 1);
+            if (ok) ok = warp_wait(&bars[T_K_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
+            // V's scales: a byte over 134 is a row that is not a number; its
+            // values count as 0 here and the rows that see it are marked
+            const uint4 bad = make_uint4(__vcmpgtu4(vs.x, 0x86868686u), __vcmpgtu4(vs.y, 0x86868686u),
+                                         __vcmpgtu4(vs.z, 0x86868686u), __vcmpgtu4(vs.w, 0x86868686u));
+            const bool any = (bad.x | bad.y | bad.z | bad.w) != 0u;
+            if (ok) {
+                // slot j & 3: the softmax of tile j - 4 has read it (S of tile j - 2 came after that)
+                if (ct < 8) *reinterpret_cast<uint4*>(smem + Lay::kScale + (j & 3) * kTileN + 16 * ct) = vs;
+                const bool w_any = __any_sync(0xffffffffu, any);  // every warp holds all 8 blocks
+                if (ct == 0) misc[4 + (j & 3)] = w_any ? 1u : 0u;
+                uint8_t* dst = smem + Lay::kK + st * Lay::kTile;
+#pragma unroll
+                for (int k = 0; k < KU; ++k) {
+                    const int row = ct / KP + k * (128 / KP), dim = 16 * (ct % KP);
+                    const uint32_t f1 = scale_factor(ks[k]);
+                    const uint32_t f[8] = {f1, f1, f1, f1, f1, f1, f1, f1};
+                    put(dst + bktile_off(row, dim), dst + bktile_off(row, dim + 8), kr[k], f);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[T_K_FULL + st]);
+            }
+            if (j + 1 < T) fetch_k(j + 1, next);
+            if (ok) ok = warp_wait(&bars[T_V_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
+            if (ok) {
+                uint32_t f[8];
+                const uint32_t w[4] = {vs.x & ~bad.x, vs.y & ~bad.y, vs.z & ~bad.z, vs.w & ~bad.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[2 * k] = factors02(w[k]);
+                    f[2 * k + 1] = factors13(w[k]);
+                }
+                uint8_t* dst = smem + Lay::kV + st * Lay::kTile;
+#pragma unroll
+                for (int k = 0; k < VU; ++k) {
+                    const int d = (ct >> 3) + 16 * k, t = 16 * (ct & 7);
+                    put(dst + bvtile_off(d, t, D), dst + bvtile_off(d, t + 8, D), vr[k], f);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[T_V_FULL + st]);
+            }
+            if (j + 1 < T) {
+                fetch_vs(j + 1, next);
+                fetch_v(j + 1, next);
+            }
+        }
+    }
+
+    // ------------------------------------------------------------ teardown
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTcTmem);
+    }
+}
+
+// Joins the splits of each row, in split order: a warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) paged_tc_join_kernel(PagedAttnParams p) {
+    const int lane = threadIdx.x & 31;
+    int b = blockIdx.x;
+    const int h = b % p.g.kv_heads;
+    b /= p.g.kv_heads;
+    const int s = b % p.g.seqs, row = (b / p.g.seqs) * 8 + (threadIdx.x >> 5);
+    const Seq q = load_seq(p.g, s);
+    const int tile = row / kRowsTc;
+    const TileWork tw = tile_work(p, q, tile);
+    if (row >= tw.rows || tw.nsplit == 1) return;
+    const int tr = row - tile * kRowsTc;
+    const int slot = (s * p.row_tiles + tile) * p.g.kv_heads + h;
+    const float* part = p.part + static_cast<size_t>(slot) * p.splits * tc_part_floats<D>();
+    const float* ml = part + kRowsTc * D + tr;
+    float M = -INFINITY;
+    for (int k = 0; k < tw.nsplit; ++k) M = fmaxf(M, __ldg(ml + static_cast<size_t>(k) * tc_part_floats<D>()));
+    constexpr int V = D / 32;
+    float acc[V], L = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int k = 0; k < tw.nsplit; ++k) {
+        const float* mine = part + static_cast<size_t>(k) * tc_part_floats<D>();
+        const float m = __ldg(mine + kRowsTc * D + tr);
+        const float f = m == -INFINITY ? 0.f : ex2(m - M);
+        L += f * __ldg(mine + kRowsTc * D + kRowsTc + tr);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += f * __ldg(mine + static_cast<size_t>(tr) * D + V * lane + i);
+    }
+    const float inv = (L > 0.f || L != L) ? 1.f / L : 0.f;
+    const int tok = row / p.group, head = h * p.group + row - tok * p.group;
+    __nv_bfloat16* out = p.out + static_cast<int64_t>(q.q0 + tok) * p.out_stride + static_cast<int64_t>(head) * D + V * lane;
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+        *reinterpret_cast<uint32_t*>(out + i) = pack_bf16(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[static_cast<int64_t>(q.q0 + tok) * p.heads + head] =
+            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+template <int D>
+cudaError_t launch_d(PagedAttnParams& p, size_t part_floats_max, cudaStream_t s) {
+    static std::atomic<uint64_t> configured{0};
+    constexpr uint32_t smem = TcLayout<D>::kAlloc;
+    static_assert(smem <= 227 * 1024, "shared memory over the sm_103 limit");
+    cudaError_t e = smem_limit_once(paged_tc_kernel<D>, smem, configured);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
+    p.row_tiles = static_cast<int>((rows + kRowsTc - 1) / kRowsTc);
+    const int64_t blocks = static_cast<int64_t>(p.row_tiles) * p.g.seqs * p.g.kv_heads;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    // Splits: while there are fewer blocks than SMs, down to four KV tiles
+    // each, as many as the workspace holds.
+    int64_t want = std::max<int64_t>(1, 152 / blocks);
+    want = std::min<int64_t>(want, (p.g.max_kv + 4 * kTileN - 1) / (4 * kTileN));
+    want = std::min<int64_t>(want, static_cast<int64_t>(part_floats_max / (blocks * tc_part_floats<D>())));
+    want = std::max<int64_t>(want, 1);
+    const int per = static_cast<int>((p.g.max_kv + want - 1) / want);
+    p.split_tokens = std::max(kTileN, (per + kTileN - 1) / kTileN * kTileN);
+    p.splits = std::max(1, (p.g.max_kv + p.split_tokens - 1) / p.split_tokens);
+    paged_tc_kernel<D><<<dim3(static_cast<unsigned>(blocks), p.splits), kTcThreads, smem, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const int64_t joins = (rows + 7) / 8 * p.g.seqs * p.g.kv_heads;
+    paged_tc_join_kernel<D><<<static_cast<unsigned>(joins), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(PagedAttnParams& p, int D, size_t part_floats_max, cudaStream_t s) {
+    return D == 128 ? launch_d<128>(p, part_floats_max, s) : launch_d<64>(p, part_floats_max, s);
+}
+
+}  // namespace rc
