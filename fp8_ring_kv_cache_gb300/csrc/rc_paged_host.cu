@@ -69,6 +69,8 @@ int check_paged(const rc_paged_view* v, const rc_paged_batch* b, bool queries, P
         (reinterpret_cast<uintptr_t>(v->workspace) & 255u))
         return RC_ERR_ARG;
     if (v->pages < 1 || v->kv_heads < 1 || v->kv_heads > 1024) return RC_ERR_ARG;
+    // blocks of 16 tokens are counted in 32 bits (2^32 of them would be 4 TB of codes at head_dim 64)
+    if ((static_cast<int64_t>(v->pages) * v->kv_heads << (shift - 4)) > INT64_C(0xffffffff)) return RC_ERR_UNSUPPORTED;
     if (b->seqs < 1 || b->seqs > 65535 || b->table_pages < 0 || b->tokens < 0 || b->max_new < 0 || b->max_kv < 0)
         return RC_ERR_ARG;
     if (b->max_kv > (1 << 24) || b->max_kv > static_cast<int64_t>(b->table_pages) * v->page_tokens) return RC_ERR_ARG;

@@ -2,13 +2,13 @@
 // tensor cores (tcgen05).
 //
 // A block has up to 256 query rows of one KV head (a sequence's new tokens x
-// the query heads that share it), 16 warps:
+// the query heads that share it), 20 warps:
 //   warp 0        issues the matrix products (one lane) and owns TMEM
 //   warps 4..7    softmax group 0, warps 8..11 softmax group 1 (a row a thread)
-//   warps 12..15  converters: read the codes of 128 cached tokens from their
-//                 pages (half a tile ahead, in registers), make them bf16 and
-//                 write the K and V tiles in the swizzled layout of a K-major
-//                 operand, two buffers each
+//   warps 12..15  convert K, warps 16..19 convert V: read the codes of 128
+//                 cached tokens from their pages (a tile ahead, in registers),
+//                 make them bf16 and write the tile in the swizzled layout of a
+//                 K-major operand, two buffers each
 // Scales are powers of two, so the bf16 tiles are exact, S = Q K^T needs no
 // factor per column, and both products run at the bf16 rate:
 //   S_i = Q_i K_j^T into TMEM; softmax of a row by its thread: P to bf16, over
@@ -30,10 +30,12 @@ namespace rc {
 
 namespace {
 
-constexpr int kTcThreads = 512;
+// A launch of 640 threads has 96 registers a thread; the warpgroups then share
+// them 32 + 2 x 168 + 2 x 56 = 5 x 96.
+constexpr int kTcThreads = 640;
 constexpr int kTileM = 128, kTileN = 128;
 constexpr int kRowsTc = 2 * kTileM;
-constexpr int kWgSoftmax0 = 1, kWgConvert = 3;
+constexpr int kWgSoftmax0 = 1, kWgConvertK = 3;
 constexpr uint32_t kTcTmem = 512;
 
 enum : int {
@@ -80,6 +82,12 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The first `left` of 16 bytes, the others 0.
+__device__ __forceinline__ uint4 cut16(uint4 v, int left) {
+    auto cut = [](uint32_t w, int n) { return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u); };
+    return make_uint4(cut(v.x, left), cut(v.y, left - 4), cut(v.z, left - 8), cut(v.w, left - 12));
 }
 
 // Cached tokens that the rows of a tile see, and how they are split.
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
     const uint32_t tmem = misc[0];
 
     if (wg == 0) {
-        regs_dec<56>();
+        regs_dec<32>();
         if (warp == 0 && U > 0) {
             // -------------------------------------------------------- products
             // Operand descriptors differ from a base only in the start address
@@ -226,9 +234,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                 }
             }
         }
-    } else if (wg != kWgConvert) {
+    } else if (wg < kWgConvertK) {
         // ------------------------------------------------------------ softmax
-        regs_inc<184>();
+        regs_inc<168>();
         const int i = wg - kWgSoftmax0;
         const int quad = warp & 3, r = quad * 32 + lane;  // TMEM lane quadrant; row within the group's tile
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
@@ -453,124 +461,131 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
         }
     } else {
         // ------------------------------------------------------------ converters
-        // Thread ct: of K, the piece of 16 dims ct % KP of the rows ct / KP +
-        // k 128 / KP; of V, the 16 tokens (ct % 8) 16 .. of the dims ct / 8 + 16 k.
-        // Lane l < 8 of each warp looks up the page of the tile's tokens 16 l ..
-        regs_dec<88>();
-        constexpr int KP = D / 16, KU = KP, VU = D / 16;  // pieces of a K row; pieces of a thread
-        const int ct = tid - kWgConvert * 128;
-        const int P = 1 << p.g.page_shift;
+        // Warpgroup 3 converts K, warpgroup 4 V, each its next tile in registers
+        // while it waits for a free buffer.  Lane l < 8 of a warp looks up where
+        // the tile's tokens [16 l, 16 l + 16) are: the number of their block of
+        // 16 among the pool's (page, head, 16 tokens).  Blocks behind the end of
+        // the sequence, or on a bad page, read block 0 instead: the softmax cuts
+        // K's columns, and V's get the scale byte 0 (a finite factor), as P is 0 there.
+        // Neighbouring groups of four lanes have neighbouring rows, whose
+        // swizzles differ in the lowest bit: the stores meet no bank conflict.
+        regs_dec<56>();
+        const int ct = tid & 127;
+        const int pb = p.g.page_shift - 4;  // blocks of a page: 1 << pb
         bool ok = true;
-        // page of the tile's tokens [16 (ct % 8), + 16); -1: none (bad page or behind the end)
-        auto page_at = [&](int j) {
-            const int t = j0 + j * kTileN + 16 * (ct & 7);
-            return j < T && t < q.kv ? load_page(p.g, s, t >> p.g.page_shift) : -1;
+        auto block_at = [&](int j) {
+            const int t = j0 + j * kTileN + 16 * (lane & 7);
+            if (j >= T || t >= q.kv) return 0u;
+            const int page = load_page(p.g, s, t >> p.g.page_shift);
+            const uint32_t at = static_cast<uint32_t>(max(page, 0)) * p.g.kv_heads + h;
+            return (at << pb) + (static_cast<uint32_t>(t >> 4) & ((1u << pb) - 1u));
         };
-        uint4 kr[KU], vr[VU];
-        uint32_t ks[KU];
-        uint4 vs;
-        auto fetch_k = [&](int j, int page) {
-#pragma unroll
-            for (int k = 0; k < KU; ++k) {
-                const int row = ct / KP + k * (128 / KP);
-                const int pg = __shfl_sync(0xffffffffu, page, row >> 4);
-                kr[k] = make_uint4(0, 0, 0, 0);
-                ks[k] = 0;
-                if (pg >= 0) {
-                    const size_t at = (static_cast<size_t>(pg) * p.g.kv_heads + h) * P + ((j0 + j * kTileN + row) & (P - 1));
-                    kr[k] = ldg_nc_na_v4(p.g.kcodes + at * D + 16 * (ct % KP));
-                    ks[k] = __ldg(p.g.kscale + at);
-                }
-            }
-        };
-        auto fetch_v = [&](int j, int page) {
-            const size_t ph = static_cast<size_t>(max(page, 0)) * p.g.kv_heads + h;
-            const int off = (j0 + j * kTileN + 16 * (ct & 7)) & (P - 1);
-#pragma unroll
-            for (int k = 0; k < VU; ++k) {
-                vr[k] = make_uint4(0, 0, 0, 0);
-                if (page >= 0) vr[k] = ldg_nc_na_v4(p.g.vcodes + (ph * D + (ct >> 3) + 16 * k) * P + off);
-            }
-        };
-        auto fetch_vs = [&](int j, int page) {
-            vs = make_uint4(0, 0, 0, 0);
-            if (page >= 0) {
-                const size_t ph = static_cast<size_t>(page) * p.g.kv_heads + h;
-                vs = __ldg(reinterpret_cast<const uint4*>(p.g.vscale + ph * P + ((j0 + j * kTileN + 16 * (ct & 7)) & (P - 1))));
-                // tokens behind the sequence's end: byte 0, with which any code is 0 or next to it
-                const int left = q.kv - (j0 + j * kTileN + 16 * (ct & 7));
-                if (left < 16) {
-                    uint32_t* w = &vs.x;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int n = left - 4 * k;
-                        w[k] = n <= 0 ? 0u : n < 4 ? w[k] & ((1u << (8 * n)) - 1u) : w[k];
-                    }
-                }
-            }
-        };
-        // the four values pairs of 16 codes, as bf16
+        // 16 codes as bf16, in the order (0, 2), (1, 3) of each four
         auto put = [&](uint8_t* lo, uint8_t* hi, const uint4& w, const uint32_t (&f)[8]) {
             *reinterpret_cast<uint4*>(lo) = make_uint4(bf2_mul(codes02(w.x), f[0]), bf2_mul(codes13(w.x), f[1]),
                                                        bf2_mul(codes02(w.y), f[2]), bf2_mul(codes13(w.y), f[3]));
             *reinterpret_cast<uint4*>(hi) = make_uint4(bf2_mul(codes02(w.z), f[4]), bf2_mul(codes13(w.z), f[5]),
                                                        bf2_mul(codes02(w.w), f[6]), bf2_mul(codes13(w.w), f[7]));
         };
-        int page = page_at(0);
-        if (T > 0) {
-            fetch_k(0, page);
-            fetch_vs(0, page);
-            fetch_v(0, page);
-        }
-        for (int j = 0; j < T; ++j) {
-            const int st = j & 1;
-            const int next = page_at(j + 1);
-            if (ok) ok = warp_wait(&bars[T_K_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
-            // V's scales: a byte over 134 is a row that is not a number; its
-            // values count as 0 here and the rows that see it are marked
-            const uint4 bad = make_uint4(__vcmpgtu4(vs.x, 0x86868686u), __vcmpgtu4(vs.y, 0x86868686u),
-                                         __vcmpgtu4(vs.z, 0x86868686u), __vcmpgtu4(vs.w, 0x86868686u));
-            const bool any = (bad.x | bad.y | bad.z | bad.w) != 0u;
-            if (ok) {
-                // slot j & 3: the softmax of tile j - 4 has read it (S of tile j - 2 came after that)
-                if (ct < 8) *reinterpret_cast<uint4*>(smem + Lay::kScale + (j & 3) * kTileN + 16 * ct) = vs;
-                const bool w_any = __any_sync(0xffffffffu, any);  // every warp holds all 8 blocks
-                if (ct == 0) misc[4 + (j & 3)] = w_any ? 1u : 0u;
-                uint8_t* dst = smem + Lay::kK + st * Lay::kTile;
-#pragma unroll
-                for (int k = 0; k < KU; ++k) {
-                    const int row = ct / KP + k * (128 / KP), dim = 16 * (ct % KP);
-                    const uint32_t f1 = scale_factor(ks[k]);
-                    const uint32_t f[8] = {f1, f1, f1, f1, f1, f1, f1, f1};
-                    put(dst + bktile_off(row, dim), dst + bktile_off(row, dim + 8), kr[k], f);
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[T_K_FULL + st]);
-            }
-            if (j + 1 < T) fetch_k(j + 1, next);
-            if (ok) ok = warp_wait(&bars[T_V_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
-            if (ok) {
-                uint32_t f[8];
-                const uint32_t w[4] = {vs.x & ~bad.x, vs.y & ~bad.y, vs.z & ~bad.z, vs.w & ~bad.w};
+        if (wg == kWgConvertK) {
+            // unit k: row rr + 32 (k / NB), dims 64 (k % NB) + 16 (ct % 4) ..
+            constexpr int NB = D / 64, KU = 4 * NB;
+            const int rr = ct >> 2;
+            const uint8_t* kbase = p.g.kcodes + (rr & 15) * D + 16 * (ct & 3);
+            const uint8_t* sbase = p.g.kscale + (rr & 15);
+            uint4 kr[KU];
+            uint32_t ks[4];
+            uint4 vs = make_uint4(0, 0, 0, 0);  // V scale bytes of the lane's block: only looked at
+            auto fetch = [&](int j, uint32_t blk) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    f[2 * k] = factors02(w[k]);
-                    f[2 * k + 1] = factors13(w[k]);
-                }
-                uint8_t* dst = smem + Lay::kV + st * Lay::kTile;
+                    const uint64_t at = __shfl_sync(0xffffffffu, blk, (rr >> 4) + 2 * k);
 #pragma unroll
-                for (int k = 0; k < VU; ++k) {
-                    const int d = (ct >> 3) + 16 * k, t = 16 * (ct & 7);
-                    put(dst + bvtile_off(d, t, D), dst + bvtile_off(d, t + 8, D), vr[k], f);
+                    for (int n = 0; n < NB; ++n) kr[k * NB + n] = ldg_nc_na_v4(kbase + at * (16 * D) + 64 * n);
+                    ks[k] = __ldg(sbase + at * 16);
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[T_V_FULL + st]);
+                vs = make_uint4(0, 0, 0, 0);
+                const int left = q.kv - (j0 + j * kTileN + 16 * lane);
+                if (ct < 8 && left > 0) {
+                    vs = __ldg(reinterpret_cast<const uint4*>(p.g.vscale + static_cast<uint64_t>(blk) * 16));
+                    vs = cut16(vs, left);
+                }
+            };
+            uint32_t next = block_at(0);
+            if (T > 0) fetch(0, next);
+            for (int j = 0; j < T; ++j) {
+                const int st = j & 1;
+                next = block_at(j + 1);
+                if (ok) ok = warp_wait(&bars[T_K_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
+                if (ok) {
+                    // A V row that is not a number (scale byte over 134) counts
+                    // as 0 in the product; the rows that see it are marked.  Slot
+                    // j & 3: the softmax of tile j - 4 has read it (the S whose
+                    // end freed this buffer came after that).
+                    if (warp == kWgConvertK * 4) {
+                        if (lane < 8) *reinterpret_cast<uint4*>(smem + Lay::kScale + (j & 3) * kTileN + 16 * lane) = vs;
+                        const bool bad = __any_sync(0xffffffffu, (__vcmpgtu4(vs.x, 0x86868686u) | __vcmpgtu4(vs.y, 0x86868686u) |
+                                                                  __vcmpgtu4(vs.z, 0x86868686u) | __vcmpgtu4(vs.w, 0x86868686u)) != 0u);
+                        if (lane == 0) misc[4 + (j & 3)] = bad ? 1u : 0u;
+                    }
+                    uint8_t* dst = smem + Lay::kK + st * Lay::kTile;
+                    uint8_t* lo = dst + bktile_off(rr, 16 * (ct & 3));
+                    uint8_t* hi = dst + bktile_off(rr, 16 * (ct & 3) + 8);
+#pragma unroll
+                    for (int k = 0; k < KU; ++k) {
+                        const uint32_t f1 = scale_factor(ks[k / NB]);
+                        const uint32_t f[8] = {f1, f1, f1, f1, f1, f1, f1, f1};
+                        const int off = (k % NB) * (kTileN * 128) + (k / NB) * (32 * 128);
+                        put(lo + off, hi + off, kr[k], f);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[T_K_FULL + st]);
+                }
+                if (j + 1 < T) fetch(j + 1, next);
             }
-            if (j + 1 < T) {
-                fetch_vs(j + 1, next);
-                fetch_v(j + 1, next);
+        } else {
+            // tokens 16 c .. of the dims d0 + 16 k
+            constexpr int VU = D / 16;
+            const int c = (ct & 3) | ((ct >> 4) & 4), d0 = (ct >> 2) & 15;
+            uint4 vr[VU];
+            uint4 vs;
+            auto fetch = [&](int j, uint32_t blk) {
+                const uint32_t at = __shfl_sync(0xffffffffu, blk, c);
+                // block `at` of 16 tokens: page and head at >> pb, place 16 (at mod 2^pb)
+                const uint8_t* src = p.g.vcodes + ((static_cast<uint64_t>(at >> pb) * D + d0) << p.g.page_shift) +
+                                     16 * (at & ((1u << pb) - 1u));
+#pragma unroll
+                for (int k = 0; k < VU; ++k) vr[k] = ldg_nc_na_v4(src + (static_cast<uint32_t>(16 * k) << p.g.page_shift));
+                const int left = q.kv - (j0 + j * kTileN + 16 * c);
+                vs = make_uint4(0, 0, 0, 0);
+                if (left > 0) vs = cut16(__ldg(reinterpret_cast<const uint4*>(p.g.vscale + static_cast<uint64_t>(at) * 16)), left);
+            };
+            uint32_t next = block_at(0);
+            if (T > 0) fetch(0, next);
+            for (int j = 0; j < T; ++j) {
+                const int st = j & 1;
+                next = block_at(j + 1);
+                if (ok) ok = warp_wait(&bars[T_V_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
+                if (ok) {
+                    uint32_t f[8];
+                    const uint32_t w[4] = {vs.x & ~__vcmpgtu4(vs.x, 0x86868686u), vs.y & ~__vcmpgtu4(vs.y, 0x86868686u),
+                                           vs.z & ~__vcmpgtu4(vs.z, 0x86868686u), vs.w & ~__vcmpgtu4(vs.w, 0x86868686u)};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        f[2 * k] = factors02(w[k]);
+                        f[2 * k + 1] = factors13(w[k]);
+                    }
+                    uint8_t* dst = smem + Lay::kV + st * Lay::kTile;
+                    uint8_t* lo = dst + bvtile_off(d0, 16 * c, D);
+                    uint8_t* hi = dst + bvtile_off(d0, 16 * c + 8, D);
+#pragma unroll
+                    for (int k = 0; k < VU; ++k) put(lo + 16 * 128 * k, hi + 16 * 128 * k, vr[k], f);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[T_V_FULL + st]);
+                }
+                if (j + 1 < T) fetch(j + 1, next);
             }
         }
     }
