@@ -52,15 +52,31 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int s) {
     return q;
 }
 
+// Read-only loads that stay where they are written: the compiler would move a
+// plain load made for the next step of a loop down to its use there.
+__device__ __forceinline__ uint32_t ldg_early(const uint32_t* p) {
+    uint32_t r;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint32_t ldg_early(const uint8_t* p) {
+    uint32_t r;
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+}
+
+// Whether a page table entry is a page of the pool; flagged if not.
+__device__ __forceinline__ bool check_page(const PagedParams& p, int page) {
+    if (page >= 0 && page < p.pages) return true;
+    flag_meta(p.status);
+    return false;
+}
+
 // Page of tokens [i P, i P + P) of sequence s, or -1 (flagged) if the table
 // holds no page of the pool.  i P < kv_len <= table_pages P by load_seq.
 __device__ __forceinline__ int load_page(const PagedParams& p, int s, int i) {
     const int page = __ldg(p.page_table + static_cast<size_t>(s) * p.table_pages + i);
-    if (page < 0 || page >= p.pages) {
-        flag_meta(p.status);
-        return -1;
-    }
-    return page;
+    return check_page(p, page) ? page : -1;
 }
 
 // (cos, sin) of position * frequency: the product modulo one turn is exact in

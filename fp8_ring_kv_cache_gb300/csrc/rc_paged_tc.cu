@@ -177,61 +177,77 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
         regs_dec<32>();
         if (warp == 0 && U > 0) {
             // -------------------------------------------------------- products
-            // Operand descriptors differ from a base only in the start address
-            // (16-byte units, no carry below 256 KB), so one add moves them.
+            // Operand descriptors differ only in the start address (the low 14
+            // bits, in 16 bytes; no carry below 256 KB): an add of a constant.
             const uint32_t idesc_qk = instr_desc(kFmtBF16, kFmtBF16, 128, 128);
             const uint32_t idesc_pv = instr_desc(kFmtBF16, kFmtBF16, 128, D);
-            const uint64_t dq0 = smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2);
-            const uint64_t dk0 = smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2);
-            const uint64_t dv0 = smem_desc(smem_u32(smem + Lay::kV), 16, 1024, 2);
+            const uint64_t dq = smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2);
+            const uint32_t hi = static_cast<uint32_t>(dq >> 32), q_lo = static_cast<uint32_t>(dq);
+            const uint32_t k_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2));
+            const uint32_t v_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + Lay::kV), 16, 1024, 2));
+            // the same in every lane, and known to be by the compiler
+            const bool two_u = __shfl_sync(0xffffffffu, two ? 1 : 0, 0) != 0;
+            const int U_u = __shfl_sync(0xffffffffu, U, 0);
             auto issue_qk = [&](int u) {
-                const int i = u & 1, j = tile_of(u);
-                const uint64_t qa = dq0 + ((two && i) ? Lay::kTile >> 4 : 0u);
-                const uint64_t kb = dk0 + ((j & 1) ? Lay::kTile >> 4 : 0u);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_f16_ss(tmem + 128u * i, qa + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                               kb + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), idesc_qk, k != 0);
+                const int i = u & 1, j = two_u ? u >> 1 : u;
+                const uint32_t d = tmem + 128u * i, qa = q_lo + ((two_u && i) ? Lay::kTile >> 4 : 0u);
+                const uint32_t kb = k_lo + ((j & 1) ? Lay::kTile >> 4 : 0u);
+                mma_f16_ss_at<0, 0>(d, qa, kb, hi, idesc_qk, 0);
+                mma_f16_ss_at<2, 2>(d, qa, kb, hi, idesc_qk, 1);
+                mma_f16_ss_at<4, 4>(d, qa, kb, hi, idesc_qk, 1);
+                mma_f16_ss_at<6, 6>(d, qa, kb, hi, idesc_qk, 1);
+                if (D == 128) {
+                    mma_f16_ss_at<1024, 1024>(d, qa, kb, hi, idesc_qk, 1);
+                    mma_f16_ss_at<1026, 1026>(d, qa, kb, hi, idesc_qk, 1);
+                    mma_f16_ss_at<1028, 1028>(d, qa, kb, hi, idesc_qk, 1);
+                    mma_f16_ss_at<1030, 1030>(d, qa, kb, hi, idesc_qk, 1);
+                }
                 mma_commit(&bars[T_S_FULL + i]);
-                if (!two || i == 1) mma_commit(&bars[T_K_EMPTY + (j & 1)]);
+                if (!two_u || i == 1) mma_commit(&bars[T_K_EMPTY + (j & 1)]);
             };
             auto issue_pv = [&](int u) {
-                const int i = u & 1, j = tile_of(u);
-                const uint64_t vb = dv0 + ((j & 1) ? Lay::kTile >> 4 : 0u);
-#pragma unroll
-                for (int k = 0; k < kTileN / 16; ++k)
-                    mma_f16_ts(tmem + 256u + static_cast<uint32_t>(D) * i, tmem + 128u * i + 8 * k,
-                               vb + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), idesc_pv, (u > 1 || k > 0) ? 1u : 0u);
-                if (!two || i == 1) mma_commit(&bars[T_V_EMPTY + (j & 1)]);
+                const int i = u & 1, j = two_u ? u >> 1 : u;
+                const uint32_t d = tmem + 256u + static_cast<uint32_t>(D) * i, pa = tmem + 128u * i;
+                const uint32_t vb = v_lo + ((j & 1) ? Lay::kTile >> 4 : 0u);
+                constexpr uint32_t H = D * 128 / 16;  // the second 64 tokens
+                mma_f16_ts_at<0, 0>(d, pa, vb, hi, idesc_pv, u > 1);
+                mma_f16_ts_at<8, 2>(d, pa, vb, hi, idesc_pv, 1);
+                mma_f16_ts_at<16, 4>(d, pa, vb, hi, idesc_pv, 1);
+                mma_f16_ts_at<24, 6>(d, pa, vb, hi, idesc_pv, 1);
+                mma_f16_ts_at<32, H>(d, pa, vb, hi, idesc_pv, 1);
+                mma_f16_ts_at<40, H + 2>(d, pa, vb, hi, idesc_pv, 1);
+                mma_f16_ts_at<48, H + 4>(d, pa, vb, hi, idesc_pv, 1);
+                mma_f16_ts_at<56, H + 6>(d, pa, vb, hi, idesc_pv, 1);
+                if (!two_u || i == 1) mma_commit(&bars[T_V_EMPTY + (j & 1)]);
             };
-            const bool leader = lane == 0;
             bool ok = true;
-            for (int u = 0; u < 2 && u < U; ++u) {
-                const int j = tile_of(u);
-                bool r = true;
-                if (leader && ok) r = mbar_wait(&bars[T_K_FULL + (j & 1)], 0, ab, kDevTimeoutMma);
-                ok = ok && __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
-                if (ok && leader) {
-                    tc_fence_after();
-                    issue_qk(u);
-                }
+#pragma unroll 1
+            for (int u = 0; u < 2 && u < U_u; ++u) {
+                ok = ok && warp_wait(&bars[T_K_FULL + ((two_u ? 0 : u) & 1)], 0, ab, kDevTimeoutMma);
+                tc_fence_after();
+                if (ok && elect_one()) issue_qk(u);
+                __syncwarp();
             }
             // every unit passes its rendezvous, also after an abort, so no partner is left waiting
-            for (int u = 0; u < U; ++u) {
+#pragma unroll 1
+            for (int u = 0; u < U_u; ++u) {
                 ok = named_barrier_and(kNbUnit + (u & 1), kNbUnitThreads, ok);
-                if (ok && leader) {
-                    tc_fence_after();
+                tc_fence_after();
+                if (ok && elect_one()) {
                     issue_pv(u);
-                    if (u + 2 < U) issue_qk(u + 2);
-                    if (u + 1 == U) mma_commit(&bars[T_O_DONE]);
+                    if (u + 2 < U_u) issue_qk(u + 2);
                 }
+                __syncwarp();
             }
-            if (leader) {
+            // (the lane that issued the products commits them)
+            if (elect_one()) {
+                if (ok) mma_commit(&bars[T_O_DONE]);
                 // every product has finished before the tensor memory is released
                 mma_commit(&bars[T_DRAIN]);
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(&bars[T_DRAIN], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
-                }
+            }
+            __syncwarp();
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(&bars[T_DRAIN], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
         }
     } else if (wg < kWgConvertK) {
@@ -267,35 +283,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             if (!warp_wait(&bars[T_S_FULL + i], (u >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
             tc_fence_after();
             const int room = limit - j * kTileN;  // columns the row sees
-            uint32_t v0[32], v1[32], v2[32], v3[32];
-            tmem_ld32_async(s_tm, v0);
-            tmem_ld32_async(s_tm + 32, v1);
-            tmem_ld32_async(s_tm + 64, v2);
-            tmem_ld32_async(s_tm + 96, v3);
-            tmem_wait_ld_dep(v0);
-            reg_fence(v1);
-            reg_fence(v2);
-            reg_fence(v3);
+            uint32_t v[128];
+            tmem_ld128(s_tm, v);
             if (!__all_sync(0xffffffffu, room >= kTileN)) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    if (k >= room) v0[k] = 0xff800000u;
-                    if (k + 32 >= room) v1[k] = 0xff800000u;
-                    if (k + 64 >= room) v2[k] = 0xff800000u;
-                    if (k + 96 >= room) v3[k] = 0xff800000u;
-                }
+                for (int k = 0; k < kTileN; ++k)
+                    if (k >= room) v[k] = 0xff800000u;
             }
-            auto chunk_max = [](const uint32_t (&v)[32]) {
-                float t[11];
+            float mx[4];
 #pragma unroll
-                for (int k = 0; k < 10; ++k)
-                    t[k] = max3(__uint_as_float(v[3 * k]), __uint_as_float(v[3 * k + 1]), __uint_as_float(v[3 * k + 2]));
-                t[10] = fmaxf(__uint_as_float(v[30]), __uint_as_float(v[31]));
-                const float u0 = max3(t[0], t[1], t[2]), u1 = max3(t[3], t[4], t[5]);
-                const float u2 = max3(t[6], t[7], t[8]), u3 = max3(t[9], t[10], u0);
-                return max3(u1, u2, u3);
-            };
-            const float m_tile = fmaxf(fmaxf(chunk_max(v0), chunk_max(v1)), fmaxf(chunk_max(v2), chunk_max(v3))) * a;
+            for (int c = 0; c < 4; ++c) {
+                mx[c] = fmaxf(__uint_as_float(v[c]), __uint_as_float(v[4 + c]));
+#pragma unroll
+                for (int k = 8; k < kTileN; k += 8)
+                    mx[c] = max3(mx[c], __uint_as_float(v[k + c]), __uint_as_float(v[k + 4 + c]));
+            }
+            const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a;
             // the running max moves only when a tile raises it by more than
             // 2^8 of weight: bf16 and fp32 hold the larger weights as well
             const bool bump = (m_run == -INFINITY) || (m_tile > m_run + 8.f);
@@ -304,11 +307,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             const float alpha = bump ? ex2(m_run - base) : 1.f;
             const float2 n2 = make_float2(-base, -base);
             float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
-            auto p_chunk = [&](const uint32_t (&v)[32], uint32_t* pk) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    const float2 x0 = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), a2, n2);
-                    const float2 x1 = fma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), a2, n2);
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 64; k += 4) {
+                    const uint32_t* w = v + 64 * half + k;
+                    const float2 x0 = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), a2, n2);
+                    const float2 x1 = fma2(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), a2, n2);
                     const float2 q0 = make_float2(ex2(x0.x), ex2(x0.y));
                     const float2 q1 = make_float2(ex2(x1.x), ex2(x1.y));
                     ls0 = add2(ls0, q0);
@@ -316,14 +322,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                     pk[k / 2] = pack_bf16(q0.x, q1.x);      // tokens 0, 2
                     pk[k / 2 + 1] = pack_bf16(q0.y, q1.y);  // tokens 1, 3
                 }
-            };
-            uint32_t pa[32], pb[32];
-            p_chunk(v0, pa);
-            p_chunk(v1, pa + 16);
-            tmem_st32(s_tm, pa);
-            p_chunk(v2, pb);
-            p_chunk(v3, pb + 16);
-            tmem_st32(s_tm + 32, pb);
+                tmem_st32(s_tm + 32 * half, pk);
+            }
             if (misc[4 + (j & 3)] != 0u) {
                 const uint8_t* vs = smem + Lay::kScale + (j & 3) * kTileN;
                 for (int k = 0; k < kTileN; ++k) poison |= vs[k] > 134 && k < room;
@@ -473,11 +473,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
         const int ct = tid & 127;
         const int pb = p.g.page_shift - 4;  // blocks of a page: 1 << pb
         bool ok = true;
-        auto block_at = [&](int j) {
+        const uint32_t* table =
+            reinterpret_cast<const uint32_t*>(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages);
+        // the page table's entry is read two tiles ahead and looked at one
+        // tile ahead, so no load waits for another
+        auto entry_at = [&](int j) {
+            const int t = j0 + j * kTileN + 16 * (lane & 7);
+            return j < T && t < q.kv ? static_cast<int>(ldg_early(table + (t >> p.g.page_shift))) : 0;
+        };
+        auto block_of = [&](int j, int page) {
             const int t = j0 + j * kTileN + 16 * (lane & 7);
             if (j >= T || t >= q.kv) return 0u;
-            const int page = load_page(p.g, s, t >> p.g.page_shift);
-            const uint32_t at = static_cast<uint32_t>(max(page, 0)) * p.g.kv_heads + h;
+            const uint32_t at = static_cast<uint32_t>(check_page(p.g, page) ? page : 0) * p.g.kv_heads + h;
             return (at << pb) + (static_cast<uint32_t>(t >> 4) & ((1u << pb) - 1u));
         };
         // 16 codes as bf16, in the order (0, 2), (1, 3) of each four
@@ -496,96 +503,110 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             uint4 kr[KU];
             uint32_t ks[4];
             uint4 vs = make_uint4(0, 0, 0, 0);  // V scale bytes of the lane's block: only looked at
-            auto fetch = [&](int j, uint32_t blk) {
+            // rows rr + 32 m of tile j, whose block is `blk` of lane (rr >> 4) + 2 m
+            auto fetch = [&](int m, uint32_t blk) {
+                const uint64_t at = __shfl_sync(0xffffffffu, blk, (rr >> 4) + 2 * m);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint64_t at = __shfl_sync(0xffffffffu, blk, (rr >> 4) + 2 * k);
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) kr[k * NB + n] = ldg_nc_na_v4(kbase + at * (16 * D) + 64 * n);
-                    ks[k] = __ldg(sbase + at * 16);
-                }
-                vs = make_uint4(0, 0, 0, 0);
-                const int left = q.kv - (j0 + j * kTileN + 16 * lane);
-                if (ct < 8 && left > 0) {
-                    vs = __ldg(reinterpret_cast<const uint4*>(p.g.vscale + static_cast<uint64_t>(blk) * 16));
-                    vs = cut16(vs, left);
-                }
+                for (int n = 0; n < NB; ++n) kr[m * NB + n] = ldg_nc_na_v4(kbase + at * (16 * D) + 64 * n);
+                ks[m] = ldg_early(sbase + at * 16);
             };
-            uint32_t next = block_at(0);
-            if (T > 0) fetch(0, next);
+            auto fetch_vs = [&](uint32_t blk) {
+                if (ct < 8) vs = ldg_nc_na_v4(p.g.vscale + static_cast<uint64_t>(blk) * 16);
+            };
+            int ahead = entry_at(1);
+            if (T > 0) {
+                const uint32_t blk = block_of(0, entry_at(0));
+#pragma unroll
+                for (int m = 0; m < 4; ++m) fetch(m, blk);
+                fetch_vs(blk);
+            }
             for (int j = 0; j < T; ++j) {
                 const int st = j & 1;
-                next = block_at(j + 1);
+                const uint32_t blk = block_of(j + 1, ahead);  // (block 0 past the last tile: read, not used)
+                ahead = entry_at(j + 2);
                 if (ok) ok = warp_wait(&bars[T_K_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
-                if (ok) {
-                    // A V row that is not a number (scale byte over 134) counts
-                    // as 0 in the product; the rows that see it are marked.  Slot
-                    // j & 3: the softmax of tile j - 4 has read it (the S whose
-                    // end freed this buffer came after that).
-                    if (warp == kWgConvertK * 4) {
-                        if (lane < 8) *reinterpret_cast<uint4*>(smem + Lay::kScale + (j & 3) * kTileN + 16 * lane) = vs;
-                        const bool bad = __any_sync(0xffffffffu, (__vcmpgtu4(vs.x, 0x86868686u) | __vcmpgtu4(vs.y, 0x86868686u) |
-                                                                  __vcmpgtu4(vs.z, 0x86868686u) | __vcmpgtu4(vs.w, 0x86868686u)) != 0u);
-                        if (lane == 0) misc[4 + (j & 3)] = bad ? 1u : 0u;
-                    }
-                    uint8_t* dst = smem + Lay::kK + st * Lay::kTile;
-                    uint8_t* lo = dst + bktile_off(rr, 16 * (ct & 3));
-                    uint8_t* hi = dst + bktile_off(rr, 16 * (ct & 3) + 8);
-#pragma unroll
-                    for (int k = 0; k < KU; ++k) {
-                        const uint32_t f1 = scale_factor(ks[k / NB]);
-                        const uint32_t f[8] = {f1, f1, f1, f1, f1, f1, f1, f1};
-                        const int off = (k % NB) * (kTileN * 128) + (k / NB) * (32 * 128);
-                        put(lo + off, hi + off, kr[k], f);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[T_K_FULL + st]);
+                if (!ok) continue;
+                // A V row that is not a number (scale byte over 134) counts as
+                // 0 in the product; the rows that see it are marked.  Slot
+                // j & 3: the softmax of tile j - 4 has read it (the S whose end
+                // freed this buffer came after that).
+                if (warp == kWgConvertK * 4) {
+                    const uint4 cut = cut16(vs, q.kv - (j0 + j * kTileN + 16 * lane));
+                    if (lane < 8) *reinterpret_cast<uint4*>(smem + Lay::kScale + (j & 3) * kTileN + 16 * lane) = cut;
+                    const bool bad =
+                        __any_sync(0xffffffffu, lane < 8 && (__vcmpgtu4(cut.x, 0x86868686u) | __vcmpgtu4(cut.y, 0x86868686u) |
+                                                             __vcmpgtu4(cut.z, 0x86868686u) | __vcmpgtu4(cut.w, 0x86868686u)) != 0u);
+                    if (lane == 0) misc[4 + (j & 3)] = bad ? 1u : 0u;
                 }
-                if (j + 1 < T) fetch(j + 1, next);
+                fetch_vs(blk);
+                uint8_t* dst = smem + Lay::kK + st * Lay::kTile;
+                uint8_t* lo = dst + bktile_off(rr, 16 * (ct & 3));
+                uint8_t* hi = dst + bktile_off(rr, 16 * (ct & 3) + 8);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t f1 = scale_factor(ks[m]);
+                    const uint32_t f[8] = {f1, f1, f1, f1, f1, f1, f1, f1};
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        const int off = n * (kTileN * 128) + m * (32 * 128);
+                        put(lo + off, hi + off, kr[m * NB + n], f);
+                    }
+                    fetch(m, blk);  // the next tile's rows, into the registers just freed
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[T_K_FULL + st]);
             }
         } else {
             // tokens 16 c .. of the dims d0 + 16 k
             constexpr int VU = D / 16;
             const int c = (ct & 3) | ((ct >> 4) & 4), d0 = (ct >> 2) & 15;
             uint4 vr[VU];
-            uint4 vs;
-            auto fetch = [&](int j, uint32_t blk) {
-                const uint32_t at = __shfl_sync(0xffffffffu, blk, c);
-                // block `at` of 16 tokens: page and head at >> pb, place 16 (at mod 2^pb)
-                const uint8_t* src = p.g.vcodes + ((static_cast<uint64_t>(at >> pb) * D + d0) << p.g.page_shift) +
-                                     16 * (at & ((1u << pb) - 1u));
-#pragma unroll
-                for (int k = 0; k < VU; ++k) vr[k] = ldg_nc_na_v4(src + (static_cast<uint32_t>(16 * k) << p.g.page_shift));
-                const int left = q.kv - (j0 + j * kTileN + 16 * c);
-                vs = make_uint4(0, 0, 0, 0);
-                if (left > 0) vs = cut16(__ldg(reinterpret_cast<const uint4*>(p.g.vscale + static_cast<uint64_t>(at) * 16)), left);
+            uint4 vs = make_uint4(0, 0, 0, 0);
+            // block `at` of 16 tokens: page and head at >> pb, place 16 (at mod 2^pb)
+            auto source = [&](uint32_t at) {
+                return p.g.vcodes + ((static_cast<uint64_t>(at >> pb) * D + d0) << p.g.page_shift) + 16 * (at & ((1u << pb) - 1u));
             };
-            uint32_t next = block_at(0);
-            if (T > 0) fetch(0, next);
+            const uint32_t step = 16u << p.g.page_shift;  // 16 dims
+            auto fetch_vs = [&](uint32_t at) {
+                vs = ldg_nc_na_v4(p.g.vscale + static_cast<uint64_t>(at) * 16);
+            };
+            int ahead = entry_at(1);
+            if (T > 0) {
+                const uint32_t at = __shfl_sync(0xffffffffu, block_of(0, entry_at(0)), c);
+                const uint8_t* src = source(at);
+#pragma unroll
+                for (int k = 0; k < VU; ++k) vr[k] = ldg_nc_na_v4(src + k * step);
+                fetch_vs(at);
+            }
             for (int j = 0; j < T; ++j) {
                 const int st = j & 1;
-                next = block_at(j + 1);
+                const uint32_t at = __shfl_sync(0xffffffffu, block_of(j + 1, ahead), c);
+                ahead = entry_at(j + 2);
                 if (ok) ok = warp_wait(&bars[T_V_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
-                if (ok) {
-                    uint32_t f[8];
-                    const uint32_t w[4] = {vs.x & ~__vcmpgtu4(vs.x, 0x86868686u), vs.y & ~__vcmpgtu4(vs.y, 0x86868686u),
-                                           vs.z & ~__vcmpgtu4(vs.z, 0x86868686u), vs.w & ~__vcmpgtu4(vs.w, 0x86868686u)};
+                if (!ok) continue;
+                uint32_t f[8];
+                const uint4 cut = cut16(vs, q.kv - (j0 + j * kTileN + 16 * c));
+                const uint32_t w[4] = {cut.x & ~__vcmpgtu4(cut.x, 0x86868686u), cut.y & ~__vcmpgtu4(cut.y, 0x86868686u),
+                                       cut.z & ~__vcmpgtu4(cut.z, 0x86868686u), cut.w & ~__vcmpgtu4(cut.w, 0x86868686u)};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        f[2 * k] = factors02(w[k]);
-                        f[2 * k + 1] = factors13(w[k]);
-                    }
-                    uint8_t* dst = smem + Lay::kV + st * Lay::kTile;
-                    uint8_t* lo = dst + bvtile_off(d0, 16 * c, D);
-                    uint8_t* hi = dst + bvtile_off(d0, 16 * c + 8, D);
-#pragma unroll
-                    for (int k = 0; k < VU; ++k) put(lo + 16 * 128 * k, hi + 16 * 128 * k, vr[k], f);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[T_V_FULL + st]);
+                for (int k = 0; k < 4; ++k) {
+                    f[2 * k] = factors02(w[k]);
+                    f[2 * k + 1] = factors13(w[k]);
                 }
-                if (j + 1 < T) fetch(j + 1, next);
+                fetch_vs(at);
+                const uint8_t* src = source(at);
+                uint8_t* dst = smem + Lay::kV + st * Lay::kTile;
+                uint8_t* lo = dst + bvtile_off(d0, 16 * c, D);
+                uint8_t* hi = dst + bvtile_off(d0, 16 * c + 8, D);
+#pragma unroll
+                for (int k = 0; k < VU; ++k) {
+                    put(lo + 16 * 128 * k, hi + 16 * 128 * k, vr[k], f);
+                    vr[k] = ldg_nc_na_v4(src + k * step);  // the next tile's, into the registers just freed
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[T_V_FULL + st]);
             }
         }
     }
