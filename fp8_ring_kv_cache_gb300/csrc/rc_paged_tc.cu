@@ -3,29 +3,22 @@
 //
 // A block has up to 256 query rows of one KV head (a sequence's new tokens x
 // the query heads that share it), 20 warps:
-//   warp 0        issues the products Q K^T (one lane) and owns TMEM
-//   warp 3        issues the products P V: a thread that issues products is
-//                 held up by them, so one thread for both left the tensor cores
-//                 idle while it looked for the next unit
+//   warp 0        issues the matrix products (one lane) and owns TMEM
 //   warps 4..7    softmax group 0, warps 8..11 softmax group 1 (a row a thread)
-//   warp 2        marks the tiles that hold a V that is not a number
 //   warps 12..15  convert K, warps 16..19 convert V: read the codes of 128
 //                 cached tokens from their pages (a tile ahead, in registers),
 //                 make them bf16 and write the tile in the swizzled layout of a
 //                 K-major operand, two buffers each
 // Scales are powers of two, so the bf16 tiles are exact, S = Q K^T needs no
 // factor per column, and both products run at the bf16 rate:
-//   S = Q K^T into TMEM; softmax of a row by its thread: P to bf16, over S in
-//   TMEM; O += P V with P read from TMEM.
-// The work is a chain of units: unit v belongs to group v & 1 and is 64 cached
-// tokens, half a tile, for 128 rows.  With more than 128 rows group i has rows
-// [128 i, 128 i + 128) and both groups take each half tile; with fewer both
-// groups have the same rows, group i takes half i of every tile, and their
-// results are joined at the end.  A group has two places for scores in TMEM: the
-// products of its next unit run while it is in the softmax of this one.  (With
-// one place for 128 tokens each group spent a third of its time waiting for
-// products: 108 us for 757 x 5,788 tokens x 48 heads.)  After P of unit v come
-// O += P V of unit v and S of unit v + 4, which overwrites P's place.
+//   S_i = Q_i K_j^T into TMEM; softmax of a row by its thread: P to bf16, over
+//   S in TMEM; O_i += P_i V_j with P read from TMEM.
+// The work is a chain of units: unit u is (KV tile, group u & 1).  With more
+// than 128 rows group i has rows [128 i, 128 i + 128) and both groups take
+// each KV tile; with fewer both groups have the same rows and take the KV tiles
+// in turn, and their results are joined at the end.  Either way the products of
+// one group run while the other is in softmax.  After P of unit u: O += P V of
+// unit u, then S of unit u + 2, which overwrites P's place.
 // A code word gives the pairs (0, 2) and (1, 3) of its four values cheapest:
 // that order is kept along the summed dims (Q is stored in it) and along the
 // cached tokens (P is packed in it).
@@ -38,7 +31,7 @@ namespace rc {
 namespace {
 
 // A launch of 640 threads has 96 registers a thread; the warpgroups then share
-// them 48 + 2 x 144 + 2 x 72 = 5 x 96.
+// them 32 + 2 x 168 + 2 x 56 = 5 x 96.
 constexpr int kTcThreads = 640;
 constexpr int kTileM = 128, kTileN = 128;
 constexpr int kRowsTc = 2 * kTileM;
@@ -50,15 +43,17 @@ enum : int {
     T_K_EMPTY = 2,  // [2] its products have finished
     T_V_FULL = 4,
     T_V_EMPTY = 6,
-    T_S_FULL = 8,    // [group][place] scores in TMEM
-    T_P_FULL = 12,   // [group][place] weights in TMEM
-    T_O_READY = 16,  // [group][place] the unit's product into O has finished
-    T_O_DONE = 20,
-    T_DRAIN = 21,
-    T_COUNT = 22
+    T_S_FULL = 8,  // [2] scores of group i in TMEM
+    T_O_DONE = 10,
+    T_DRAIN = 11,
+    T_COUNT = 12
 };
-constexpr int kUnit = 64;   // cached tokens of a unit
-constexpr int kNbJoin = 1;  // named barrier of the two softmax groups at the end
+// Named barriers: group i with the product warp (P in TMEM; the group's
+// checker lane has seen V of this unit and K of unit u + 2), and the two
+// groups at the end.
+constexpr int kNbUnit = 1;  // [2]
+constexpr int kNbJoin = 3;
+constexpr int kNbUnitThreads = 128 + 32;
 
 template <int D>
 struct TcLayout {
@@ -66,9 +61,9 @@ struct TcLayout {
     static constexpr uint32_t kQ = 0;                  // [2][D/64][128][128 B]
     static constexpr uint32_t kK = 2 * kTile;          // [2 buffers]
     static constexpr uint32_t kV = kK + 2 * kTile;     // [2 buffers][2 halves][D][128 B]
-    static constexpr uint32_t kScale = kV + 2 * kTile; // V scale bytes of the last eight KV tiles, where marked
-    static constexpr uint32_t kBar = kScale + 8 * kTileN;
-    static constexpr uint32_t kMisc = kBar + 8 * T_COUNT;  // [0] tmem, [1] abort, [4..11] KV tile holds a V that is not a number
+    static constexpr uint32_t kScale = kV + 2 * kTile; // V scale bytes of the last four KV tiles
+    static constexpr uint32_t kBar = kScale + 4 * kTileN;
+    static constexpr uint32_t kMisc = kBar + 8 * T_COUNT;  // [0] tmem, [1] abort, [4..7] KV tile holds a V that is not a number
     static constexpr uint32_t kTotal = kMisc + 64;
     static constexpr uint32_t kAlloc = kTotal + 1024;
 };
@@ -132,26 +127,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
     const int rows_here = min(kRowsTc, tw.rows - row0);
     const bool two = rows_here > kTileM;              // two row tiles; else one, KV tiles in turn
     const int T = (j1 - j0 + kTileN - 1) / kTileN;    // KV tiles
-    const int U = two ? 4 * T : 2 * T;                // units
+    const int U = two ? 2 * T : T;                    // units
     AbortState ab{reinterpret_cast<volatile uint32_t*>(&misc[1]), p.g.status, p.wait_ns};
+    auto tile_of = [&](int u) { return two ? u >> 1 : u; };
 
     // ------------------------------------------------------------ set-up
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[T_K_FULL + i], 5);  // four converters and the marking warp
+            mbar_init(&bars[T_K_FULL + i], 4);
             mbar_init(&bars[T_K_EMPTY + i], 1);
             mbar_init(&bars[T_V_FULL + i], 4);
             mbar_init(&bars[T_V_EMPTY + i], 1);
-        }
-        for (int i = 0; i < 4; ++i) {
             mbar_init(&bars[T_S_FULL + i], 1);
-            mbar_init(&bars[T_P_FULL + i], 4);
-            mbar_init(&bars[T_O_READY + i], 1);
         }
         mbar_init(&bars[T_O_DONE], 1);
-        mbar_init(&bars[T_DRAIN], 2);
+        mbar_init(&bars[T_DRAIN], 1);
         misc[1] = 0u;
-        for (int i = 4; i < 12; ++i) misc[i] = 0u;
+        for (int i = 4; i < 8; ++i) misc[i] = 0u;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -182,31 +174,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
     const uint32_t tmem = misc[0];
 
     if (wg == 0) {
-        regs_dec<48>();
-        if ((warp == 0 || warp == 3) && U > 0) {
+        regs_dec<32>();
+        if (warp == 0 && U > 0) {
             // -------------------------------------------------------- products
             // Operand descriptors differ only in the start address (the low 14
             // bits, in 16 bytes; no carry below 256 KB): an add of a constant.
-            const uint32_t idesc_qk = instr_desc(kFmtBF16, kFmtBF16, 128, kUnit);
+            const uint32_t idesc_qk = instr_desc(kFmtBF16, kFmtBF16, 128, 128);
             const uint32_t idesc_pv = instr_desc(kFmtBF16, kFmtBF16, 128, D);
             const uint64_t dq = smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2);
             const uint32_t hi = static_cast<uint32_t>(dq >> 32), q_lo = static_cast<uint32_t>(dq);
             const uint32_t k_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2));
             const uint32_t v_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + Lay::kV), 16, 1024, 2));
-            // The same in every lane, and known to be by the compiler (votes and
-            // reductions have uniform results), which then keeps all operands in
-            // uniform registers.
-            const bool two_u = __ballot_sync(0xffffffffu, two) != 0u;
-            const int U_u = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(U)));
-            const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
-            auto tile_of = [&](int v) { return two_u ? v >> 2 : v >> 1; };
-            auto half_of = [&](int v) { return two_u ? (v >> 1) & 1 : v & 1; };
-            auto first_of = [&](int v) { return (v & (two_u ? 3 : 1)) == 0; };  // first, last unit of its tile
-            auto last_of = [&](int v) { return (v & (two_u ? 3 : 1)) == (two_u ? 3 : 1); };
-            auto issue_qk = [&](int v) {
-                const int i = v & 1, n = (v >> 1) & 1, j = tile_of(v);
-                const uint32_t d = tm + 128u * i + kUnit * n, qa = q_lo + ((two_u && i) ? Lay::kTile >> 4 : 0u);
-                const uint32_t kb = k_lo + ((j & 1) ? Lay::kTile >> 4 : 0u) + (half_of(v) ? kUnit * 128 >> 4 : 0u);
+            // the same in every lane, and known to be by the compiler
+            const bool two_u = __shfl_sync(0xffffffffu, two ? 1 : 0, 0) != 0;
+            const int U_u = __shfl_sync(0xffffffffu, U, 0);
+            auto issue_qk = [&](int u) {
+                const int i = u & 1, j = two_u ? u >> 1 : u;
+                const uint32_t d = tmem + 128u * i, qa = q_lo + ((two_u && i) ? Lay::kTile >> 4 : 0u);
+                const uint32_t kb = k_lo + ((j & 1) ? Lay::kTile >> 4 : 0u);
                 mma_f16_ss_at<0, 0>(d, qa, kb, hi, idesc_qk, 0);
                 mma_f16_ss_at<2, 2>(d, qa, kb, hi, idesc_qk, 1);
                 mma_f16_ss_at<4, 4>(d, qa, kb, hi, idesc_qk, 1);
@@ -217,48 +202,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                     mma_f16_ss_at<1028, 1028>(d, qa, kb, hi, idesc_qk, 1);
                     mma_f16_ss_at<1030, 1030>(d, qa, kb, hi, idesc_qk, 1);
                 }
-                mma_commit(&bars[T_S_FULL + 2 * i + n]);
-                if (last_of(v)) mma_commit(&bars[T_K_EMPTY + (j & 1)]);
+                mma_commit(&bars[T_S_FULL + i]);
+                if (!two_u || i == 1) mma_commit(&bars[T_K_EMPTY + (j & 1)]);
             };
-            auto issue_pv = [&](int v) {
-                const int i = v & 1, n = (v >> 1) & 1, j = tile_of(v);
-                const uint32_t d = tm + 256u + static_cast<uint32_t>(D) * i, pa = tm + 128u * i + kUnit * n;
-                const uint32_t vb = v_lo + ((j & 1) ? Lay::kTile >> 4 : 0u) + (half_of(v) ? D * 128 >> 4 : 0u);
-                mma_f16_ts_at<0, 0>(d, pa, vb, hi, idesc_pv, v > 1);
+            auto issue_pv = [&](int u) {
+                const int i = u & 1, j = two_u ? u >> 1 : u;
+                const uint32_t d = tmem + 256u + static_cast<uint32_t>(D) * i, pa = tmem + 128u * i;
+                const uint32_t vb = v_lo + ((j & 1) ? Lay::kTile >> 4 : 0u);
+                constexpr uint32_t H = D * 128 / 16;  // the second 64 tokens
+                mma_f16_ts_at<0, 0>(d, pa, vb, hi, idesc_pv, u > 1);
                 mma_f16_ts_at<8, 2>(d, pa, vb, hi, idesc_pv, 1);
                 mma_f16_ts_at<16, 4>(d, pa, vb, hi, idesc_pv, 1);
                 mma_f16_ts_at<24, 6>(d, pa, vb, hi, idesc_pv, 1);
-                mma_commit(&bars[T_O_READY + 2 * i + n]);
-                if (last_of(v)) mma_commit(&bars[T_V_EMPTY + (j & 1)]);
+                mma_f16_ts_at<32, H>(d, pa, vb, hi, idesc_pv, 1);
+                mma_f16_ts_at<40, H + 2>(d, pa, vb, hi, idesc_pv, 1);
+                mma_f16_ts_at<48, H + 4>(d, pa, vb, hi, idesc_pv, 1);
+                mma_f16_ts_at<56, H + 6>(d, pa, vb, hi, idesc_pv, 1);
+                if (!two_u || i == 1) mma_commit(&bars[T_V_EMPTY + (j & 1)]);
             };
             bool ok = true;
-            if (warp == 0) {
-                // S of each unit, once the product that read P from its place has finished
 #pragma unroll 1
-                for (int v = 0; v < U_u && ok; ++v) {
-                    const int j = tile_of(v);
-                    if (first_of(v)) ok = warp_wait(&bars[T_K_FULL + (j & 1)], (j >> 1) & 1, ab, kDevTimeoutMma);
-                    if (v >= 4)
-                        ok = ok && warp_wait(&bars[T_O_READY + 2 * (v & 1) + ((v >> 1) & 1)], ((v >> 2) & 1) ^ 1, ab, kDevTimeoutMma);
-                    tc_fence_after();
-                    if (ok && elect_one()) issue_qk(v);
-                    __syncwarp();
-                }
-            } else {
-                // O of each unit, once its weights are there
+            for (int u = 0; u < 2 && u < U_u; ++u) {
+                ok = ok && warp_wait(&bars[T_K_FULL + ((two_u ? 0 : u) & 1)], 0, ab, kDevTimeoutMma);
+                tc_fence_after();
+                if (ok && elect_one()) issue_qk(u);
+                __syncwarp();
+            }
+            // every unit passes its rendezvous, also after an abort, so no partner is left waiting
 #pragma unroll 1
-                for (int v = 0; v < U_u && ok; ++v) {
-                    const int j = tile_of(v);
-                    if (first_of(v)) ok = warp_wait(&bars[T_V_FULL + (j & 1)], (j >> 1) & 1, ab, kDevTimeoutMma);
-                    ok = ok && warp_wait(&bars[T_P_FULL + 2 * (v & 1) + ((v >> 1) & 1)], (v >> 2) & 1, ab, kDevTimeoutMma);
-                    tc_fence_after();
-                    if (ok && elect_one()) issue_pv(v);
-                    __syncwarp();
+            for (int u = 0; u < U_u; ++u) {
+                ok = named_barrier_and(kNbUnit + (u & 1), kNbUnitThreads, ok);
+                tc_fence_after();
+                if (ok && elect_one()) {
+                    issue_pv(u);
+                    if (u + 2 < U_u) issue_qk(u + 2);
                 }
+                __syncwarp();
             }
             // (the lane that issued the products commits them)
             if (elect_one()) {
-                if (ok && warp == 3) mma_commit(&bars[T_O_DONE]);
+                if (ok) mma_commit(&bars[T_O_DONE]);
                 // every product has finished before the tensor memory is released
                 mma_commit(&bars[T_DRAIN]);
             }
@@ -266,42 +249,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             const uint64_t t0 = global_timer_ns();
             while (!mbar_try_wait(&bars[T_DRAIN], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
-        } else if (warp == 2) {
-            // -------------------------------------------------------- marks
-            // A V row that is not a number (scale byte over 134) counts as 0 in
-            // the product, and the rows that see it are marked: whether a tile
-            // has one is known before its scores are.  Four tokens a lane.
-            // Slot j & 7: the softmax of tile j - 8 has read it (when K's buffer
-            // is free for tile j, the last S of tile j - 2 has been computed,
-            // which came after the weights of tile j - 4 or a later one).
-            bool ok = true;
-            auto fetch = [&](int j) {
-                const int t = j0 + j * kTileN + 4 * lane;
-                if (j >= T || t >= q.kv) return 0u;
-                const int page = __ldg(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages + (t >> p.g.page_shift));
-                if (page < 0 || page >= p.g.pages) return 0u;  // (flagged by the converters)
-                const size_t at = ((static_cast<size_t>(page) * p.g.kv_heads + h) << p.g.page_shift) +
-                                  (t & ((1 << p.g.page_shift) - 1));
-                const uint32_t v = ldg_early(reinterpret_cast<const uint32_t*>(p.g.vscale + at));
-                const int left = q.kv - t;
-                return left >= 4 ? v : v & ((1u << (8 * left)) - 1u);
-            };
-            uint32_t v = fetch(0);
-#pragma unroll 1
-            for (int j = 0; j < T; ++j) {
-                const bool bad = __any_sync(0xffffffffu, __vcmpgtu4(v, 0x86868686u) != 0u);
-                ok = ok && warp_wait(&bars[T_K_EMPTY + (j & 1)], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
-                if (!ok) break;
-                if (bad) *reinterpret_cast<uint32_t*>(smem + Lay::kScale + (j & 7) * kTileN + 4 * lane) = v;
-                if (lane == 0) misc[4 + (j & 7)] = bad ? 1u : 0u;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[T_K_FULL + (j & 1)]);
-                v = fetch(j + 1);
-            }
         }
     } else if (wg < kWgConvertK) {
         // ------------------------------------------------------------ softmax
-        regs_inc<144>();
+        regs_inc<168>();
         const int i = wg - kWgSoftmax0;
         const int quad = warp & 3, r = quad * 32 + lane;  // TMEM lane quadrant; row within the group's tile
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
@@ -313,22 +264,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
         // tokens the row sees, counted from j0; rows past the end see all (nothing of theirs is stored)
         const int limit = (!live || !p.causal ? j1 : min(j1, max(0, q.kv - q.n + tok + 1))) - j0;
         const float a = p.sm_log2;
+        const float2 a2 = make_float2(a, a);
         float m_run = -INFINITY, l_run = 0.f;
         bool poison = false;  // a token whose V is not a number is seen
         bool ok = true;
+        const bool checker = quad == 0 && lane == 0;
 
-        // unit n of the group, at place n & 1
-        auto unit = [&](int n) -> bool {
-            const int j = two ? n >> 1 : n, half = two ? n & 1 : i;
-            const uint32_t at = s_tm + kUnit * (n & 1);
-            if (!warp_wait(&bars[T_S_FULL + 2 * i + (n & 1)], (n >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
+        auto unit = [&](int u) -> bool {
+            const int j = tile_of(u);
+            // V of this unit and K of unit u + 2, tested now and looked at after the softmax
+            const int jk = tile_of(u + 2);
+            const bool want_k = u + 2 < U;
+            bool vk = true;
+            if (checker) {
+                vk = mbar_test(&bars[T_V_FULL + (j & 1)], (j >> 1) & 1);
+                if (want_k) vk = mbar_test(&bars[T_K_FULL + (jk & 1)], (jk >> 1) & 1) && vk;
+            }
+            if (!warp_wait(&bars[T_S_FULL + i], (u >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
             tc_fence_after();
-            const int room = limit - j * kTileN - half * kUnit;  // columns the row sees
-            uint32_t v[kUnit];
-            tmem_ld64(at, v);
-            if (!__all_sync(0xffffffffu, room >= kUnit)) {
+            const int room = limit - j * kTileN;  // columns the row sees
+            uint32_t v[128];
+            tmem_ld128(s_tm, v);
+            if (!__all_sync(0xffffffffu, room >= kTileN)) {
 #pragma unroll
-                for (int k = 0; k < kUnit; ++k)
+                for (int k = 0; k < kTileN; ++k)
                     if (k >= room) v[k] = 0xff800000u;
             }
             float mx[4];
@@ -336,66 +295,67 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             for (int c = 0; c < 4; ++c) {
                 mx[c] = fmaxf(__uint_as_float(v[c]), __uint_as_float(v[4 + c]));
 #pragma unroll
-                for (int k = 8; k < kUnit; k += 8)
+                for (int k = 8; k < kTileN; k += 8)
                     mx[c] = max3(mx[c], __uint_as_float(v[k + c]), __uint_as_float(v[k + 4 + c]));
             }
             const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a;
-            // the running max moves only when a unit raises it by more than
+            // the running max moves only when a tile raises it by more than
             // 2^8 of weight: bf16 and fp32 hold the larger weights as well
             const bool bump = (m_run == -INFINITY) || (m_tile > m_run + 8.f);
             const float m_new = bump ? fmaxf(m_run, m_tile) : m_run;
             const float base = (m_new == -INFINITY) ? 0.f : m_new;
             const float alpha = bump ? ex2(m_run - base) : 1.f;
-            const float2 a2 = make_float2(a, a), n2 = make_float2(-base, -base);
-            float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            uint32_t pk[kUnit / 2];
+            const float2 n2 = make_float2(-base, -base);
+            float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < kUnit; c += 32) {
-                // 32 columns in stages, so that many values are in flight
-                float2 x[16];
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pk[32];
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    x[k] = fma2(make_float2(__uint_as_float(v[c + 2 * k]), __uint_as_float(v[c + 2 * k + 1])), a2, n2);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] = make_float2(ex2(x[k].x), ex2(x[k].y));
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                    ls[k & 3] = add2(ls[k & 3], x[k]);
-                    ls[(k + 1) & 3] = add2(ls[(k + 1) & 3], x[k + 1]);
-                    pk[c / 2 + k] = pack_bf16(x[k].x, x[k + 1].x);      // tokens 0, 2
-                    pk[c / 2 + k + 1] = pack_bf16(x[k].y, x[k + 1].y);  // tokens 1, 3
+                for (int k = 0; k < 64; k += 4) {
+                    const uint32_t* w = v + 64 * half + k;
+                    const float2 x0 = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), a2, n2);
+                    const float2 x1 = fma2(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), a2, n2);
+                    const float2 q0 = make_float2(ex2(x0.x), ex2(x0.y));
+                    const float2 q1 = make_float2(ex2(x1.x), ex2(x1.y));
+                    ls0 = add2(ls0, q0);
+                    ls1 = add2(ls1, q1);
+                    pk[k / 2] = pack_bf16(q0.x, q1.x);      // tokens 0, 2
+                    pk[k / 2 + 1] = pack_bf16(q0.y, q1.y);  // tokens 1, 3
                 }
+                tmem_st32(s_tm + 32 * half, pk);
             }
-            tmem_st32(at, pk);
-            if (misc[4 + (j & 7)] != 0u) {
-                const uint8_t* vs = smem + Lay::kScale + (j & 7) * kTileN + half * kUnit;
-                for (int k = 0; k < kUnit; ++k) poison |= vs[k] > 134 && k < room;
+            if (misc[4 + (j & 3)] != 0u) {
+                const uint8_t* vs = smem + Lay::kScale + (j & 3) * kTileN;
+                for (int k = 0; k < kTileN; ++k) poison |= vs[k] > 134 && k < room;
             }
-            // rescale the running output when the max moved, once the group's
-            // product before this one has finished
-            if (__any_sync(0xffffffffu, n > 0 && alpha != 1.f)) {
-                if (!warp_wait(&bars[T_O_READY + 2 * i + ((n - 1) & 1)], ((n - 1) >> 1) & 1, ab, kDevTimeoutSoftmax))
-                    return false;
-                tc_fence_after();
+            tmem_st_wait();
+            // rescale the running output when the max moved (the product of
+            // unit u - 2 has finished: S of this unit came after it)
+            if (__any_sync(0xffffffffu, u > 1 && alpha != 1.f)) {
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
-                    uint32_t w[32];
-                    tmem_ld32(o_tm + 32 * c, w);
+                    uint32_t v[32];
+                    tmem_ld32(o_tm + 32 * c, v);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
-                    tmem_st32(o_tm + 32 * c, w);
+                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+                    tmem_st32(o_tm + 32 * c, v);
                 }
+                tmem_st_wait();
             }
-            ls[0] = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
-            l_run = l_run * alpha + (ls[0].x + ls[0].y);
+            l_run = l_run * alpha + ((ls0.x + ls0.y) + (ls1.x + ls1.y));
             m_run = m_new;
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[T_P_FULL + 2 * i + (n & 1)]);
+            if (checker && !vk) {
+                if (!mbar_wait(&bars[T_V_FULL + (j & 1)], (j >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
+                if (want_k && !mbar_wait(&bars[T_K_FULL + (jk & 1)], (jk >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
+            }
             return true;
         };
-        for (int n = 0; n < U / 2 && ok; ++n) ok = unit(n);
+        for (int u = i; u < U; u += 2) {
+            if (ok) ok = unit(u);
+            tc_fence_before();
+            __syncwarp();
+            ok = named_barrier_and(kNbUnit + i, kNbUnitThreads, ok);
+        }
         // ------------------------------------------------------------ epilogue
         if (ok && U > 0) ok = warp_wait(&bars[T_O_DONE], 0, ab, kDevTimeoutEpilogue);
         tc_fence_after();
@@ -509,7 +469,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
         // K's columns, and V's get the scale byte 0 (a finite factor), as P is 0 there.
         // Neighbouring groups of four lanes have neighbouring rows, whose
         // swizzles differ in the lowest bit: the stores meet no bank conflict.
-        regs_dec<72>();
+        regs_dec<56>();
         const int ct = tid & 127;
         const int pb = p.g.page_shift - 4;  // blocks of a page: 1 << pb
         bool ok = true;
@@ -542,6 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             const uint8_t* sbase = p.g.kscale + (rr & 15);
             uint4 kr[KU];
             uint32_t ks[4];
+            uint4 vs = make_uint4(0, 0, 0, 0);  // V scale bytes of the lane's block: only looked at
             // rows rr + 32 m of tile j, whose block is `blk` of lane (rr >> 4) + 2 m
             auto fetch = [&](int m, uint32_t blk) {
                 const uint64_t at = __shfl_sync(0xffffffffu, blk, (rr >> 4) + 2 * m);
@@ -549,11 +510,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                 for (int n = 0; n < NB; ++n) kr[m * NB + n] = ldg_nc_na_v4(kbase + at * (16 * D) + 64 * n);
                 ks[m] = ldg_early(sbase + at * 16);
             };
+            auto fetch_vs = [&](uint32_t blk) {
+                if (ct < 8) vs = ldg_nc_na_v4(p.g.vscale + static_cast<uint64_t>(blk) * 16);
+            };
             int ahead = entry_at(1);
             if (T > 0) {
                 const uint32_t blk = block_of(0, entry_at(0));
 #pragma unroll
                 for (int m = 0; m < 4; ++m) fetch(m, blk);
+                fetch_vs(blk);
             }
             for (int j = 0; j < T; ++j) {
                 const int st = j & 1;
@@ -561,6 +526,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                 ahead = entry_at(j + 2);
                 if (ok) ok = warp_wait(&bars[T_K_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
                 if (!ok) continue;
+                // A V row that is not a number (scale byte over 134) counts as
+                // 0 in the product; the rows that see it are marked.  Slot
+                // j & 3: the softmax of tile j - 4 has read it (the S whose end
+                // freed this buffer came after that).
+                if (warp == kWgConvertK * 4) {
+                    const uint4 cut = cut16(vs, q.kv - (j0 + j * kTileN + 16 * lane));
+                    if (lane < 8) *reinterpret_cast<uint4*>(smem + Lay::kScale + (j & 3) * kTileN + 16 * lane) = cut;
+                    const bool bad =
+                        __any_sync(0xffffffffu, lane < 8 && (__vcmpgtu4(cut.x, 0x86868686u) | __vcmpgtu4(cut.y, 0x86868686u) |
+                                                             __vcmpgtu4(cut.z, 0x86868686u) | __vcmpgtu4(cut.w, 0x86868686u)) != 0u);
+                    if (lane == 0) misc[4 + (j & 3)] = bad ? 1u : 0u;
+                }
+                fetch_vs(blk);
                 uint8_t* dst = smem + Lay::kK + st * Lay::kTile;
                 uint8_t* lo = dst + bktile_off(rr, 16 * (ct & 3));
                 uint8_t* hi = dst + bktile_off(rr, 16 * (ct & 3) + 8);
