@@ -132,6 +132,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+// 16 codes as bf16, in the order (0, 2), (1, 3) of each four, with the factors
+// of the pairs.
+__device__ __forceinline__ void put16(uint8_t* lo, uint8_t* hi, const uint4& w, const uint32_t (&f)[8]) {
+    *reinterpret_cast<uint4*>(lo) = make_uint4(bf2_mul(codes02(w.x), f[0]), bf2_mul(codes13(w.x), f[1]),
+                                               bf2_mul(codes02(w.y), f[2]), bf2_mul(codes13(w.y), f[3]));
+    *reinterpret_cast<uint4*>(hi) = make_uint4(bf2_mul(codes02(w.z), f[4]), bf2_mul(codes13(w.z), f[5]),
+                                               bf2_mul(codes02(w.w), f[6]), bf2_mul(codes13(w.w), f[7]));
+}
+
 // E8M0 byte of a row's scale from its largest magnitude: the smallest e with
 // amax <= 448 * 2^e = 1.75 * 2^(e + 8), cut to -124 .. 7; 0 for a row of zeros.
 __device__ __forceinline__ int scale_exponent(float amax) {
@@ -215,6 +224,7 @@ cudaError_t launch_paged_write(const PagedWriteParams& p, int D, cudaStream_t s)
 cudaError_t launch_paged_attention(PagedAttnParams& p, int D, size_t part_floats, int max_counters, cudaStream_t s);
 cudaError_t launch_paged_tc(PagedAttnParams& p, int D, size_t part_floats, cudaStream_t s);
 cudaError_t launch_paged_scores(const PagedScoreParams& p, int D, cudaStream_t s);
+cudaError_t launch_paged_scores_tc(const PagedScoreParams& p, int D, cudaStream_t s);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int D, cudaStream_t s);
 
 }  // namespace rc

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kScoreWarps = 4;
 constexpr int kScoreTokens = 32;  // of a warp
+constexpr int kScoreRowsMax = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_rows_kernel(PagedScoreParams p) {
@@ -124,6 +125,9 @@ cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_paged_scores(const PagedScoreParams& p, int D, cudaStream_t s) {
+    // up to a few row tiles the warps' own products keep up with the reading of
+    // the codes; with more rows the tensor cores' do
+    if (static_cast<int64_t>(p.g.max_new) * p.group > kScoreRowsMax) return launch_paged_scores_tc(p, D, s);
     return D == 128 ? launch_d<128>(p, s) : launch_d<64>(p, s);
 }
 

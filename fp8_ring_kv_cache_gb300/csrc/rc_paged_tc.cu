@@ -487,13 +487,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             const uint32_t at = static_cast<uint32_t>(check_page(p.g, page) ? page : 0) * p.g.kv_heads + h;
             return (at << pb) + (static_cast<uint32_t>(t >> 4) & ((1u << pb) - 1u));
         };
-        // 16 codes as bf16, in the order (0, 2), (1, 3) of each four
-        auto put = [&](uint8_t* lo, uint8_t* hi, const uint4& w, const uint32_t (&f)[8]) {
-            *reinterpret_cast<uint4*>(lo) = make_uint4(bf2_mul(codes02(w.x), f[0]), bf2_mul(codes13(w.x), f[1]),
-                                                       bf2_mul(codes02(w.y), f[2]), bf2_mul(codes13(w.y), f[3]));
-            *reinterpret_cast<uint4*>(hi) = make_uint4(bf2_mul(codes02(w.z), f[4]), bf2_mul(codes13(w.z), f[5]),
-                                                       bf2_mul(codes02(w.w), f[6]), bf2_mul(codes13(w.w), f[7]));
-        };
         if (wg == kWgConvertK) {
             // unit k: row rr + 32 (k / NB), dims 64 (k % NB) + 16 (ct % 4) ..
             constexpr int NB = D / 64, KU = 4 * NB;
@@ -549,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
                         const int off = n * (kTileN * 128) + m * (32 * 128);
-                        put(lo + off, hi + off, kr[m * NB + n], f);
+                        put16(lo + off, hi + off, kr[m * NB + n], f);
                     }
                     fetch(m, blk);  // the next tile's rows, into the registers just freed
                 }
@@ -601,7 +594,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                 uint8_t* hi = dst + bvtile_off(d0, 16 * c + 8, D);
 #pragma unroll
                 for (int k = 0; k < VU; ++k) {
-                    put(lo + 16 * 128 * k, hi + 16 * 128 * k, vr[k], f);
+                    put16(lo + 16 * 128 * k, hi + 16 * 128 * k, vr[k], f);
                     vr[k] = ldg_nc_na_v4(src + k * step);  // the next tile's, into the registers just freed
                 }
                 fence_async_smem();
