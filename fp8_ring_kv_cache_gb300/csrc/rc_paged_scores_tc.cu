@@ -6,14 +6,18 @@
 // threads add to one entry.  A block has a range of the cached tokens of one
 // (sequence, KV head) and goes over the head's query rows in blocks of up to
 // 384, which stay in shared memory as three tiles while the cached tokens stream
-// past, two tiles of 128 at a time (one for each group of four warps):
-//   warp 0         issues the products (one lane) and owns TMEM: four places of
-//                  128 x 128 scores, two a group, so that the products of a
-//                  group's next tile run while it sums this one
-//   warps 4 .. 11  groups 0 and 1: exp2(S c - lse) and the sum over the columns
-//   warps 12 .. 19 read K's codes from the pages (a pair of tiles ahead, in
-//                  registers), make them bf16 operand tiles (two pairs of
-//                  buffers), and bring the query rows
+// past, in pairs of tiles of 128:
+//   warps 0, 1     issue the products of groups 0 and 1 (one lane each); warp 0
+//                  owns TMEM: 256 x 128 scores a group
+//   warps 4 .. 11  groups 0 and 1: exp2(S c - lse) and the sum over the columns.
+//                  They take the pairs in turn, so that one group's products run
+//                  while the other sums, and a thread has a token of each tile of
+//                  the pair: each query's lse is read from shared memory for two
+//                  (that reading fills the pipe that feeds the products; with one
+//                  token a thread the sums took twice as long)
+//   warps 12 .. 15 read K's codes from the pages (a pair of tiles ahead, in
+//                  registers), make them bf16 operand tiles, and bring the
+//                  query rows
 // With the queries kept, K is read and converted once per 384 rows, and the
 // queries once per block: keeping K instead would read them for every 128
 // tokens (430 MB of cache traffic for 757 x 5,788 tokens x 48 heads).
@@ -25,20 +29,23 @@ namespace rc {
 
 namespace {
 
-constexpr int kStThreads = 640;
+// 512 threads launched with 128 registers each; the warpgroups share them
+// 40 + 2 x 168 + 136 (a spilled register would come back from the L2 cache:
+// next to 227 KB of shared memory little is left of L1).
+constexpr int kStThreads = 512;
 constexpr int kStTile = 128;
 constexpr int kStQTiles = 3;  // query tiles in shared memory
-constexpr int kStConvert = 256;
+constexpr int kStConvert = 128;
 
 enum : int {
-    S_K_FULL = 0,    // [4] buffer 2 (tile of the group & 1) + group: K tile converted
+    S_K_FULL = 0,    // [4] buffer 2 group + tile of the pair: K tile converted
     S_K_EMPTY = 4,   // [4] its products have finished
-    S_S_FULL = 8,    // [4] place 2 group + (unit & 1): scores in TMEM
-    S_S_FREE = 12,   // [4] the group has read them
-    S_Q_FULL = 16,   // the block's query rows are in place
-    S_Q_EMPTY = 17,  // products and groups are done with them
-    S_DRAIN = 18,
-    S_COUNT = 19
+    S_S_FULL = 8,    // [group] scores of the pair and a query tile in TMEM
+    S_S_FREE = 10,   // [group] the group has read them
+    S_Q_FULL = 12,   // the block's query rows are in place
+    S_Q_EMPTY = 13,  // products and groups are done with them
+    S_DRAIN = 14,
+    S_COUNT = 15
 };
 
 template <int D>
@@ -112,14 +119,16 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
 
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&bars[S_K_FULL + i], 8);
+            mbar_init(&bars[S_K_FULL + i], 4);
             mbar_init(&bars[S_K_EMPTY + i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[S_S_FULL + i], 1);
             mbar_init(&bars[S_S_FREE + i], 4);
         }
-        mbar_init(&bars[S_Q_FULL], 8);
-        mbar_init(&bars[S_Q_EMPTY], 1 + 8);
-        mbar_init(&bars[S_DRAIN], 1);
+        mbar_init(&bars[S_Q_FULL], 4);
+        mbar_init(&bars[S_Q_EMPTY], 2 + 8);
+        mbar_init(&bars[S_DRAIN], 2);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -132,149 +141,172 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
     tc_fence_after();
     const uint32_t tmem = misc[0];
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ products
-        const uint32_t idesc = instr_desc(kFmtBF16, kFmtBF16, 128, 128);
-        const uint64_t dk = smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2);
-        const uint32_t hi = static_cast<uint32_t>(dk >> 32), k_lo = static_cast<uint32_t>(dk);
-        const uint32_t q_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2));
-        bool ok = true;
-        int kc[2] = {0, 0}, uc[2] = {0, 0};  // K tiles, units of each group so far
-        for (int rb = 0; rb < w.blocks && ok; ++rb) {
-            ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutMma);
-            for (int pair = 0; pair < w.pairs && ok; ++pair) {
-                if (!w.has(rb, pair)) continue;
-                const int q0 = w.first_tile(rb, pair), q1 = w.end_tile(rb), groups = w.second(pair) ? 2 : 1;
-                for (int g = 0; g < groups && ok; ++g)
-                    ok = warp_wait(&bars[S_K_FULL + 2 * (kc[g] & 1) + g], (kc[g] >> 1) & 1, ab, kDevTimeoutMma);
-                for (int t = q0; t < q1 && ok; ++t)
-                    for (int g = 0; g < groups && ok; ++g) {
-                        const int n = g == 0 ? uc[0]++ : uc[1]++, place = 2 * g + (n & 1);
-                        ok = warp_wait(&bars[S_S_FREE + place], ((n >> 1) & 1) ^ 1, ab, kDevTimeoutMma);
+    if (wg == 0) {
+        regs_dec<40>();
+        if (warp < 2) {
+            // -------------------------------------------------------- products
+            const int g = warp;
+            const uint32_t idesc = instr_desc(kFmtBF16, kFmtBF16, 128, 128);
+            const uint64_t dk = smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2);
+            const uint32_t hi = static_cast<uint32_t>(dk >> 32), k_lo = static_cast<uint32_t>(dk);
+            const uint32_t q_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2));
+            bool ok = true;
+            // pairs of all groups; first, second K tiles and units of this one
+            int pc = 0, ka_count = 0, kb_count = 0, uc = 0;
+            for (int rb = 0; rb < w.blocks && ok; ++rb) {
+                ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutMma);
+                for (int pair = 0; pair < w.pairs && ok; ++pair) {
+                    if (!w.has(rb, pair) || (pc++ & 1) != g) continue;
+                    const int q0 = w.first_tile(rb, pair), q1 = w.end_tile(rb), tiles = w.second(pair) ? 2 : 1;
+                    ok = warp_wait(&bars[S_K_FULL + 2 * g], ka_count++ & 1, ab, kDevTimeoutMma);
+                    if (ok && tiles == 2) ok = warp_wait(&bars[S_K_FULL + 2 * g + 1], kb_count++ & 1, ab, kDevTimeoutMma);
+                    for (int t = q0; t < q1 && ok; ++t, ++uc) {
+                        ok = warp_wait(&bars[S_S_FREE + g], (uc & 1) ^ 1, ab, kDevTimeoutMma);
                         tc_fence_after();
-                        const int buf = 2 * (kc[g] & 1) + g;
                         if (ok && elect_one()) {
-                            const uint32_t d = tmem + 128u * place;
-                            const uint32_t ka = k_lo + buf * (Lay::kTile >> 4);
                             const uint32_t qb = q_lo + (t - rb * w.per) * (Lay::kTile >> 4);
-                            mma_f16_ss_at<0, 0>(d, ka, qb, hi, idesc, 0);
-                            mma_f16_ss_at<2, 2>(d, ka, qb, hi, idesc, 1);
-                            mma_f16_ss_at<4, 4>(d, ka, qb, hi, idesc, 1);
-                            mma_f16_ss_at<6, 6>(d, ka, qb, hi, idesc, 1);
-                            if (D == 128) {
-                                mma_f16_ss_at<1024, 1024>(d, ka, qb, hi, idesc, 1);
-                                mma_f16_ss_at<1026, 1026>(d, ka, qb, hi, idesc, 1);
-                                mma_f16_ss_at<1028, 1028>(d, ka, qb, hi, idesc, 1);
-                                mma_f16_ss_at<1030, 1030>(d, ka, qb, hi, idesc, 1);
+                            for (int a = 0; a < tiles; ++a) {
+                                const uint32_t d = tmem + 256u * g + 128u * a;
+                                const uint32_t ka = k_lo + (2 * g + a) * (Lay::kTile >> 4);
+                                mma_f16_ss_at<0, 0>(d, ka, qb, hi, idesc, 0);
+                                mma_f16_ss_at<2, 2>(d, ka, qb, hi, idesc, 1);
+                                mma_f16_ss_at<4, 4>(d, ka, qb, hi, idesc, 1);
+                                mma_f16_ss_at<6, 6>(d, ka, qb, hi, idesc, 1);
+                                if (D == 128) {
+                                    mma_f16_ss_at<1024, 1024>(d, ka, qb, hi, idesc, 1);
+                                    mma_f16_ss_at<1026, 1026>(d, ka, qb, hi, idesc, 1);
+                                    mma_f16_ss_at<1028, 1028>(d, ka, qb, hi, idesc, 1);
+                                    mma_f16_ss_at<1030, 1030>(d, ka, qb, hi, idesc, 1);
+                                }
+                                if (t + 1 == q1) mma_commit(&bars[S_K_EMPTY + 2 * g + a]);
                             }
-                            mma_commit(&bars[S_S_FULL + place]);
-                            if (t + 1 == q1) mma_commit(&bars[S_K_EMPTY + buf]);
+                            mma_commit(&bars[S_S_FULL + g]);
                         }
                         __syncwarp();
                     }
-                ++kc[0];
-                kc[1] += groups - 1;
+                }
+                if (elect_one()) mma_commit(&bars[S_Q_EMPTY]);
+                __syncwarp();
             }
-            if (elect_one()) mma_commit(&bars[S_Q_EMPTY]);
+            // every product has finished before the tensor memory is released
+            if (elect_one()) mma_commit(&bars[S_DRAIN]);
             __syncwarp();
-        }
-        // every product has finished before the tensor memory is released
-        if (elect_one()) mma_commit(&bars[S_DRAIN]);
-        __syncwarp();
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&bars[S_DRAIN], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(&bars[S_DRAIN], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+            }
         }
     } else if (wg == 1 || wg == 2) {
         // ------------------------------------------------------------ sums
+        regs_inc<168>();
         const int g = wg - 1, quad = warp & 3, r = quad * 32 + lane;
-        const uint32_t at0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 256u * g;
-        const float c = p.sm_log2;
-        const float2 c2 = make_float2(c, c);
+        const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 256u * g;
+        const float2 c2 = make_float2(p.sm_log2, p.sm_log2);
         const float* minus = reinterpret_cast<const float*>(smem + Lay::kMinus);
-        int n = 0;  // units so far
+        int pc = 0, n = 0;  // pairs of all groups, units of this one
         bool ok = true;
         for (int rb = 0; rb < w.blocks && ok; ++rb) {
             // (lse of the rows: written with the query tiles)
             ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutSoftmax);
             for (int pair = 0; pair < w.pairs && ok; ++pair) {
-                const int j = j0 + (2 * pair + g) * kStTile + r;  // the thread's token
-                const bool mine = j < stop;
-                if (!w.has(rb, pair) || (g == 1 && !w.second(pair))) {
-                    // no row of any block sees the pair, or its second tile is empty
-                    if (rb == 0 && (w.first_row(j0 + pair * 2 * kStTile) >= w.rows || (g == 1 && !w.second(pair))) && mine)
-                        p.out[row_at + j] = p.scores[row_at + j];
+                const int jp = j0 + pair * 2 * kStTile;
+                // the thread's tokens, one of each tile
+                const int ja = jp + r, jb = ja + kStTile;
+                if (!w.has(rb, pair)) {
+                    if (rb == 0 && g == 0 && w.first_row(jp) >= w.rows) {  // no row sees the pair
+                        if (ja < stop) p.out[row_at + ja] = p.scores[row_at + ja];
+                        if (jb < stop) p.out[row_at + jb] = p.scores[row_at + jb];
+                    }
                     continue;
                 }
+                if ((pc++ & 1) != g) continue;
                 const int q0 = w.first_tile(rb, pair), q1 = w.end_tile(rb);
-                const int first = w.first_row(j);  // the first row that sees the token
-                float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                for (int t = q0; t < q1 && ok; ++t, ++n) {
-                    ok = warp_wait(&bars[S_S_FULL + 2 * g + (n & 1)], (n >> 1) & 1, ab, kDevTimeoutSoftmax);
+                const int fa = w.first_row(ja), fb = w.first_row(jb);  // the first rows that see the tokens
+                float2 sa[4], sb[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sa[k] = sb[k] = make_float2(0.f, 0.f);
+                for (int t = q0; t < q1; ++t, ++n) {
+                    ok = warp_wait(&bars[S_S_FULL + g], n & 1, ab, kDevTimeoutSoftmax);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t at = at0 + 128u * (n & 1);
                     const float* mt = minus + (t - rb * w.per) * kStTile;
-                    // columns of the tile that count: rows [first, rows)
-                    const int lo = first - t * kStTile, hi = w.rows - t * kStTile;
-                    const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= kStTile);
-                    uint32_t va[32], vb[32];
-                    auto add = [&](uint32_t (&v)[32], int c0) {
+                    // columns from these on count (rows past the last have a factor of 0)
+                    const int la = fa - t * kStTile, lb = fb - t * kStTile;
+                    const bool full = __all_sync(0xffffffffu, la <= 0 && lb <= 0);
+                    auto add = [&](uint32_t (&v)[16], const float2 (&m)[8], int c0, float2 (&acc)[4], int lo) {
+                        float2 x[8];
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(mt + c0 + k);
-                            const float2 x0 = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2,
-                                                   make_float2(m.x, m.y));
-                            const float2 x1 = fma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), c2,
-                                                   make_float2(m.z, m.w));
-                            v[k] = __float_as_uint(ex2(x0.x));
-                            v[k + 1] = __float_as_uint(ex2(x0.y));
-                            v[k + 2] = __float_as_uint(ex2(x1.x));
-                            v[k + 3] = __float_as_uint(ex2(x1.y));
-                        }
+                        for (int k = 0; k < 8; ++k)
+                            x[k] = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, m[k]);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = make_float2(ex2(x[k].x), ex2(x[k].y));
                         if (!full) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (c0 + k < lo || c0 + k >= hi) v[k] = 0u;
+                            for (int k = 0; k < 8; ++k) {
+                                if (c0 + 2 * k < lo) x[k].x = 0.f;
+                                if (c0 + 2 * k + 1 < lo) x[k].y = 0.f;
+                            }
                         }
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2)
-                            acc[(k >> 1) & 3] =
-                                add2(acc[(k >> 1) & 3], make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                        for (int k = 0; k < 8; ++k) acc[k & 3] = add2(acc[k & 3], x[k]);
                     };
-                    tmem_ld32_async(at, va);
+                    // 16 columns of both tokens while the next are on their way
+                    // (the second tile's place is read also where the pair has no
+                    // second tile: its sums are not stored)
+                    uint32_t va[16], vb[16], wa[16], wb[16];
+                    auto both = [&](uint32_t (&x)[16], uint32_t (&y)[16], int c0) {
+                        float2 m[8];
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2) {
+                            const float4 f = *reinterpret_cast<const float4*>(mt + c0 + 2 * k);
+                            m[k] = make_float2(f.x, f.y);
+                            m[k + 1] = make_float2(f.z, f.w);
+                        }
+                        add(x, m, c0, sa, la);
+                        add(y, m, c0, sb, lb);
+                    };
+                    tmem_ld16_async(at, va);
+                    tmem_ld16_async(at + 128, vb);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kStTile; c0 += 64) {
+                    for (int c0 = 0; c0 < kStTile; c0 += 32) {
                         tmem_wait_ld_dep(va);
-                        tmem_ld32_async(at + c0 + 32, vb);
-                        add(va, c0);
                         tmem_wait_ld_dep(vb);
-                        if (c0 + 64 < kStTile) tmem_ld32_async(at + c0 + 64, va);
-                        if (c0 + 64 == kStTile) {
+                        tmem_ld16_async(at + c0 + 16, wa);
+                        tmem_ld16_async(at + 128 + c0 + 16, wb);
+                        both(va, vb, c0);
+                        tmem_wait_ld_dep(wa);
+                        tmem_wait_ld_dep(wb);
+                        if (c0 + 32 < kStTile) {
+                            tmem_ld16_async(at + c0 + 32, va);
+                            tmem_ld16_async(at + 128 + c0 + 32, vb);
+                        } else {
                             // the scores are in registers: their place is free
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars[S_S_FREE + 2 * g + (n & 1)]);
+                            if (lane == 0) mbar_arrive(&bars[S_S_FREE + g]);
                         }
-                        add(vb, c0 + 32);
+                        both(wa, wb, c0 + 16);
                     }
                 }
                 if (!ok) break;
-                if (mine) {
-                    const float2 a = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
-                    // the first block of rows that sees the pair starts from the given scores
-                    const bool begin = rb == (w.first_row(j0 + pair * 2 * kStTile) / kStTile) / w.per;
-                    const float old = begin ? p.scores[row_at + j] : p.out[row_at + j];
-                    p.out[row_at + j] = old + (j < q.kv ? a.x + a.y : 0.f);
-                }
+                // the first block of rows that sees the pair starts from the given scores
+                const float* from = rb == w.first_row(jp) / kStTile / w.per ? p.scores : p.out;
+                auto store = [&](int j, const float2 (&acc)[4]) {
+                    if (j >= stop) return;
+                    const float2 x = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+                    p.out[row_at + j] = from[row_at + j] + (j < q.kv ? x.x + x.y : 0.f);
+                };
+                store(ja, sa);
+                store(jb, sb);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_Q_EMPTY]);
         }
-    } else if (wg >= 3) {
+    } else {
         // ------------------------------------------------------------ K and Q
         // Thread ct: the pieces of 16 dims ct % 4 (+ 4 in the second 64 dims) of
-        // the rows ct / 4 and ct / 4 + 64 of each tile.  Lane l < 16 of a warp
+        // the rows ct / 4 + 32 m of each tile.  Lane l < 16 of a warp
         // looks up the block of 16 tokens l of the pair.
+        regs_inc<136>();
         const int ct = tid - 3 * 128;
         constexpr int NB = D / 64;
         const int rr = ct >> 2, pb = p.g.page_shift - 4;
@@ -282,8 +314,8 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         const uint8_t* sbase = p.g.kscale + (rr & 15);
         const uint32_t* table =
             reinterpret_cast<const uint32_t*>(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages);
-        uint4 kr[2][2 * NB];
-        uint32_t ks[2][2];
+        uint4 kr[2][4 * NB];
+        uint32_t ks[2][4];
         // the next pair with work after (rb, pair); pair = -1 starts; rb = blocks ends
         auto advance = [&](int& rb, int& pair) {
             do {
@@ -306,14 +338,15 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         };
         auto fetch = [&](int g, uint32_t blk) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const uint64_t at = __shfl_sync(0xffffffffu, blk, 8 * g + (rr >> 4) + 4 * m);
+            for (int m = 0; m < 4; ++m) {
+                const uint64_t at = __shfl_sync(0xffffffffu, blk, 8 * g + (rr >> 4) + 2 * m);
 #pragma unroll
                 for (int x = 0; x < NB; ++x) kr[g][m * NB + x] = ldg_nc_na_v4(kbase + at * (16 * D) + 64 * x);
                 ks[g][m] = ldg_early(sbase + at * 16);
             }
         };
-        int rb = 0, pair = -1, kc[2] = {0, 0};
+        int rb = 0, pair = -1, pc = 0;
+        int uses[4] = {0, 0, 0, 0};  // of each buffer so far
         advance(rb, pair);
         int rb1 = rb, pair1 = pair;
         if (rb < w.blocks) {
@@ -333,25 +366,37 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 if (!ok) break;
                 constexpr int kPieces = D / 8;
                 const int first = loaded * w.per * kStTile, count = (w.end_tile(loaded) - loaded * w.per) * kStTile;
-                for (int u = ct; u < count * kPieces; u += kStConvert) {
-                    const int row = u / kPieces, c = u % kPieces, rw = first + row;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (rw < w.rows) {
-                        const int tok = rw / p.group, head = h * p.group + rw - tok * p.group;
-                        v = ldg_nc_na_v4(p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D +
-                                         8 * c);
+                // thread ct: piece ct % kPieces of the rows ct / kPieces + i kRows
+                constexpr int kRows = kStConvert / kPieces, kBatch = 8;  // rows a step, loads in flight
+                const int c = ct % kPieces;
+                for (int r0 = ct / kPieces; r0 < count; r0 += kBatch * kRows) {
+                    uint4 v[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int rw = first + r0 + i * kRows;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (r0 + i * kRows < count && rw < w.rows) {
+                            const int tok = p.group == 1 ? rw : rw / p.group, head = h * p.group + rw - tok * p.group;
+                            v[i] = ldg_nc_na_v4(p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride +
+                                                static_cast<int64_t>(head) * D + 8 * c);
+                        }
                     }
-                    *reinterpret_cast<uint4*>(smem + Lay::kQ + (row >> 7) * Lay::kTile + bktile_off(row & 127, 8 * c)) =
-                        make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                                   __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int row = r0 + i * kRows;
+                        if (row < count)
+                            *reinterpret_cast<uint4*>(smem + Lay::kQ + (row >> 7) * Lay::kTile + bktile_off(row & 127, 8 * c)) =
+                                make_uint4(__byte_perm(v[i].x, v[i].y, 0x5410), __byte_perm(v[i].x, v[i].y, 0x7632),
+                                           __byte_perm(v[i].z, v[i].w, 0x5410), __byte_perm(v[i].z, v[i].w, 0x7632));
+                    }
                 }
                 for (int row = ct; row < count; row += kStConvert) {
                     const int rw = first + row;
-                    float m = 0.f;
+                    float m = -INFINITY;  // rows past the last, and rows that saw nothing, add nothing
                     if (rw < w.rows) {
                         const int tok = rw / p.group, head = h * p.group + rw - tok * p.group;
                         m = -__ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head) * 1.4426950408889634f;
-                        if (m == INFINITY) m = -INFINITY;  // a row that saw nothing adds nothing
+                        if (m == INFINITY) m = -INFINITY;
                     }
                     reinterpret_cast<float*>(smem + Lay::kMinus)[row] = m;
                 }
@@ -367,20 +412,19 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 if (ok && (g == 0 || w.second(pair))) {
-                    const int buf = 2 * (kc[g] & 1) + g;
-                    ok = warp_wait(&bars[S_K_EMPTY + buf], ((kc[g] >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
-                    ++kc[g];
+                    const int buf = 2 * (pc & 1) + g;  // (the group of the pair, the tile of the pair)
+                    ok = warp_wait(&bars[S_K_EMPTY + buf], (uses[buf]++ & 1) ^ 1, ab, kDevTimeoutConvert);
                     if (ok) {
                         uint8_t* dst = smem + Lay::kK + buf * Lay::kTile;
                         uint8_t* lo = dst + bktile_off(rr, 16 * (ct & 3));
                         uint8_t* hi = dst + bktile_off(rr, 16 * (ct & 3) + 8);
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
+                        for (int m = 0; m < 4; ++m) {
                             const uint32_t f1 = scale_factor(ks[g][m]);
                             const uint32_t f[8] = {f1, f1, f1, f1, f1, f1, f1, f1};
 #pragma unroll
                             for (int x = 0; x < NB; ++x) {
-                                const int off = x * (kStTile * 128) + m * (64 * 128);
+                                const int off = x * (kStTile * 128) + m * (32 * 128);
                                 put16(lo + off, hi + off, kr[g][m * NB + x], f);
                             }
                         }
@@ -391,6 +435,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 }
                 fetch(g, blk);
             }
+            ++pc;
             rb = rb1;
             pair = pair1;
             rb1 = rb2;

@@ -75,15 +75,6 @@ constexpr int tc_part_floats() {
     return kRowsTc * D + 2 * kRowsTc;
 }
 
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // The first `left` of 16 bytes, the others 0.
 __device__ __forceinline__ uint4 cut16(uint4 v, int left) {
     auto cut = [](uint32_t w, int n) { return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u); };
