@@ -7,17 +7,17 @@
 // (sequence, KV head) and goes over the head's query rows in blocks of up to
 // 384, which stay in shared memory as three tiles while the cached tokens stream
 // past, in pairs of tiles of 128:
-//   warps 0, 1     issue the products of groups 0 and 1 (one lane each); warp 0
-//                  owns TMEM: 256 x 128 scores a group
-//   warps 4 .. 11  groups 0 and 1: exp2(S c - lse) and the sum over the columns.
-//                  They take the pairs in turn, so that one group's products run
-//                  while the other sums, and a thread has a token of each tile of
-//                  the pair: each query's lse is read from shared memory for two
-//                  (that reading fills the pipe that feeds the products; with one
-//                  token a thread the sums took twice as long)
-//   warps 12 .. 15 read K's codes from the pages (a pair of tiles ahead, in
-//                  registers), make them bf16 operand tiles, and bring the
-//                  query rows
+//   warps 0, 1     issue the products of the pairs with an even, an odd number
+//                  (one lane each); warp 0 owns TMEM: four places of 128 x 128
+//                  scores, one for each tile of two pairs
+//   warps 4 .. 19  four groups, one a place: exp2(S c - lse) and the sum over the
+//                  columns, a token a thread.  One warp's chain of load, product
+//                  sum, exponential and add leaves the units idle most of the
+//                  time, so each scheduler has four of them (with two it took
+//                  111 us for 757 x 5,788 tokens x 48 heads).  They also bring
+//                  the query rows.
+//   warps 20 .. 23 read K's codes from the pages (a pair of tiles ahead, in
+//                  registers) and make them bf16 operand tiles
 // With the queries kept, K is read and converted once per 384 rows, and the
 // queries once per block: keeping K instead would read them for every 128
 // tokens (430 MB of cache traffic for 757 x 5,788 tokens x 48 heads).
@@ -29,23 +29,22 @@ namespace rc {
 
 namespace {
 
-// 512 threads launched with 128 registers each; the warpgroups share them
-// 40 + 2 x 168 + 136 (a spilled register would come back from the L2 cache:
-// next to 227 KB of shared memory little is left of L1).
-constexpr int kStThreads = 512;
+// 768 threads launched with 80 registers each; the warpgroups share them
+// 40 + 4 x 88 + 88.
+constexpr int kStThreads = 768;
+constexpr int kStSums = 512;  // threads of the four groups
 constexpr int kStTile = 128;
 constexpr int kStQTiles = 3;  // query tiles in shared memory
-constexpr int kStConvert = 128;
 
 enum : int {
-    S_K_FULL = 0,    // [4] buffer 2 group + tile of the pair: K tile converted
+    S_K_FULL = 0,    // [4] buffer 2 (pair & 1) + tile of the pair: K tile converted
     S_K_EMPTY = 4,   // [4] its products have finished
-    S_S_FULL = 8,    // [group] scores of the pair and a query tile in TMEM
-    S_S_FREE = 10,   // [group] the group has read them
-    S_Q_FULL = 12,   // the block's query rows are in place
-    S_Q_EMPTY = 13,  // products and groups are done with them
-    S_DRAIN = 14,
-    S_COUNT = 15
+    S_S_FULL = 8,    // [4] scores of the K tile and a query tile in TMEM
+    S_S_FREE = 12,   // [4] the group has read them
+    S_Q_FULL = 16,   // the block's query rows are in place
+    S_Q_EMPTY = 17,  // every group has the scores of the block before
+    S_DRAIN = 18,
+    S_COUNT = 19
 };
 
 template <int D>
@@ -121,13 +120,11 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars[S_K_FULL + i], 4);
             mbar_init(&bars[S_K_EMPTY + i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[S_S_FULL + i], 1);
             mbar_init(&bars[S_S_FREE + i], 4);
         }
-        mbar_init(&bars[S_Q_FULL], 4);
-        mbar_init(&bars[S_Q_EMPTY], 2 + 8);
+        mbar_init(&bars[S_Q_FULL], 16);
+        mbar_init(&bars[S_Q_EMPTY], 16);
         mbar_init(&bars[S_DRAIN], 2);
         misc[1] = 0u;
         fence_mbar_init();
@@ -152,7 +149,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             const uint32_t q_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2));
             bool ok = true;
             // pairs of all groups; first, second K tiles and units of this one
-            int pc = 0, ka_count = 0, kb_count = 0, uc = 0;
+            int pc = 0, ka_count = 0, kb_count = 0, uc[2] = {0, 0};
             for (int rb = 0; rb < w.blocks && ok; ++rb) {
                 ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutMma);
                 for (int pair = 0; pair < w.pairs && ok; ++pair) {
@@ -160,14 +157,16 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                     const int q0 = w.first_tile(rb, pair), q1 = w.end_tile(rb), tiles = w.second(pair) ? 2 : 1;
                     ok = warp_wait(&bars[S_K_FULL + 2 * g], ka_count++ & 1, ab, kDevTimeoutMma);
                     if (ok && tiles == 2) ok = warp_wait(&bars[S_K_FULL + 2 * g + 1], kb_count++ & 1, ab, kDevTimeoutMma);
-                    for (int t = q0; t < q1 && ok; ++t, ++uc) {
-                        ok = warp_wait(&bars[S_S_FREE + g], (uc & 1) ^ 1, ab, kDevTimeoutMma);
-                        tc_fence_after();
-                        if (ok && elect_one()) {
-                            const uint32_t qb = q_lo + (t - rb * w.per) * (Lay::kTile >> 4);
-                            for (int a = 0; a < tiles; ++a) {
-                                const uint32_t d = tmem + 256u * g + 128u * a;
-                                const uint32_t ka = k_lo + (2 * g + a) * (Lay::kTile >> 4);
+                    for (int t = q0; t < q1 && ok; ++t) {
+                        const uint32_t qb = q_lo + (t - rb * w.per) * (Lay::kTile >> 4);
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) {
+                            if (a == tiles || !ok) break;
+                            const int place = 2 * g + a;
+                            ok = warp_wait(&bars[S_S_FREE + place], (uc[a]++ & 1) ^ 1, ab, kDevTimeoutMma);
+                            tc_fence_after();
+                            if (ok && elect_one()) {
+                                const uint32_t d = tmem + 128u * place, ka = k_lo + place * (Lay::kTile >> 4);
                                 mma_f16_ss_at<0, 0>(d, ka, qb, hi, idesc, 0);
                                 mma_f16_ss_at<2, 2>(d, ka, qb, hi, idesc, 1);
                                 mma_f16_ss_at<4, 4>(d, ka, qb, hi, idesc, 1);
@@ -178,15 +177,13 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                                     mma_f16_ss_at<1028, 1028>(d, ka, qb, hi, idesc, 1);
                                     mma_f16_ss_at<1030, 1030>(d, ka, qb, hi, idesc, 1);
                                 }
-                                if (t + 1 == q1) mma_commit(&bars[S_K_EMPTY + 2 * g + a]);
+                                mma_commit(&bars[S_S_FULL + place]);
+                                if (t + 1 == q1) mma_commit(&bars[S_K_EMPTY + place]);
                             }
-                            mma_commit(&bars[S_S_FULL + g]);
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                 }
-                if (elect_one()) mma_commit(&bars[S_Q_EMPTY]);
-                __syncwarp();
             }
             // every product has finished before the tensor memory is released
             if (elect_one()) mma_commit(&bars[S_DRAIN]);
@@ -195,119 +192,132 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             while (!mbar_try_wait(&bars[S_DRAIN], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
         }
-    } else if (wg == 1 || wg == 2) {
+    } else if (wg <= 4) {
         // ------------------------------------------------------------ sums
-        regs_inc<168>();
-        const int g = wg - 1, quad = warp & 3, r = quad * 32 + lane;
-        const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 256u * g;
+        regs_inc<88>();
+        const int place = wg - 1, g = place >> 1, a = place & 1, quad = warp & 3;
+        const int st = tid - 128;  // number among the groups' threads
+        const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * place;
         const float2 c2 = make_float2(p.sm_log2, p.sm_log2);
-        const float* minus = reinterpret_cast<const float*>(smem + Lay::kMinus);
-        int pc = 0, n = 0;  // pairs of all groups, units of this one
+        float* minus = reinterpret_cast<float*>(smem + Lay::kMinus);
+        int pc = 0, n = 0;  // pairs, units of this group
         bool ok = true;
         for (int rb = 0; rb < w.blocks && ok; ++rb) {
-            // (lse of the rows: written with the query tiles)
+            // the block's query rows: thread st has the piece st % kPieces of the
+            // rows st / kPieces + i kRows; and lse of each row
+            if (rb > 0) ok = warp_wait(&bars[S_Q_EMPTY], (rb - 1) & 1, ab, kDevTimeoutSoftmax);
+            if (!ok) break;
+            constexpr int kPieces = D / 8, kRows = kStSums / kPieces, kBatch = 6;
+            const int first = rb * w.per * kStTile, count = (w.end_tile(rb) - rb * w.per) * kStTile;
+            for (int r0 = st / kPieces; r0 < count; r0 += kBatch * kRows) {
+                uint4 v[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int rw = first + r0 + i * kRows;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (r0 + i * kRows < count && rw < w.rows) {
+                        const int tok = p.group == 1 ? rw : rw / p.group, head = h * p.group + rw - tok * p.group;
+                        v[i] = ldg_nc_na_v4(p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride +
+                                            static_cast<int64_t>(head) * D + 8 * (st % kPieces));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int row = r0 + i * kRows;
+                    if (row < count)
+                        *reinterpret_cast<uint4*>(smem + Lay::kQ + (row >> 7) * Lay::kTile +
+                                                  bktile_off(row & 127, 8 * (st % kPieces))) =
+                            make_uint4(__byte_perm(v[i].x, v[i].y, 0x5410), __byte_perm(v[i].x, v[i].y, 0x7632),
+                                       __byte_perm(v[i].z, v[i].w, 0x5410), __byte_perm(v[i].z, v[i].w, 0x7632));
+                }
+            }
+            for (int row = st; row < count; row += kStSums) {
+                const int rw = first + row;
+                float m = -INFINITY;  // rows past the last, and rows that saw nothing, add nothing
+                if (rw < w.rows) {
+                    const int tok = rw / p.group, head = h * p.group + rw - tok * p.group;
+                    m = -__ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head) * 1.4426950408889634f;
+                    if (m == INFINITY) m = -INFINITY;
+                }
+                minus[row] = m;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[S_Q_FULL]);
             ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutSoftmax);
             for (int pair = 0; pair < w.pairs && ok; ++pair) {
                 const int jp = j0 + pair * 2 * kStTile;
-                // the thread's tokens, one of each tile
-                const int ja = jp + r, jb = ja + kStTile;
+                const int j = jp + a * kStTile + quad * 32 + lane;  // the thread's token
                 if (!w.has(rb, pair)) {
-                    if (rb == 0 && g == 0 && w.first_row(jp) >= w.rows) {  // no row sees the pair
-                        if (ja < stop) p.out[row_at + ja] = p.scores[row_at + ja];
-                        if (jb < stop) p.out[row_at + jb] = p.scores[row_at + jb];
-                    }
+                    // no row of any block sees the pair
+                    if (rb == 0 && g == 0 && w.first_row(jp) >= w.rows && j < stop) p.out[row_at + j] = p.scores[row_at + j];
                     continue;
                 }
                 if ((pc++ & 1) != g) continue;
-                const int q0 = w.first_tile(rb, pair), q1 = w.end_tile(rb);
-                const int fa = w.first_row(ja), fb = w.first_row(jb);  // the first rows that see the tokens
-                float2 sa[4], sb[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sa[k] = sb[k] = make_float2(0.f, 0.f);
-                for (int t = q0; t < q1; ++t, ++n) {
-                    ok = warp_wait(&bars[S_S_FULL + g], n & 1, ab, kDevTimeoutSoftmax);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const float* mt = minus + (t - rb * w.per) * kStTile;
-                    // columns from these on count (rows past the last have a factor of 0)
-                    const int la = fa - t * kStTile, lb = fb - t * kStTile;
-                    const bool full = __all_sync(0xffffffffu, la <= 0 && lb <= 0);
-                    auto add = [&](uint32_t (&v)[16], const float2 (&m)[8], int c0, float2 (&acc)[4], int lo) {
-                        float2 x[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            x[k] = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, m[k]);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = make_float2(ex2(x[k].x), ex2(x[k].y));
-                        if (!full) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                if (c0 + 2 * k < lo) x[k].x = 0.f;
-                                if (c0 + 2 * k + 1 < lo) x[k].y = 0.f;
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) acc[k & 3] = add2(acc[k & 3], x[k]);
-                    };
-                    // 16 columns of both tokens while the next are on their way
-                    // (the second tile's place is read also where the pair has no
-                    // second tile: its sums are not stored)
-                    uint32_t va[16], vb[16], wa[16], wb[16];
-                    auto both = [&](uint32_t (&x)[16], uint32_t (&y)[16], int c0) {
-                        float2 m[8];
-#pragma unroll
-                        for (int k = 0; k < 8; k += 2) {
-                            const float4 f = *reinterpret_cast<const float4*>(mt + c0 + 2 * k);
-                            m[k] = make_float2(f.x, f.y);
-                            m[k + 1] = make_float2(f.z, f.w);
-                        }
-                        add(x, m, c0, sa, la);
-                        add(y, m, c0, sb, lb);
-                    };
-                    tmem_ld16_async(at, va);
-                    tmem_ld16_async(at + 128, vb);
-#pragma unroll 1
-                    for (int c0 = 0; c0 < kStTile; c0 += 32) {
-                        tmem_wait_ld_dep(va);
-                        tmem_wait_ld_dep(vb);
-                        tmem_ld16_async(at + c0 + 16, wa);
-                        tmem_ld16_async(at + 128 + c0 + 16, wb);
-                        both(va, vb, c0);
-                        tmem_wait_ld_dep(wa);
-                        tmem_wait_ld_dep(wb);
-                        if (c0 + 32 < kStTile) {
-                            tmem_ld16_async(at + c0 + 32, va);
-                            tmem_ld16_async(at + 128 + c0 + 32, vb);
-                        } else {
-                            // the scores are in registers: their place is free
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars[S_S_FREE + g]);
-                        }
-                        both(wa, wb, c0 + 16);
-                    }
-                }
-                if (!ok) break;
                 // the first block of rows that sees the pair starts from the given scores
                 const float* from = rb == w.first_row(jp) / kStTile / w.per ? p.scores : p.out;
-                auto store = [&](int j, const float2 (&acc)[4]) {
-                    if (j >= stop) return;
+                float2 acc[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
+                if (a == 0 || w.second(pair)) {
+                    const int q0 = w.first_tile(rb, pair), q1 = w.end_tile(rb);
+                    const int seen = w.first_row(j);  // the first row that sees the token
+                    for (int t = q0; t < q1; ++t, ++n) {
+                        ok = warp_wait(&bars[S_S_FULL + place], n & 1, ab, kDevTimeoutSoftmax);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const float* mt = minus + (t - rb * w.per) * kStTile;
+                        const int lo = seen - t * kStTile;  // columns from this on count
+                        const bool full = __all_sync(0xffffffffu, lo <= 0);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kStTile; c0 += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(at + c0, v);
+                            if (c0 + 32 == kStTile) {
+                                // the scores are in registers: their place is free
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&bars[S_S_FREE + place]);
+                            }
+                            float2 x[16];
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) {
+                                const float4 m = *reinterpret_cast<const float4*>(mt + c0 + 2 * k);
+                                x[k] = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2,
+                                            make_float2(m.x, m.y));
+                                x[k + 1] = fma2(make_float2(__uint_as_float(v[2 * k + 2]), __uint_as_float(v[2 * k + 3])), c2,
+                                                make_float2(m.z, m.w));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) x[k] = make_float2(ex2(x[k].x), ex2(x[k].y));
+                            if (!full) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    if (c0 + 2 * k < lo) x[k].x = 0.f;
+                                    if (c0 + 2 * k + 1 < lo) x[k].y = 0.f;
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) acc[k & 3] = add2(acc[k & 3], x[k]);
+                        }
+                    }
+                    if (!ok) break;
+                }
+                if (j < stop) {
                     const float2 x = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
                     p.out[row_at + j] = from[row_at + j] + (j < q.kv ? x.x + x.y : 0.f);
-                };
-                store(ja, sa);
-                store(jb, sb);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_Q_EMPTY]);
         }
     } else {
-        // ------------------------------------------------------------ K and Q
+        // ------------------------------------------------------------ K
         // Thread ct: the pieces of 16 dims ct % 4 (+ 4 in the second 64 dims) of
         // the rows ct / 4 + 32 m of each tile.  Lane l < 16 of a warp
         // looks up the block of 16 tokens l of the pair.
-        regs_inc<136>();
-        const int ct = tid - 3 * 128;
+        regs_inc<88>();
+        const int ct = tid - 5 * 128;
         constexpr int NB = D / 64;
         const int rr = ct >> 2, pb = p.g.page_shift - 4;
         const uint8_t* kbase = p.g.kcodes + (rr & 15) * D + 16 * (ct & 3);
@@ -357,54 +367,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         }
         int ahead = entry(rb1, pair1);
         bool ok = true;
-        int loaded = -1;  // the block of rows in shared memory
-        while (ok) {
-            // query rows up to the current pair's block (blocks without work are passed as well)
-            for (const int want = min(rb, w.blocks - 1); loaded < want && ok;) {
-                ++loaded;
-                if (loaded > 0) ok = warp_wait(&bars[S_Q_EMPTY], (loaded - 1) & 1, ab, kDevTimeoutConvert);
-                if (!ok) break;
-                constexpr int kPieces = D / 8;
-                const int first = loaded * w.per * kStTile, count = (w.end_tile(loaded) - loaded * w.per) * kStTile;
-                // thread ct: piece ct % kPieces of the rows ct / kPieces + i kRows
-                constexpr int kRows = kStConvert / kPieces, kBatch = 8;  // rows a step, loads in flight
-                const int c = ct % kPieces;
-                for (int r0 = ct / kPieces; r0 < count; r0 += kBatch * kRows) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int rw = first + r0 + i * kRows;
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (r0 + i * kRows < count && rw < w.rows) {
-                            const int tok = p.group == 1 ? rw : rw / p.group, head = h * p.group + rw - tok * p.group;
-                            v[i] = ldg_nc_na_v4(p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride +
-                                                static_cast<int64_t>(head) * D + 8 * c);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int row = r0 + i * kRows;
-                        if (row < count)
-                            *reinterpret_cast<uint4*>(smem + Lay::kQ + (row >> 7) * Lay::kTile + bktile_off(row & 127, 8 * c)) =
-                                make_uint4(__byte_perm(v[i].x, v[i].y, 0x5410), __byte_perm(v[i].x, v[i].y, 0x7632),
-                                           __byte_perm(v[i].z, v[i].w, 0x5410), __byte_perm(v[i].z, v[i].w, 0x7632));
-                    }
-                }
-                for (int row = ct; row < count; row += kStConvert) {
-                    const int rw = first + row;
-                    float m = -INFINITY;  // rows past the last, and rows that saw nothing, add nothing
-                    if (rw < w.rows) {
-                        const int tok = rw / p.group, head = h * p.group + rw - tok * p.group;
-                        m = -__ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head) * 1.4426950408889634f;
-                        if (m == INFINITY) m = -INFINITY;
-                    }
-                    reinterpret_cast<float*>(smem + Lay::kMinus)[row] = m;
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[S_Q_FULL]);
-            }
-            if (!ok || rb >= w.blocks) break;
+        while (ok && rb < w.blocks) {
             const uint32_t blk = block_of(rb1, pair1, ahead);
             int rb2 = rb1, pair2 = pair1;
             if (rb1 < w.blocks) advance(rb2, pair2);
