@@ -126,6 +126,13 @@ __device__ __forceinline__ uint32_t scale_factor2(uint32_t two) {  // bytes in b
 __device__ __forceinline__ uint32_t factors02(uint32_t w) { return scale_factor2(w & 0x00ff00ffu); }
 __device__ __forceinline__ uint32_t factors13(uint32_t w) { return scale_factor2((w >> 8) & 0x00ff00ffu); }
 
+// The fp32 value of E8M0 byte `byte` of a word: 2^(b - 127), and NaN (or, for
+// bytes that no row here has, 2^127 and up) for 255.
+__device__ __forceinline__ float e8m0_float(uint32_t w, int byte) {
+    const uint32_t b = (w >> (8 * byte)) & 0xffu;
+    return __uint_as_float(b == 255u ? 0x7fc00000u : b << 23);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -150,13 +157,98 @@ __device__ __forceinline__ int scale_exponent(float amax) {
     return amax == 0.f ? 0 : max(-124, min(7, e));
 }
 
-// D (+)= A B, A 16 x 16 row-major fragment, B 16 x 8, fp32 accumulators.
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// D += A B, A a 16 x 16 row-major fragment, B 16 x 8, fp32 accumulators, for
+// 8 NR rows: with NR = 1 the fragment's rows 8 .. 15 are zero and take no registers.
+template <int NR>
+__device__ __forceinline__ void mma_rows_bf16(float (&d)[2 * NR], const uint32_t (&a)[2 * NR], uint32_t b0, uint32_t b1) {
+    if constexpr (NR == 2) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    } else {
+        float z0 = 0.f, z1 = 0.f;
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(z0), "+f"(z1)
+            : "r"(a[0]), "r"(0u), "r"(a[1]), "r"(b0), "r"(b1));
+    }
+}
+template <int NR>
+__device__ __forceinline__ void mma_rows_f16(float (&d)[2 * NR], const uint32_t (&a)[2 * NR], uint32_t b0, uint32_t b1) {
+    if constexpr (NR == 2) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    } else {
+        float z0 = 0.f, z1 = 0.f;
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(z0), "+f"(z1)
+            : "r"(a[0]), "r"(0u), "r"(a[1]), "r"(b0), "r"(b1));
+    }
+}
+
+// Four E4M3 codes (code 0 in the low byte) as fp16, exactly: pairs (0, 1), (2, 3).
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+// Fragments of query rows for products with K's codes as fp16: 8 NR rows, each
+// divided by a power of two that puts its largest magnitude in [2^14, 2^15), so
+// that bf16's 8 bits are exact in fp16 down to 2^-32 of it (what is smaller
+// loses bits that are nothing beside the row's largest).  scale[r]: that power
+// times `factor`.  Product c * 4 + i of the lane (row lane / 4, t = lane % 4)
+// holds dims 16 (t + 4 c) + 4 i + {0, 1} and + {2, 3}, as codes_f16 gives them.
+template <int D, int NR>
+__device__ __forceinline__ void query_rows_f16(const __nv_bfloat16* const (&row)[NR], const bool (&live)[NR], float factor,
+                                               uint32_t (&qa)[D / 16][2 * NR], float (&scale)[NR]) {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        uint32_t w[D / 8];
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (live[r]) {
+                a = __ldg(reinterpret_cast<const uint4*>(row[r] + 16 * (t + 4 * c)));
+                b = __ldg(reinterpret_cast<const uint4*>(row[r] + 16 * (t + 4 * c) + 8));
+            }
+            const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                w[8 * c + i] = x[i];
+                amax = max3(amax, fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u)));
+            }
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^e with 14 <= log2(amax) - e < 15, e kept where 2^e and 2^-e are normal
+        // numbers; rows of zeros, and rows that are not finite, are taken as they are
+        int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+        e = amax > 0.f && amax <= 3.4028235e38f ? max(-126, min(126, e)) : 0;
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        scale[r] = factor * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t v = w[2 * k + x];
+                __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xFFFF0000u) * inv);
+                qa[k][x * NR + r] = *reinterpret_cast<uint32_t*>(&h);
+            }
+    }
 }
 
 struct PagedWriteParams {

@@ -6,12 +6,14 @@
 // instructions want them, with no shared memory and no barrier on the way.
 // A block has one (sequence, KV head, tile of 16 rows, split of the cached
 // tokens); a warp takes 64 cached tokens at a time:
-//   S = Q K^T   mma m16n8k16 in bf16: a 16-byte piece of a K row is 16 of the
-//               summed dims for its token; which dims of the product they are
-//               is free as long as Q is held in the same order
+//   S = Q K^T   mma m16n8k16 in fp16: one conversion makes two codes exact fp16
+//               numbers, the rows of Q are scaled to fp16's range, and the
+//               tokens' scales (powers of two) multiply S.  A 16-byte piece of a
+//               K row is 16 of the summed dims for its token; which dims of the
+//               product they are is free as long as Q is held in the same order
 //   P = exp2(S - max), online; P's accumulator layout is the A operand of
-//   O += P V    whose B operand is a 16-byte piece of a V row: 16 tokens of
-//               one dim.  The tokens of S's columns are chosen to match.
+//   O += P V    in bf16, whose B operand is a 16-byte piece of a V row: 16 tokens
+//               of one dim, with their scales (which fp16 could not hold).  The tokens of S's columns are chosen to match.
 // The warps' (max, sum, O) are joined through shared memory; with several
 // splits they go to the workspace, and the block that arrives last at its row
 // tile's counter joins them in split order, so results do not depend on timing.
@@ -25,22 +27,24 @@ namespace {
 
 constexpr int kRowsWarps = 4;
 constexpr int kRowsThreads = kRowsWarps * 32;
-constexpr int kRowTile = 16;
 constexpr int kChunk = 64;  // cached tokens of a warp's step
 
-// One split's result for a row tile in the workspace: O [16][D], then max and
-// sum [16] each.
-template <int D>
+// One split's result for a row tile of 8 NR rows in the workspace: O [rows][D],
+// then max and sum [rows] each.
+template <int D, int NR>
 constexpr int part_floats() {
-    return kRowTile * D + 2 * kRowTile;
+    return 8 * NR * D + 2 * 8 * NR;
 }
 
 // Weight of a partial whose running max is m against the joint max M (both in
 // log2 units; -inf: the partial saw nothing).
 __device__ __forceinline__ float join_weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
 
-template <int D>
-__global__ void __launch_bounds__(kRowsThreads) paged_rows_kernel(PagedAttnParams p) {
+// 8 NR rows a block (NR 1 or 2): with eight the accumulators take half the
+// registers, and a third block fits an SM.
+template <int D, int NR>
+__global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kernel(PagedAttnParams p) {
+    constexpr int kRowTile = 8 * NR;
     constexpr int CH = D / 64;  // 16-byte pieces of a K row that a lane reads
     constexpr int NT = D / 8;   // n tiles of O
     __shared__ __align__(16) float so[kRowsWarps][kRowTile][D + 4];
@@ -59,134 +63,148 @@ __global__ void __launch_bounds__(kRowsThreads) paged_rows_kernel(PagedAttnParam
     if (split >= nsplit) return;
     const int j0 = split * p.split_tokens, j1 = min(seen, j0 + p.split_tokens);
 
-    // rows r0 = g and r1 = g + 8 of the tile: token, query head, tokens seen
-    int limit[2];
-    const __nv_bfloat16* qrow[2];
-    bool live[2];
+    // the lane's rows g (and g + 8) of the tile: token, query head, tokens seen
+    int limit[NR];
+    const __nv_bfloat16* qrow[NR];
+    bool live[NR];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NR; ++i) {
         const int r = tile * kRowTile + g + 8 * i;
         live[i] = r < rows;
         const int tok = live[i] ? r / p.group : 0, head = h * p.group + (live[i] ? r - tok * p.group : 0);
         qrow[i] = p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D;
         limit[i] = !live[i] ? 1 << 30 : p.causal ? max(0, q.kv - q.n + tok + 1) : q.kv;
     }
-    // Q fragments: product c * 4 + i of the lane holds dims 16 (t + 4 c) + 4 i + {0, 2} and + {1, 3}
-    uint32_t qa[CH * 4][4];
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (live[r]) {
-                a = *reinterpret_cast<const uint4*>(qrow[r] + 16 * (t + 4 * c));
-                b = *reinterpret_cast<const uint4*>(qrow[r] + 16 * (t + 4 * c) + 8);
-            }
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                qa[c * 4 + i][r] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);      // dims 0, 2
-                qa[c * 4 + i][2 + r] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);  // dims 1, 3
-            }
-        }
+    uint32_t qa[CH * 4][2 * NR];
+    float qscale[NR];
+    query_rows_f16<D, NR>(qrow, live, p.sm_log2, qa, qscale);
 
-    float o[NT][4];
+    float o[NT][2 * NR];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        for (int i = 0; i < 2 * NR; ++i) o[n][i] = 0.f;
+    float m_run[NR], l_run[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        m_run[r] = -INFINITY;
+        l_run[r] = 0.f;
+    }
     const int P = 1 << p.g.page_shift;
 
-    for (int jc = j0 + warp * kChunk; jc < j1; jc += kRowsWarps * kChunk) {
-        // The lane reads K rows of the 16-token block g >> 1 and V pieces of
-        // block t.  A block behind the sequence's end, or on a bad page, is
-        // read from page 0 instead and masked (K) or given the factor 0 (V).
-        const int kblk = jc + 16 * (g >> 1), vblk = jc + 16 * t;
-        const int kpage = kblk < q.kv ? load_page(p.g, s, kblk >> p.g.page_shift) : 0;
-        const int vpage = vblk < q.kv ? load_page(p.g, s, vblk >> p.g.page_shift) : 0;
-        const bool vok = vblk < q.kv && vpage >= 0;
-        const size_t kph = static_cast<size_t>(max(kpage, 0)) * p.g.kv_heads + h;
-        const size_t vph = static_cast<size_t>(max(vpage, 0)) * p.g.kv_heads + h;
-        const int koff = kblk & (P - 1), voff = vblk & (P - 1);
+    // Lane l < 4 of each four reads the page of the chunk's block l of 16 tokens a
+    // chunk ahead.
+    const uint32_t* table =
+        reinterpret_cast<const uint32_t*>(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages);
+    auto entry = [&](int jc) {
+        const int j = jc + 16 * t;
+        return jc < j1 && j < q.kv ? static_cast<int>(ldg_early(table + (j >> p.g.page_shift))) : 0;
+    };
+    constexpr int kStride = kRowsWarps * kChunk;
+    int ahead = entry(j0 + warp * kChunk);
+    for (int jc = j0 + warp * kChunk; jc < j1; jc += kStride) {
+        // The lane reads K rows of the 16-token block g >> 1 and V pieces and
+        // scales of block t.  A block behind the sequence's end, or on a bad
+        // page, is read from page 0 instead, and its tokens are cut off (K) or
+        // given the factor 0 (V).
+        const int vblk = jc + 16 * t;
+        const bool vok = vblk < q.kv && check_page(p.g, ahead);
+        const uint32_t mine = static_cast<uint32_t>(vok ? ahead : 0);
+        const size_t vph = static_cast<size_t>(mine) * p.g.kv_heads + h;
+        const size_t kph = static_cast<size_t>(__shfl_sync(0xffffffffu, mine, g >> 1)) * p.g.kv_heads + h;
+        const int koff = (jc + 16 * (g >> 1)) & (P - 1), voff = vblk & (P - 1);
         const uint8_t* kp = p.g.kcodes + (kph * P + koff + 2 * (g & 1)) * D + 16 * t;
-        const uint8_t* ksp = p.g.kscale + kph * P + koff + 2 * (g & 1);
         const uint8_t* vp = p.g.vcodes + (vph * D + g) * P + voff;
+        ahead = entry(jc + kStride);
 
         // S: column 2t + b of n tile (i, ab) is token 16 t + 4 i + ab + 2 b, so
         // the lane's K row for it is token 16 (g >> 1) + 4 i + ab + 2 (g & 1)
-        float sc[8][4];
+        float sc[8][2 * NR];
         uint4 kw[8][CH];
-        uint32_t ks[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) kw[n][c] = ldg_nc_na_v4(kp + (4 * (n >> 1) + (n & 1)) * D + 64 * c);
+        const uint4 ksw = ldg_nc_na_v4(p.g.kscale + vph * P + voff);
+        const uint4 vsw = ldg_nc_na_v4(p.g.vscale + vph * P + voff);
+        // the first half of the V pieces is on its way while S is computed, the
+        // second while the softmax runs
+        uint4 vw[NT];
+#pragma unroll
+        for (int n = 0; n < NT / 2; ++n) vw[n] = ldg_nc_na_v4(vp + static_cast<size_t>(8 * n) * P);
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-            const int row = 4 * (n >> 1) + (n & 1);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) kw[n][c] = ldg_nc_na_v4(kp + row * D + 64 * c);
-            ks[n] = __ldg(ksp + row);
-        }
-        const uint4 vsw = __ldg(reinterpret_cast<const uint4*>(p.g.vscale + vph * P + voff));
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const uint32_t f = kpage >= 0 ? scale_factor(ks[n]) : 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
+            for (int i = 0; i < 2 * NR; ++i) sc[n][i] = 0.f;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const uint32_t w[4] = {kw[n][c].x, kw[n][c].y, kw[n][c].z, kw[n][c].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_bf16(sc[n], qa[c * 4 + i], bf2_mul(codes02(w[i]), f), bf2_mul(codes13(w[i]), f));
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t lo, hi;
+                    codes_f16(w[i], lo, hi);
+                    mma_rows_f16<NR>(sc[n], qa[c * 4 + i], lo, hi);
+                }
             }
         }
-        // V pieces on their way while the softmax runs
-        uint4 vw[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) vw[n] = ldg_nc_na_v4(vp + static_cast<size_t>(8 * n) * P);
+        for (int n = NT / 2; n < NT; ++n) vw[n] = ldg_nc_na_v4(vp + static_cast<size_t>(8 * n) * P);
 
-        // softmax: rows g (i = 0) and g + 8 (i = 1)
-        const int room = min(min(limit[0], limit[1]), j1) - jc;
+        // softmax: the lane's columns are the 16 tokens of block t
+        int room = j1 - jc;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) room = min(room, limit[r] - jc);
         const bool full = __all_sync(0xffffffffu, room >= kChunk);
-        float mx[2] = {-INFINITY, -INFINITY};
+        const uint32_t ks[4] = {ksw.x, ksw.y, ksw.z, ksw.w};
+        float mx[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
 #pragma unroll
         for (int n = 0; n < 8; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = i >> 1, b = i & 1;
-                const int j = jc + 16 * t + 4 * (n >> 1) + (n & 1) + 2 * b;
-                float x = sc[n][i] * p.sm_log2;
-                if (!full && (j >= limit[r] || j >= j1)) x = -INFINITY;
-                sc[n][i] = x;
-                mx[r] = fmaxf(mx[r], x);
-            }
-        float alpha[2], base[2];
+            for (int b = 0; b < 2; ++b) {
+                const int byte = (n & 1) + 2 * b;  // of word n >> 1: the column's token
+                const float f = e8m0_float(ks[n >> 1], byte);
+                const int j = jc + 16 * t + 4 * (n >> 1) + byte;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+                for (int r = 0; r < NR; ++r) {
+                    float x = sc[n][2 * r + b] * f;
+                    if (!full && (j >= limit[r] || j >= j1)) x = -INFINITY;
+                    sc[n][2 * r + b] = x;
+                    mx[r] = fmaxf(mx[r], x);
+                }
+            }
+        float alpha[NR], base[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-            const float m_new = fmaxf(m_run[r], mx[r]);
+            const float m_new = fmaxf(m_run[r], mx[r] * qscale[r]);
             base[r] = m_new == -INFINITY ? 0.f : m_new;
             alpha[r] = ex2(m_run[r] - base[r]);  // 0 while nothing was seen
             m_run[r] = m_new;
         }
-        float sum[2] = {0.f, 0.f};
+        float sum[NR];
+        bool moved = false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            sum[r] = 0.f;
+            moved |= alpha[r] != 1.f;
+        }
 #pragma unroll
         for (int n = 0; n < 8; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sc[n][i] = ex2(sc[n][i] - base[i >> 1]);
+            for (int i = 0; i < 2 * NR; ++i) {
+                sc[n][i] = ex2(fmaf(sc[n][i], qscale[i >> 1], -base[i >> 1]));
                 sum[i >> 1] += sc[n][i];
             }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) l_run[r] = l_run[r] * alpha[r] + sum[r];
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+        for (int r = 0; r < NR; ++r) l_run[r] = l_run[r] * alpha[r] + sum[r];
+        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                o[n][0] *= alpha[0];
-                o[n][1] *= alpha[0];
-                o[n][2] *= alpha[1];
-                o[n][3] *= alpha[1];
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2 * NR; ++i) o[n][i] *= alpha[i >> 1];
         }
         // the V pieces' 16 tokens: factors by word, 0 for tokens the sequence does not have
         uint32_t vf[8];
@@ -197,11 +215,12 @@ __global__ void __launch_bounds__(kRowsThreads) paged_rows_kernel(PagedAttnParam
         uint32_t nans = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) nans |= __vcmpgtu4(vs[i], 0x86868686u);
-        if (__any_sync(0xffffffffu, nans != 0)) {
+        const bool special = __any_sync(0xffffffffu, nans != 0) || !full;
+        if (special) {
 #pragma unroll
             for (int n = 0; n < 8; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2 * NR; ++i) {
                     const int byte = (n & 1) + 2 * (i & 1);
                     const int j = jc + 16 * t + 4 * (n >> 1) + byte;
                     if (((vs[n >> 1] >> (8 * byte)) & 0xffu) > 134u && j < limit[i >> 1] && j < j1)
@@ -210,32 +229,37 @@ __global__ void __launch_bounds__(kRowsThreads) paged_rows_kernel(PagedAttnParam
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t good = vs[i] & ~__vcmpgtu4(vs[i], 0x86868686u);
-            vf[2 * i] = factors02(good);
-            vf[2 * i + 1] = factors13(good);
-            if (!full || !vok) {
+            vf[2 * i] = factors02(vs[i]);
+            vf[2 * i + 1] = factors13(vs[i]);
+        }
+        if (special || __any_sync(0xffffffffu, !vok)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t good = vs[i] & ~__vcmpgtu4(vs[i], 0x86868686u);
                 const int left = vok ? q.kv - (vblk + 4 * i) : 0;  // tokens of the word that exist
-                vf[2 * i] &= (left > 0 ? 0xffffu : 0u) | (left > 2 ? 0xffff0000u : 0u);
-                vf[2 * i + 1] &= (left > 1 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u);
+                vf[2 * i] = factors02(good) & ((left > 0 ? 0xffffu : 0u) | (left > 2 ? 0xffff0000u : 0u));
+                vf[2 * i + 1] = factors13(good) & ((left > 1 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u));
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             // products over tokens 16 t + 4 i + {0, 2} (n tile (i, 0)) and + {1, 3} (n tile (i, 1))
-            const uint32_t pa[4] = {pack_bf16(sc[2 * i][0], sc[2 * i][1]), pack_bf16(sc[2 * i][2], sc[2 * i][3]),
-                                    pack_bf16(sc[2 * i + 1][0], sc[2 * i + 1][1]),
-                                    pack_bf16(sc[2 * i + 1][2], sc[2 * i + 1][3])};
+            uint32_t pa[2 * NR];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int r = 0; r < NR; ++r) pa[x * NR + r] = pack_bf16(sc[2 * i + x][2 * r], sc[2 * i + x][2 * r + 1]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const uint32_t w = i == 0 ? vw[n].x : i == 1 ? vw[n].y : i == 2 ? vw[n].z : vw[n].w;
-                mma_bf16(o[n], pa, bf2_mul(codes02(w), vf[2 * i]), bf2_mul(codes13(w), vf[2 * i + 1]));
+                mma_rows_bf16<NR>(o[n], pa, bf2_mul(codes02(w), vf[2 * i]), bf2_mul(codes13(w), vf[2 * i + 1]));
             }
         }
     }
 
     // ---- join the warps
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < NR; ++r) {
         l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
         l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
         if (t == 0) {
@@ -249,7 +273,7 @@ __global__ void __launch_bounds__(kRowsThreads) paged_rows_kernel(PagedAttnParam
     __syncthreads();
     const int rows_here = min(kRowTile, rows - tile * kRowTile);
     const int slot = (s * p.row_tiles + tile) * p.g.kv_heads + h;
-    float* part = p.part + static_cast<size_t>(slot) * p.splits * part_floats<D>();
+    float* part = p.part + static_cast<size_t>(slot) * p.splits * part_floats<D, NR>();
     auto store_out = [&](int r, int d, float4 v, float M, float L) {
         const int rr = tile * kRowTile + r, tok = rr / p.group, head = h * p.group + rr - tok * p.group;
         const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // a sum that is not a number stays one
@@ -280,7 +304,7 @@ __global__ void __launch_bounds__(kRowsThreads) paged_rows_kernel(PagedAttnParam
         if (nsplit == 1) {
             store_out(r, d, acc, M, L);
         } else {
-            float* mine = part + static_cast<size_t>(split) * part_floats<D>();
+            float* mine = part + static_cast<size_t>(split) * part_floats<D, NR>();
             *reinterpret_cast<float4*>(mine + r * D + d) = acc;
             if (d == 0) {
                 mine[kRowTile * D + r] = M;
@@ -301,11 +325,11 @@ __global__ void __launch_bounds__(kRowsThreads) paged_rows_kernel(PagedAttnParam
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         float M = -INFINITY;
         for (int k = 0; k < nsplit; ++k)
-            M = fmaxf(M, __ldcg(part + static_cast<size_t>(k) * part_floats<D>() + kRowTile * D + r));
+            M = fmaxf(M, __ldcg(part + static_cast<size_t>(k) * part_floats<D, NR>() + kRowTile * D + r));
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float L = 0.f;
         for (int k = 0; k < nsplit; ++k) {
-            const float* b = part + static_cast<size_t>(k) * part_floats<D>();
+            const float* b = part + static_cast<size_t>(k) * part_floats<D, NR>();
             const float f = join_weight(__ldcg(b + kRowTile * D + r), M);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(b + r * D + d));
             acc.x += f * v.x;
@@ -318,10 +342,10 @@ __global__ void __launch_bounds__(kRowsThreads) paged_rows_kernel(PagedAttnParam
     }
 }
 
-template <int D>
+template <int D, int NR>
 cudaError_t launch_rows(PagedAttnParams& p, size_t part_floats_max, int max_counters, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
-    p.row_tiles = static_cast<int>((rows + kRowTile - 1) / kRowTile);
+    p.row_tiles = static_cast<int>((rows + 8 * NR - 1) / (8 * NR));
     const int64_t slots = static_cast<int64_t>(p.g.seqs) * p.row_tiles * p.g.kv_heads;
     if (static_cast<int64_t>(p.row_tiles) * p.g.kv_heads > 65535) return cudaErrorInvalidValue;
     // Splits: enough blocks for several on each of the 152 SMs, at least one
@@ -331,25 +355,32 @@ cudaError_t launch_rows(PagedAttnParams& p, size_t part_floats_max, int max_coun
     int64_t want = (152 * 12 + slots - 1) / slots;
     want = std::min<int64_t>(want, 32);
     want = std::min<int64_t>(want, (p.g.max_kv + step - 1) / step);
-    want = std::min<int64_t>(want, static_cast<int64_t>(part_floats_max / (slots * part_floats<D>())));
+    want = std::min<int64_t>(want, static_cast<int64_t>(part_floats_max / (slots * part_floats<D, NR>())));
     if (slots > max_counters || want < 1) want = 1;
     const int per = static_cast<int>((p.g.max_kv + want - 1) / want);
     p.split_tokens = std::max(step, (per + step - 1) / step * step);
     p.splits = std::max(1, (p.g.max_kv + p.split_tokens - 1) / p.split_tokens);
     dim3 grid(p.splits, p.row_tiles * p.g.kv_heads, p.g.seqs);
-    paged_rows_kernel<D><<<grid, kRowsThreads, 0, s>>>(p);
+    paged_rows_kernel<D, NR><<<grid, kRowsThreads, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_attention_d(PagedAttnParams& p, size_t part_floats_max, int max_counters, cudaStream_t s) {
+    const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
+    // up to one row tile per KV head the reading of the codes is what counts;
+    // with more rows each tile would read them again
+    if (rows <= 8) return launch_rows<D, 1>(p, part_floats_max, max_counters, s);
+    if (rows <= 16) return launch_rows<D, 2>(p, part_floats_max, max_counters, s);
+    return launch_paged_tc(p, D, part_floats_max, s);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attention(PagedAttnParams& p, int D, size_t part_floats_max, int max_counters,
                                    cudaStream_t s) {
-    // up to one row tile per KV head the reading of the codes is what counts;
-    // with more rows each tile would read them again
-    if (static_cast<int64_t>(p.g.max_new) * p.group > kRowTile) return launch_paged_tc(p, D, part_floats_max, s);
-    return D == 128 ? launch_rows<128>(p, part_floats_max, max_counters, s)
-                    : launch_rows<64>(p, part_floats_max, max_counters, s);
+    return D == 128 ? launch_attention_d<128>(p, part_floats_max, max_counters, s)
+                    : launch_attention_d<64>(p, part_floats_max, max_counters, s);
 }
 
 }  // namespace rc

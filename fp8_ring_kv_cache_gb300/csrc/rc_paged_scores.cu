@@ -1,11 +1,18 @@
 // rc_paged_scores.cu -- the attention weight that each cached token received:
 // out[j] = scores[j] + sum over the query rows of exp(q . k_j scale - lse).
 //
-// paged_scores_rows_kernel, for few query rows: bound by reading the K codes.
+// paged_scores_few_kernel, for one tile of query rows (a decode step): bound by
+// reading the K codes.  The rows stay in registers while the warps go over the
+// cached tokens 64 at a time, reading K pieces straight into the fp16 products'
+// operands as the attention does; the eight lanes that hold a token's rows add
+// up by halves, so that each ends with the sums of two tokens.
+// paged_scores_rows_kernel, for some tiles of rows.
 // A warp owns 32 cached tokens of one (sequence, KV head), decodes their K rows
 // to bf16 once, into the registers where the matrix instructions want them, and
 // goes over the head's query rows 16 at a time.  A token's sum stays with its
 // owner, so no two threads add to one entry and the order is fixed.
+#include <algorithm>
+
 #include "rc_paged.cuh"
 
 namespace rc {
@@ -15,6 +22,114 @@ namespace {
 constexpr int kScoreWarps = 4;
 constexpr int kScoreTokens = 32;  // of a warp
 constexpr int kScoreRowsMax = 128;
+
+constexpr int kFewChunk = 64;  // cached tokens of a warp's step
+
+// 8 NR rows; a block has `range` cached tokens (a multiple of 256).
+template <int D, int NR>
+__global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_few_kernel(PagedScoreParams p, int range) {
+    constexpr int CH = D / 64;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int h = blockIdx.y, s = blockIdx.z;
+    const int j0 = blockIdx.x * range, stop = min(p.g.max_kv, j0 + range);
+    const Seq q = load_seq(p.g, s);
+    const int rows = q.n * p.group;
+    const int64_t at = (static_cast<int64_t>(s) * p.g.kv_heads + h) * p.score_stride;
+    const int end = rows > 0 ? min(stop, q.kv) : j0;  // tokens from here on keep their scores
+    constexpr int kStride = kScoreWarps * kFewChunk;
+    uint32_t qa[D / 16][2 * NR];
+    float qscale[NR], minus[NR];
+    int limit[NR];
+    if (j0 < end) {
+        const __nv_bfloat16* qrow[NR];
+        bool live[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int r = g + 8 * i;
+            live[i] = r < rows;
+            const int tok = live[i] ? r / p.group : 0, head = h * p.group + (live[i] ? r - tok * p.group : 0);
+            qrow[i] = p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D;
+            const float lse = live[i] ? __ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head) : -INFINITY;
+            minus[i] = -lse * 1.4426950408889634f;
+            limit[i] = lse == -INFINITY ? 0 : p.causal ? q.kv - q.n + tok + 1 : q.kv;
+        }
+        query_rows_f16<D, NR>(qrow, live, p.sm_log2, qa, qscale);
+    }
+    const int P = 1 << p.g.page_shift;
+    const uint32_t* table =
+        reinterpret_cast<const uint32_t*>(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages);
+    auto entry = [&](int jc) {
+        const int j = jc + 16 * t;
+        return jc < end && j < q.kv ? static_cast<int>(ldg_early(table + (j >> p.g.page_shift))) : 0;
+    };
+    int jc = j0 + warp * kFewChunk;
+    int ahead = entry(jc);
+    for (; jc < end; jc += kStride) {
+        // (a block of 16 tokens behind the end, or on a bad page: page 0 is read, its tokens are cut off)
+        const int blk = jc + 16 * t;
+        const uint32_t mine = static_cast<uint32_t>(blk < q.kv && check_page(p.g, ahead) ? ahead : 0);
+        const size_t kph = static_cast<size_t>(__shfl_sync(0xffffffffu, mine, g >> 1)) * p.g.kv_heads + h;
+        const int koff = (jc + 16 * (g >> 1)) & (P - 1);
+        const uint8_t* kp = p.g.kcodes + (kph * P + koff + 2 * (g & 1)) * D + 16 * t;
+        uint4 kw[8][CH];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) kw[n][c] = ldg_nc_na_v4(kp + (4 * (n >> 1) + (n & 1)) * D + 64 * c);
+        const uint4 ksw = ldg_nc_na_v4(p.g.kscale + (static_cast<size_t>(mine) * p.g.kv_heads + h) * P + (blk & (P - 1)));
+        const int j = blk + 2 * g;  // the lane's tokens in the end
+        float2 old = make_float2(0.f, 0.f);
+        if (j < stop) old.x = __ldcg(p.scores + at + j);
+        if (j + 1 < stop) old.y = __ldcg(p.scores + at + j + 1);
+        ahead = entry(jc + kStride);
+        // column 2 t + b of n tile n is token blk + 4 (n >> 1) + (n & 1) + 2 b
+        const uint32_t ks[4] = {ksw.x, ksw.y, ksw.z, ksw.w};
+        float v[16];  // token blk + k
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            float sc[2 * NR];
+#pragma unroll
+            for (int i = 0; i < 2 * NR; ++i) sc[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const uint32_t w[4] = {kw[n][c].x, kw[n][c].y, kw[n][c].z, kw[n][c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t lo, hi;
+                    codes_f16(w[i], lo, hi);
+                    mma_rows_f16<NR>(sc, qa[c * 4 + i], lo, hi);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int k = 4 * (n >> 1) + (n & 1) + 2 * b;
+                const float f = e8m0_float(ks[n >> 1], k & 3);
+                float sum = 0.f;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float w = ex2(fmaf(sc[2 * r + b] * f, qscale[r], minus[r]));
+                    sum += blk + k < limit[r] ? w : 0.f;
+                }
+                v[k] = sum;
+            }
+        }
+        // over the eight lanes g, by halves of what is left
+#pragma unroll
+        for (int half = 8; half >= 2; half /= 2) {
+            const bool up = (g & (half / 2)) != 0;
+#pragma unroll
+            for (int k = 0; k < half; ++k) {
+                const float keep = up ? v[k + half] : v[k], give = up ? v[k] : v[k + half];
+                v[k] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * half);
+            }
+        }
+        if (j < stop) p.out[at + j] = old.x + (j < q.kv ? v[0] : 0.f);
+        if (j + 1 < stop) p.out[at + j + 1] = old.y + (j + 1 < q.kv ? v[1] : 0.f);
+    }
+    // the rest of the range (behind the last chunk that was written above)
+    const int done = end > j0 ? j0 + (end - j0 + kFewChunk - 1) / kFewChunk * kFewChunk : j0;
+    for (int j = done + threadIdx.x; j < stop; j += kScoreWarps * 32) p.out[at + j] = p.scores[at + j];
+}
 
 template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_rows_kernel(PagedScoreParams p) {
@@ -81,7 +196,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_rows_kernel(Pag
             for (int n = 0; n < 4; ++n) {
                 float sc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < CH * 4; ++k) mma_bf16(sc, qa[k], kb[n][k][0], kb[n][k][1]);
+                for (int k = 0; k < CH * 4; ++k) mma_rows_bf16<2>(sc, qa[k], kb[n][k][0], kb[n][k][1]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = j0 + 8 * n + 2 * t + (i & 1), r = i >> 1;
@@ -116,6 +231,21 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_rows_kernel(Pag
 
 template <int D>
 cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
+    const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
+    if (rows <= 16) {
+        // ranges of the cached tokens: several blocks on each SM, a step of every
+        // warp at least
+        const int step = kScoreWarps * kFewChunk;
+        const int64_t steps = (p.g.max_kv + step - 1) / step, lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
+        const int64_t want = std::min(steps, std::max<int64_t>(1, (152 * 24 + lists - 1) / lists));
+        const int range = static_cast<int>((steps + want - 1) / want) * step;
+        const dim3 grid((p.g.max_kv + range - 1) / range, p.g.kv_heads, p.g.seqs);
+        if (rows <= 8)
+            paged_scores_few_kernel<D, 1><<<grid, kScoreWarps * 32, 0, s>>>(p, range);
+        else
+            paged_scores_few_kernel<D, 2><<<grid, kScoreWarps * 32, 0, s>>>(p, range);
+        return cudaGetLastError();
+    }
     const int per = kScoreWarps * kScoreTokens;
     dim3 grid((p.g.max_kv + per - 1) / per, p.g.kv_heads, p.g.seqs);
     paged_scores_rows_kernel<D><<<grid, kScoreWarps * 32, 0, s>>>(p);

@@ -421,8 +421,8 @@ int rc_rope_axes(const rc_rope_plan *plan, const void *x, int64_t x_stride, void
  * two s with max |x| <= 448 s (s = 1 for a row of zeros; s between 2^-124 and
  * 2^7, so magnitudes over 57,344 saturate).  Code times scale is then an exact
  * bf16 number.  A row that holds an infinity or a NaN gets scale byte 255 and
- * zero codes, which read as NaN.  Scale bytes 135 .. 254 are not produced and
- * read as infinity.
+ * zero codes, which read as NaN.  Scale bytes under 3 and 135 .. 254 are not
+ * produced; tokens that have them read as some number, infinity or NaN.
  *
  * Metadata of a call (rc_paged_batch), device int32, read when the kernels run,
  * so a captured graph follows the values that are there at each replay:
