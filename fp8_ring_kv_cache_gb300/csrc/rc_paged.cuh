@@ -157,41 +157,26 @@ __device__ __forceinline__ int scale_exponent(float amax) {
     return amax == 0.f ? 0 : max(-124, min(7, e));
 }
 
-// D += A B, A a 16 x 16 row-major fragment, B 16 x 8, fp32 accumulators, for
-// 8 NR rows: with NR = 1 the fragment's rows 8 .. 15 are zero and take no registers.
-template <int NR>
-__device__ __forceinline__ void mma_rows_bf16(float (&d)[2 * NR], const uint32_t (&a)[2 * NR], uint32_t b0, uint32_t b1) {
-    if constexpr (NR == 2) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    } else {
-        float z0 = 0.f, z1 = 0.f;
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(z0), "+f"(z1)
-            : "r"(a[0]), "r"(0u), "r"(a[1]), "r"(b0), "r"(b1));
-    }
+// D += A B, A a 16 x 16 row-major fragment, B 16 x 8, fp32 accumulators.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <int NR>
-__device__ __forceinline__ void mma_rows_f16(float (&d)[2 * NR], const uint32_t (&a)[2 * NR], uint32_t b0, uint32_t b1) {
-    if constexpr (NR == 2) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    } else {
-        float z0 = 0.f, z1 = 0.f;
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(z0), "+f"(z1)
-            : "r"(a[0]), "r"(0u), "r"(a[1]), "r"(b0), "r"(b1));
-    }
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 tile of 16-bit numbers transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
 // Four E4M3 codes (code 0 in the low byte) as fp16, exactly: pairs (0, 1), (2, 3).
@@ -204,15 +189,17 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
         : "r"(w));
 }
 
-// Fragments of query rows for products with K's codes as fp16: 8 NR rows, each
-// divided by a power of two that puts its largest magnitude in [2^14, 2^15), so
-// that bf16's 8 bits are exact in fp16 down to 2^-32 of it (what is smaller
-// loses bits that are nothing beside the row's largest).  scale[r]: that power
-// times `factor`.  Product c * 4 + i of the lane (row lane / 4, t = lane % 4)
-// holds dims 16 (t + 4 c) + 4 i + {0, 1} and + {2, 3}, as codes_f16 gives them.
+// Query rows as the B operand of S^T = K Q^T with K's codes as fp16: 8 rows a
+// tile, row lane / 4 of tile r at row[r].  Each row is divided by a power of two
+// that puts its largest magnitude in [2^14, 2^15), so that bf16's 8 bits are
+// exact in fp16 down to 2^-32 of it (what is smaller loses bits that are nothing
+// beside the row's largest).  Product c * 4 + i of the lane (t = lane % 4) holds
+// dims 16 (t + 4 c) + 4 i + {0, 1} and + {2, 3}, as codes_f16 gives them.
+// scale[r][x]: that power times `factor` for row 2 t + x of tile r, the rows
+// whose scores the lane gets.
 template <int D, int NR>
-__device__ __forceinline__ void query_rows_f16(const __nv_bfloat16* const (&row)[NR], const bool (&live)[NR], float factor,
-                                               uint32_t (&qa)[D / 16][2 * NR], float (&scale)[NR]) {
+__device__ __forceinline__ void query_tile_f16(const __nv_bfloat16* const (&row)[NR], const bool (&live)[NR], float factor,
+                                               uint32_t (&qb)[NR][D / 16][2], float (&scale)[NR][2]) {
     const int t = threadIdx.x & 3;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -239,14 +226,16 @@ __device__ __forceinline__ void query_rows_f16(const __nv_bfloat16* const (&row)
         int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
         e = amax > 0.f && amax <= 3.4028235e38f ? max(-126, min(126, e)) : 0;
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        scale[r] = factor * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const float mine = factor * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) scale[r][x] = __shfl_sync(0xffffffffu, mine, 4 * (2 * t + x));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint32_t v = w[2 * k + x];
                 __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xFFFF0000u) * inv);
-                qa[k][x * NR + r] = *reinterpret_cast<uint32_t*>(&h);
+                qb[r][k][x] = *reinterpret_cast<uint32_t*>(&h);
             }
     }
 }

@@ -4,16 +4,21 @@
 // new tokens x the query heads that share it): bound by reading the codes, so
 // the warps read them straight into the registers where the matrix
 // instructions want them, with no shared memory and no barrier on the way.
-// A block has one (sequence, KV head, tile of 16 rows, split of the cached
-// tokens); a warp takes 64 cached tokens at a time:
-//   S = Q K^T   mma m16n8k16 in fp16: one conversion makes two codes exact fp16
-//               numbers, the rows of Q are scaled to fp16's range, and the
-//               tokens' scales (powers of two) multiply S.  A 16-byte piece of a
-//               K row is 16 of the summed dims for its token; which dims of the
-//               product they are is free as long as Q is held in the same order
-//   P = exp2(S - max), online; P's accumulator layout is the A operand of
-//   O += P V    in bf16, whose B operand is a 16-byte piece of a V row: 16 tokens
-//               of one dim, with their scales (which fp16 could not hold).  The tokens of S's columns are chosen to match.
+// A block has one (sequence, KV head, tile of 8 or 16 rows, split of the cached
+// tokens); a warp takes 64 cached tokens at a time, transposed, so that the few
+// rows are the short side of the products (m16n8k16):
+//   S^T = K Q^T  in fp16: one conversion makes two codes exact fp16 numbers, the
+//                rows of Q are scaled to fp16's range, and the tokens' scales
+//                (powers of two) multiply S.  A 16-byte piece of a K row is 16 of
+//                the summed dims for its token; which dims of the product they
+//                are is free as long as Q is held in the same order
+//   P = exp2(S - max), online; an 8 x 8 transpose of the accumulators makes them
+//                the B operand of
+//   O^T += V^T P^T  in bf16, whose A operand is a 16-byte piece of a V row: 16
+//                tokens of one dim, with their scales (which fp16 could not
+//                hold).  The tokens of S's rows are chosen to match.
+// Rows first (S = Q K^T) took twice the products and as many moves to keep the
+// unused half of the accumulators in place: 134 us for 32 single tokens.
 // The warps' (max, sum, O) are joined through shared memory; with several
 // splits they go to the workspace, and the block that arrives last at its row
 // tile's counter joins them in split order, so results do not depend on timing.
@@ -40,13 +45,12 @@ constexpr int part_floats() {
 // log2 units; -inf: the partial saw nothing).
 __device__ __forceinline__ float join_weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
 
-// 8 NR rows a block (NR 1 or 2): with eight the accumulators take half the
-// registers, and a third block fits an SM.
+// 8 NR rows a block (NR 1 or 2).
 template <int D, int NR>
 __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kernel(PagedAttnParams p) {
     constexpr int kRowTile = 8 * NR;
     constexpr int CH = D / 64;  // 16-byte pieces of a K row that a lane reads
-    constexpr int NT = D / 8;   // n tiles of O
+    constexpr int MT = D / 16;  // m tiles of O^T
     __shared__ __align__(16) float so[kRowsWarps][kRowTile][D + 4];
     __shared__ float sm[kRowsWarps][kRowTile], sl[kRowsWarps][kRowTile];
     __shared__ int last;
@@ -63,35 +67,46 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
     if (split >= nsplit) return;
     const int j0 = split * p.split_tokens, j1 = min(seen, j0 + p.split_tokens);
 
-    // the lane's rows g (and g + 8) of the tile: token, query head, tokens seen
-    int limit[NR];
-    const __nv_bfloat16* qrow[NR];
-    bool live[NR];
+    uint32_t qb[NR][D / 16][2];
+    float qscale[NR][2];
+    // of the rows 2 t + x of each eight, whose scores the lane gets: tokens seen
+    // (rows past the end see all; nothing of theirs is stored)
+    int limit[NR][2];
+    {
+        const __nv_bfloat16* qrow[NR];
+        bool live[NR];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const int r = tile * kRowTile + g + 8 * i;
-        live[i] = r < rows;
-        const int tok = live[i] ? r / p.group : 0, head = h * p.group + (live[i] ? r - tok * p.group : 0);
-        qrow[i] = p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D;
-        limit[i] = !live[i] ? 1 << 30 : p.causal ? max(0, q.kv - q.n + tok + 1) : q.kv;
+        for (int r = 0; r < NR; ++r) {
+            const int rr = tile * kRowTile + 8 * r + g;
+            live[r] = rr < rows;
+            const int tok = live[r] ? rr / p.group : 0, head = h * p.group + (live[r] ? rr - tok * p.group : 0);
+            qrow[r] = p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D;
+            const int lim = !live[r] ? 1 << 30 : p.causal ? max(0, q.kv - q.n + tok + 1) : q.kv;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) limit[r][x] = __shfl_sync(0xffffffffu, lim, 4 * (2 * t + x));
+        }
+        query_tile_f16<D, NR>(qrow, live, p.sm_log2, qb, qscale);
     }
-    uint32_t qa[CH * 4][2 * NR];
-    float qscale[NR];
-    query_rows_f16<D, NR>(qrow, live, p.sm_log2, qa, qscale);
+    int least = j1;  // what every row sees
+#pragma unroll
+    for (int r = 0; r < NR; ++r) least = min(least, min(limit[r][0], limit[r][1]));
+    least = __reduce_min_sync(0xffffffffu, least);
 
-    float o[NT][2 * NR];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2 * NR; ++i) o[n][i] = 0.f;
-    float m_run[NR], l_run[NR];
+    float o[NR][MT][4];
+    float m_run[NR][2], l_run[NR][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-        m_run[r] = -INFINITY;
-        l_run[r] = 0.f;
+#pragma unroll
+        for (int n = 0; n < MT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[r][n][i] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            m_run[r][x] = -INFINITY;
+            l_run[r][x] = 0.f;
+        }
     }
     const int P = 1 << p.g.page_shift;
-
     // Lane l < 4 of each four reads the page of the chunk's block l of 16 tokens a
     // chunk ahead.
     const uint32_t* table =
@@ -103,173 +118,205 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
     constexpr int kStride = kRowsWarps * kChunk;
     int ahead = entry(j0 + warp * kChunk);
     for (int jc = j0 + warp * kChunk; jc < j1; jc += kStride) {
-        // The lane reads K rows of the 16-token block g >> 1 and V pieces and
-        // scales of block t.  A block behind the sequence's end, or on a bad
-        // page, is read from page 0 instead, and its tokens are cut off (K) or
-        // given the factor 0 (V).
-        const int vblk = jc + 16 * t;
+        // The lane reads K rows and scales of the 16-token block g >> 1 and V
+        // pieces and scales of block t.  A block behind the sequence's end, or on
+        // a bad page, is read from page 0 instead, and its tokens are cut off (K)
+        // or given the factor 0 (V).
+        const int vblk = jc + 16 * t, kblk = jc + 16 * (g >> 1);
         const bool vok = vblk < q.kv && check_page(p.g, ahead);
         const uint32_t mine = static_cast<uint32_t>(vok ? ahead : 0);
         const size_t vph = static_cast<size_t>(mine) * p.g.kv_heads + h;
         const size_t kph = static_cast<size_t>(__shfl_sync(0xffffffffu, mine, g >> 1)) * p.g.kv_heads + h;
-        const int koff = (jc + 16 * (g >> 1)) & (P - 1), voff = vblk & (P - 1);
+        const int koff = kblk & (P - 1), voff = vblk & (P - 1);
         const uint8_t* kp = p.g.kcodes + (kph * P + koff + 2 * (g & 1)) * D + 16 * t;
         const uint8_t* vp = p.g.vcodes + (vph * D + g) * P + voff;
         ahead = entry(jc + kStride);
 
-        // S: column 2t + b of n tile (i, ab) is token 16 t + 4 i + ab + 2 b, so
-        // the lane's K row for it is token 16 (g >> 1) + 4 i + ab + 2 (g & 1)
-        float sc[8][2 * NR];
-        uint4 kw[8][CH];
+        // m tile i of S^T: its row g is token kblk + 4 i + 2 (g & 1), its row g + 8 the next one
+        uint4 kw[4][2][CH];
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int c = 0; c < CH; ++c) kw[n][c] = ldg_nc_na_v4(kp + (4 * (n >> 1) + (n & 1)) * D + 64 * c);
-        const uint4 ksw = ldg_nc_na_v4(p.g.kscale + vph * P + voff);
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) kw[i][x][c] = ldg_nc_na_v4(kp + (4 * i + x) * D + 64 * c);
+        const uint4 ksw = ldg_nc_na_v4(p.g.kscale + kph * P + koff);
         const uint4 vsw = ldg_nc_na_v4(p.g.vscale + vph * P + voff);
         // the first half of the V pieces is on its way while S is computed, the
         // second while the softmax runs
-        uint4 vw[NT];
+        uint4 vw[MT][2];
 #pragma unroll
-        for (int n = 0; n < NT / 2; ++n) vw[n] = ldg_nc_na_v4(vp + static_cast<size_t>(8 * n) * P);
+        for (int n = 0; n < MT / 2; ++n)
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-#pragma unroll
-            for (int i = 0; i < 2 * NR; ++i) sc[n][i] = 0.f;
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const uint32_t w[4] = {kw[n][c].x, kw[n][c].y, kw[n][c].z, kw[n][c].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t lo, hi;
-                    codes_f16(w[i], lo, hi);
-                    mma_rows_f16<NR>(sc[n], qa[c * 4 + i], lo, hi);
-                }
-            }
-        }
-#pragma unroll
-        for (int n = NT / 2; n < NT; ++n) vw[n] = ldg_nc_na_v4(vp + static_cast<size_t>(8 * n) * P);
-
-        // softmax: the lane's columns are the 16 tokens of block t
-        int room = j1 - jc;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) room = min(room, limit[r] - jc);
-        const bool full = __all_sync(0xffffffffu, room >= kChunk);
-        const uint32_t ks[4] = {ksw.x, ksw.y, ksw.z, ksw.w};
-        float mx[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) mx[r] = -INFINITY;
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int byte = (n & 1) + 2 * b;  // of word n >> 1: the column's token
-                const float f = e8m0_float(ks[n >> 1], byte);
-                const int j = jc + 16 * t + 4 * (n >> 1) + byte;
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    float x = sc[n][2 * r + b] * f;
-                    if (!full && (j >= limit[r] || j >= j1)) x = -INFINITY;
-                    sc[n][2 * r + b] = x;
-                    mx[r] = fmaxf(mx[r], x);
-                }
-            }
-        float alpha[NR], base[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-            const float m_new = fmaxf(m_run[r], mx[r] * qscale[r]);
-            base[r] = m_new == -INFINITY ? 0.f : m_new;
-            alpha[r] = ex2(m_run[r] - base[r]);  // 0 while nothing was seen
-            m_run[r] = m_new;
-        }
-        float sum[NR];
-        bool moved = false;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            sum[r] = 0.f;
-            moved |= alpha[r] != 1.f;
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int i = 0; i < 2 * NR; ++i) {
-                sc[n][i] = ex2(fmaf(sc[n][i], qscale[i >> 1], -base[i >> 1]));
-                sum[i >> 1] += sc[n][i];
-            }
-#pragma unroll
-        for (int r = 0; r < NR; ++r) l_run[r] = l_run[r] * alpha[r] + sum[r];
-        if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 2 * NR; ++i) o[n][i] *= alpha[i >> 1];
-        }
-        // the V pieces' 16 tokens: factors by word, 0 for tokens the sequence does not have
-        uint32_t vf[8];
-        const uint32_t vs[4] = {vsw.x, vsw.y, vsw.z, vsw.w};
-        // A token whose V is not a number must reach the rows that see it and
-        // no other, so that is moved from V (0 x NaN would reach every row)
-        // into the weights; they are of the same 16 tokens as the V pieces.
-        uint32_t nans = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) nans |= __vcmpgtu4(vs[i], 0x86868686u);
-        const bool special = __any_sync(0xffffffffu, nans != 0) || !full;
-        if (special) {
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 2 * NR; ++i) {
-                    const int byte = (n & 1) + 2 * (i & 1);
-                    const int j = jc + 16 * t + 4 * (n >> 1) + byte;
-                    if (((vs[n >> 1] >> (8 * byte)) & 0xffu) > 134u && j < limit[i >> 1] && j < j1)
-                        sc[n][i] = __uint_as_float(0x7fc00000u);
-                }
-        }
+            for (int x = 0; x < 2; ++x) vw[n][x] = ldg_nc_na_v4(vp + static_cast<size_t>(16 * n + 8 * x) * P);
+        float sc[NR][4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[r][i][k] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const uint32_t wa[4] = {kw[i][0][c].x, kw[i][0][c].y, kw[i][0][c].z, kw[i][0][c].w};
+                const uint32_t wb[4] = {kw[i][1][c].x, kw[i][1][c].y, kw[i][1][c].z, kw[i][1][c].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t a[4];
+                    codes_f16(wa[k], a[0], a[2]);
+                    codes_f16(wb[k], a[1], a[3]);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) mma_f16(sc[r][i], a, qb[r][c * 4 + k][0], qb[r][c * 4 + k][1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = MT / 2; n < MT; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) vw[n][x] = ldg_nc_na_v4(vp + static_cast<size_t>(16 * n + 8 * x) * P);
+
+        // softmax: scores 2 a + x of m tile i: token kblk + 4 i + 2 (g & 1) + a, row 2 t + x
+        const bool full = jc + kChunk <= least;
+        const uint32_t ks[4] = {ksw.x, ksw.y, ksw.z, ksw.w};
+        float mx[NR][2];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) mx[r][0] = mx[r][1] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const float f = e8m0_float(ks[i] >> (16 * (g & 1)), a);
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) sc[r][i][2 * a + x] *= f;
+            }
+        if (!full) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const int j = kblk + 4 * i + 2 * (g & 1) + a;
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (j >= limit[r][x] || j >= j1) sc[r][i][2 * a + x] = -INFINITY;
+                }
+        }
+        bool moved = false;
+        float base[NR][2], alpha[NR][2];
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[r][x] = max3(mx[r][x], sc[r][i][x], sc[r][i][2 + x]);
+                mx[r][x] = fmaxf(mx[r][x], __shfl_xor_sync(0xffffffffu, mx[r][x], 4));
+                mx[r][x] = fmaxf(mx[r][x], __shfl_xor_sync(0xffffffffu, mx[r][x], 8));
+                mx[r][x] = fmaxf(mx[r][x], __shfl_xor_sync(0xffffffffu, mx[r][x], 16));
+                const float m_new = fmaxf(m_run[r][x], mx[r][x] * qscale[r][x]);
+                base[r][x] = m_new == -INFINITY ? 0.f : m_new;
+                alpha[r][x] = ex2(m_run[r][x] - base[r][x]);  // 0 while nothing was seen
+                m_run[r][x] = m_new;
+                moved |= alpha[r][x] != 1.f;
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        const float w = ex2(fmaf(sc[r][i][2 * a + x], qscale[r][x], -base[r][x]));
+                        sc[r][i][2 * a + x] = w;
+                        sum += w;
+                    }
+                l_run[r][x] = l_run[r][x] * alpha[r][x] + sum;
+            }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int n = 0; n < MT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[r][n][i] *= alpha[r][i & 1];
+        }
+        // the V pieces' 16 tokens: factors by word
+        uint32_t vf[8];
+        const uint32_t vs[4] = {vsw.x, vsw.y, vsw.z, vsw.w};
+        uint32_t nans = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            nans |= __vcmpgtu4(vs[i], 0x86868686u);
             vf[2 * i] = factors02(vs[i]);
             vf[2 * i + 1] = factors13(vs[i]);
         }
-        if (special || __any_sync(0xffffffffu, !vok)) {
+        if (!full || __any_sync(0xffffffffu, nans != 0 || !vok)) {
+            // factor 0 for tokens the sequence does not have.  A token whose V is
+            // not a number must reach the rows that see it and no other, so that
+            // is moved from V (0 x NaN would reach every row) into the weights.
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t good = vs[i] & ~__vcmpgtu4(vs[i], 0x86868686u);
                 const int left = vok ? q.kv - (vblk + 4 * i) : 0;  // tokens of the word that exist
                 vf[2 * i] = factors02(good) & ((left > 0 ? 0xffffu : 0u) | (left > 2 ? 0xffff0000u : 0u));
                 vf[2 * i + 1] = factors13(good) & ((left > 1 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u));
+                // the scores' tokens are of block g >> 1, which lane g >> 1 has the scales of
+                const uint32_t theirs = __shfl_sync(0xffffffffu, vs[i], g >> 1);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const int j = kblk + 4 * i + 2 * (g & 1) + a;
+                    if (((theirs >> (8 * (2 * (g & 1) + a))) & 0xffu) > 134u) {
+#pragma unroll
+                        for (int r = 0; r < NR; ++r)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                if (j < limit[r][x] && j < j1) sc[r][i][2 * a + x] = __uint_as_float(0x7fc00000u);
+                    }
+                }
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // products over tokens 16 t + 4 i + {0, 2} (n tile (i, 0)) and + {1, 3} (n tile (i, 1))
-            uint32_t pa[2 * NR];
+            // products over tokens 16 t + 4 i + {0, 2} and + {1, 3} of the chunk
+            uint32_t pb[NR][2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int r = 0; r < NR; ++r)
 #pragma unroll
-                for (int r = 0; r < NR; ++r) pa[x * NR + r] = pack_bf16(sc[2 * i + x][2 * r], sc[2 * i + x][2 * r + 1]);
+                for (int a = 0; a < 2; ++a) pb[r][a] = transpose8(pack_bf16(sc[r][i][2 * a], sc[r][i][2 * a + 1]));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint32_t w = i == 0 ? vw[n].x : i == 1 ? vw[n].y : i == 2 ? vw[n].z : vw[n].w;
-                mma_rows_bf16<NR>(o[n], pa, bf2_mul(codes02(w), vf[2 * i]), bf2_mul(codes13(w), vf[2 * i + 1]));
+            for (int n = 0; n < MT; ++n) {
+                uint32_t a[4];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t w = i == 0 ? vw[n][x].x : i == 1 ? vw[n][x].y : i == 2 ? vw[n][x].z : vw[n][x].w;
+                    a[x] = bf2_mul(codes02(w), vf[2 * i]);
+                    a[2 + x] = bf2_mul(codes13(w), vf[2 * i + 1]);
+                }
+#pragma unroll
+                for (int r = 0; r < NR; ++r) mma_bf16(o[r][n], a, pb[r][0], pb[r][1]);
             }
         }
     }
 
     // ---- join the warps
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
-        l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
-        if (t == 0) {
-            sm[warp][g + 8 * r] = m_run[r];
-            sl[warp][g + 8 * r] = l_run[r];
-        }
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            *reinterpret_cast<float2*>(&so[warp][g + 8 * r][8 * n + 2 * t]) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
-    }
+        for (int x = 0; x < 2; ++x) {
+            float l = l_run[r][x];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const int row = 8 * r + 2 * t + x;
+            if (g == 0) {
+                sm[warp][row] = m_run[r][x];
+                sl[warp][row] = l;
+            }
+#pragma unroll
+            for (int n = 0; n < MT; ++n) {
+                so[warp][row][16 * n + g] = o[r][n][x];
+                so[warp][row][16 * n + 8 + g] = o[r][n][2 + x];
+            }
+        }
     __syncthreads();
     const int rows_here = min(kRowTile, rows - tile * kRowTile);
     const int slot = (s * p.row_tiles + tile) * p.g.kv_heads + h;

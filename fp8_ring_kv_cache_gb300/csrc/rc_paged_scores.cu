@@ -4,8 +4,8 @@
 // paged_scores_few_kernel, for one tile of query rows (a decode step): bound by
 // reading the K codes.  The rows stay in registers while the warps go over the
 // cached tokens 64 at a time, reading K pieces straight into the fp16 products'
-// operands as the attention does; the eight lanes that hold a token's rows add
-// up by halves, so that each ends with the sums of two tokens.
+// operands as the attention does; the four lanes that hold a token's rows add up
+// by halves, so that each ends with the sums of two tokens.
 // paged_scores_rows_kernel, for some tiles of rows.
 // A warp owns 32 cached tokens of one (sequence, KV head), decodes their K rows
 // to bf16 once, into the registers where the matrix instructions want them, and
@@ -37,23 +37,27 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_few_kernel(Page
     const int64_t at = (static_cast<int64_t>(s) * p.g.kv_heads + h) * p.score_stride;
     const int end = rows > 0 ? min(stop, q.kv) : j0;  // tokens from here on keep their scores
     constexpr int kStride = kScoreWarps * kFewChunk;
-    uint32_t qa[D / 16][2 * NR];
-    float qscale[NR], minus[NR];
-    int limit[NR];
+    uint32_t qb[NR][D / 16][2];
+    float qscale[NR][2], minus[NR][2];  // of rows 2 t + x, whose scores the lane gets
+    int limit[NR][2];
     if (j0 < end) {
         const __nv_bfloat16* qrow[NR];
         bool live[NR];
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            const int r = g + 8 * i;
-            live[i] = r < rows;
-            const int tok = live[i] ? r / p.group : 0, head = h * p.group + (live[i] ? r - tok * p.group : 0);
-            qrow[i] = p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D;
-            const float lse = live[i] ? __ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head) : -INFINITY;
-            minus[i] = -lse * 1.4426950408889634f;
-            limit[i] = lse == -INFINITY ? 0 : p.causal ? q.kv - q.n + tok + 1 : q.kv;
+        for (int r = 0; r < NR; ++r) {
+            const int rr = 8 * r + g;
+            live[r] = rr < rows;
+            const int tok = live[r] ? rr / p.group : 0, head = h * p.group + (live[r] ? rr - tok * p.group : 0);
+            qrow[r] = p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D;
+            const float lse = live[r] ? __ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head) : -INFINITY;
+            const int lim = lse == -INFINITY ? 0 : p.causal ? q.kv - q.n + tok + 1 : q.kv;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                minus[r][x] = -__shfl_sync(0xffffffffu, lse, 4 * (2 * t + x)) * 1.4426950408889634f;
+                limit[r][x] = __shfl_sync(0xffffffffu, lim, 4 * (2 * t + x));
+            }
         }
-        query_rows_f16<D, NR>(qrow, live, p.sm_log2, qa, qscale);
+        query_tile_f16<D, NR>(qrow, live, p.sm_log2, qb, qscale);
     }
     const int P = 1 << p.g.page_shift;
     const uint32_t* table =
@@ -69,62 +73,76 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_few_kernel(Page
         const int blk = jc + 16 * t;
         const uint32_t mine = static_cast<uint32_t>(blk < q.kv && check_page(p.g, ahead) ? ahead : 0);
         const size_t kph = static_cast<size_t>(__shfl_sync(0xffffffffu, mine, g >> 1)) * p.g.kv_heads + h;
-        const int koff = (jc + 16 * (g >> 1)) & (P - 1);
+        const int kblk = jc + 16 * (g >> 1), koff = kblk & (P - 1);
         const uint8_t* kp = p.g.kcodes + (kph * P + koff + 2 * (g & 1)) * D + 16 * t;
-        uint4 kw[8][CH];
+        // m tile i of S^T: its row g is token kblk + 4 i + 2 (g & 1), its row g + 8 the next one
+        uint4 kw[4][2][CH];
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int c = 0; c < CH; ++c) kw[n][c] = ldg_nc_na_v4(kp + (4 * (n >> 1) + (n & 1)) * D + 64 * c);
-        const uint4 ksw = ldg_nc_na_v4(p.g.kscale + (static_cast<size_t>(mine) * p.g.kv_heads + h) * P + (blk & (P - 1)));
-        const int j = blk + 2 * g;  // the lane's tokens in the end
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) kw[i][x][c] = ldg_nc_na_v4(kp + (4 * i + x) * D + 64 * c);
+        const uint4 ksw = ldg_nc_na_v4(p.g.kscale + kph * P + koff);
+        const int j = kblk + 4 * t + 2 * (g & 1);  // the lane's tokens in the end: j, j + 1
         float2 old = make_float2(0.f, 0.f);
         if (j < stop) old.x = __ldcg(p.scores + at + j);
         if (j + 1 < stop) old.y = __ldcg(p.scores + at + j + 1);
         ahead = entry(jc + kStride);
-        // column 2 t + b of n tile n is token blk + 4 (n >> 1) + (n & 1) + 2 b
         const uint32_t ks[4] = {ksw.x, ksw.y, ksw.z, ksw.w};
-        float v[16];  // token blk + k
+        float v[4][2];  // tokens kblk + 4 i + 2 (g & 1) + a: sums over the lane's rows
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            float sc[2 * NR];
+        for (int i = 0; i < 4; ++i) {
+            float sc[NR][4];
 #pragma unroll
-            for (int i = 0; i < 2 * NR; ++i) sc[i] = 0.f;
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[r][k] = 0.f;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const uint32_t w[4] = {kw[n][c].x, kw[n][c].y, kw[n][c].z, kw[n][c].w};
+                const uint32_t wa[4] = {kw[i][0][c].x, kw[i][0][c].y, kw[i][0][c].z, kw[i][0][c].w};
+                const uint32_t wb[4] = {kw[i][1][c].x, kw[i][1][c].y, kw[i][1][c].z, kw[i][1][c].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t lo, hi;
-                    codes_f16(w[i], lo, hi);
-                    mma_rows_f16<NR>(sc, qa[c * 4 + i], lo, hi);
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t x[4];
+                    codes_f16(wa[k], x[0], x[2]);
+                    codes_f16(wb[k], x[1], x[3]);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) mma_f16(sc[r], x, qb[r][c * 4 + k][0], qb[r][c * 4 + k][1]);
                 }
             }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int k = 4 * (n >> 1) + (n & 1) + 2 * b;
-                const float f = e8m0_float(ks[n >> 1], k & 3);
-                float sum = 0.f;
+            for (int a = 0; a < 2; ++a) {
+                const float f = e8m0_float(ks[i] >> (16 * (g & 1)), a);
+                const int token = kblk + 4 * i + 2 * (g & 1) + a;
+                v[i][a] = 0.f;
 #pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const float w = ex2(fmaf(sc[2 * r + b] * f, qscale[r], minus[r]));
-                    sum += blk + k < limit[r] ? w : 0.f;
-                }
-                v[k] = sum;
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float w = ex2(fmaf(sc[r][2 * a + x] * f, qscale[r][x], minus[r][x]));
+                        v[i][a] += token < limit[r][x] ? w : 0.f;
+                    }
             }
         }
-        // over the eight lanes g, by halves of what is left
+        // over the four lanes t, by halves of what is left: lane t ends with m tile t
+        float u[2][2], z[2];
 #pragma unroll
-        for (int half = 8; half >= 2; half /= 2) {
-            const bool up = (g & (half / 2)) != 0;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int k = 0; k < half; ++k) {
-                const float keep = up ? v[k + half] : v[k], give = up ? v[k] : v[k + half];
-                v[k] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * half);
+            for (int a = 0; a < 2; ++a) {
+                const bool up = (t & 2) != 0;
+                const float keep = up ? v[2 + i][a] : v[i][a], give = up ? v[i][a] : v[2 + i][a];
+                u[i][a] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
             }
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const bool up = (t & 1) != 0;
+            const float keep = up ? u[1][a] : u[0][a], give = up ? u[0][a] : u[1][a];
+            z[a] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
         }
-        if (j < stop) p.out[at + j] = old.x + (j < q.kv ? v[0] : 0.f);
-        if (j + 1 < stop) p.out[at + j + 1] = old.y + (j + 1 < q.kv ? v[1] : 0.f);
+        if (j < stop) p.out[at + j] = old.x + (j < q.kv ? z[0] : 0.f);
+        if (j + 1 < stop) p.out[at + j + 1] = old.y + (j + 1 < q.kv ? z[1] : 0.f);
     }
     // the rest of the range (behind the last chunk that was written above)
     const int done = end > j0 ? j0 + (end - j0 + kFewChunk - 1) / kFewChunk * kFewChunk : j0;
@@ -196,7 +214,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_rows_kernel(Pag
             for (int n = 0; n < 4; ++n) {
                 float sc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < CH * 4; ++k) mma_rows_bf16<2>(sc, qa[k], kb[n][k][0], kb[n][k][1]);
+                for (int k = 0; k < CH * 4; ++k) mma_bf16(sc, qa[k], kb[n][k][0], kb[n][k][1]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = j0 + 8 * n + 2 * t + (i & 1), r = i >> 1;
