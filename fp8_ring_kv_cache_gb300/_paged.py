@@ -109,17 +109,26 @@ def _positions(t, axes, n, what: str, device) -> tuple[int, int]:
     return t.data_ptr(), st[0] if axes > 1 else n
 
 
+# the raw handle of a device's current stream, and the current device, without the
+# wrapper objects of torch.cuda (a fifth of a short call's time on the host)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(device, stream, what: str, fn, *args) -> None:
     """Call fn(*args, stream) with `device` current."""
+    index = device.index
     if stream is None:
-        sp = torch.cuda.current_stream(device).cuda_stream
+        sp = _raw_stream(index)
     else:
         sp = stream if isinstance(stream, int) else stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, sp), what)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, sp)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, sp), what)
+            st = fn(*args, sp)
+    if st:
+        _check(st, what)
 
 
 class RopeAxes:
@@ -150,19 +159,14 @@ def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, 
         out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
     op, os_ = _rows(out, x.dtype, n, heads, dim, "out", x.device)
     pp, ps = _positions(positions, rope.axes, n, "positions", x.device)
-    if out is not x and n and _overlap(x, out) and not (xp == op and xs == os_):
-        raise ValueError("out overlaps x without being x")
+    if out is not x and (xp != op or xs != os_):
+        size = x.element_size()  # spans of memory from the first to the last token's end
+        xe, oe = xp + ((n - 1) * xs + heads * dim) * size, op + ((n - 1) * os_ + heads * dim) * size
+        if xp < oe and op < xe and n:
+            raise ValueError("out overlaps x without being x")
     _call(x.device, stream, "rc_rope_axes", lib.rc_rope_axes, rope._ptr, xp, xs, op, os_,
           RC_BF16 if x.dtype == torch.bfloat16 else RC_F32, n, heads, pp, ps, 1 if inverse else 0)
     return out
-
-
-def _overlap(a, b) -> bool:
-    """Whether the spans of memory from a tensor's first to its last element meet."""
-    def span(t):
-        return t.data_ptr(), t.data_ptr() + (sum((s - 1) * st for s, st in zip(t.shape, t.stride())) + 1) * t.element_size()
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
 
 
 class PagedBatch:

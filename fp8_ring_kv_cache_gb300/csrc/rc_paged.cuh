@@ -15,6 +15,16 @@ struct RopePlanDev {
     uint8_t axis[kMaxHalfDim];
 };
 
+// A generic address of a kernel's (__grid_constant__) parameter bytes, whose
+// origin the compiler does not see: lanes that read different entries of an
+// array there go through the data cache together, where the constant bank
+// would serve one address at a time (4 us of the 22 us that a chunk's write took).
+template <typename T>
+__device__ __forceinline__ const T* param_address(const T* p) {
+    asm volatile("mov.b64 %0, %0;" : "+l"(p));
+    return p;
+}
+
 struct PagedParams {
     uint8_t* kcodes;
     uint8_t* vcodes;

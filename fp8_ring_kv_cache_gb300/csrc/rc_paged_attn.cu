@@ -399,7 +399,7 @@ cudaError_t launch_rows(PagedAttnParams& p, size_t part_floats_max, int max_coun
     // step of every warp each, at most 32 (the last block reads them all), and
     // as many as the workspace holds.
     const int step = kRowsWarps * kChunk;
-    int64_t want = (152 * 12 + slots - 1) / slots;
+    int64_t want = (152 * 24 + slots - 1) / slots;
     want = std::min<int64_t>(want, 32);
     want = std::min<int64_t>(want, (p.g.max_kv + step - 1) / step);
     want = std::min<int64_t>(want, static_cast<int64_t>(part_floats_max / (slots * part_floats<D, NR>())));

@@ -255,7 +255,7 @@ cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
         // warp at least
         const int step = kScoreWarps * kFewChunk;
         const int64_t steps = (p.g.max_kv + step - 1) / step, lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
-        const int64_t want = std::min(steps, std::max<int64_t>(1, (152 * 24 + lists - 1) / lists));
+        const int64_t want = std::min(steps, std::max<int64_t>(1, (152 * 12 + lists - 1) / lists));
         const int range = static_cast<int>((steps + want - 1) / want) * step;
         const dim3 grid((p.g.max_kv + range - 1) / range, p.g.kv_heads, p.g.seqs);
         if (rows <= 8)

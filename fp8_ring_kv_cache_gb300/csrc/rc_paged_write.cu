@@ -42,7 +42,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint2& codes) 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRun* D / 8) paged_write_kernel(PagedWriteParams p, int runs, int heads_per_block) {
+__global__ void __launch_bounds__(kRun* D / 8) paged_write_kernel(const __grid_constant__ PagedWriteParams p, int runs, int heads_per_block) {
     constexpr int LANES = D / 8;  // of one token
     constexpr int kThreads = kRun * LANES;
     constexpr int kRow = D + 16;  // a token's staged codes: 16-byte aligned, rows spread over the banks
@@ -67,11 +67,11 @@ __global__ void __launch_bounds__(kRun* D / 8) paged_write_kernel(PagedWritePara
     const int row = q.q0 + (live ? index - first : 0);
 
     float2 cs[4];
+    const uint64_t* turns = param_address(p.rope.turns) + 4 * c;
+    const uint32_t axes = *reinterpret_cast<const uint32_t*>(param_address(p.rope.axis) + 4 * c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int pair = 4 * c + i;
-        cs[i] = turn_cos_sin(__ldg(p.pos + p.rope.axis[pair] * p.pos_stride + row), p.rope.turns[pair]);
-    }
+    for (int i = 0; i < 4; ++i)
+        cs[i] = turn_cos_sin(__ldg(p.pos + ((axes >> (8 * i)) & 0xffu) * p.pos_stride + row), turns[i]);
     const __nv_bfloat16* kr = p.K + row * p.k_stride + c * 8;
     const __nv_bfloat16* vr = p.V + row * p.v_stride + c * 8;
     const int h0 = blockIdx.y * heads_per_block, h1 = min(p.g.kv_heads, h0 + heads_per_block);

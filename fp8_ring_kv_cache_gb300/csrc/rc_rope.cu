@@ -36,22 +36,15 @@ __device__ __forceinline__ uint4 turn_piece(uint4 w, const float2* cs, float sig
 constexpr int kRopeMaxTokens = 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(RopeAxesParams p, int tb) {
+__global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_constant__ RopeAxesParams p, int tb) {
     constexpr int kPairs = D / 2;
     constexpr int kValues = 16 / sizeof(T);  // of one piece
     constexpr int kUnroll = 4;
     __shared__ float2 table[kRopeMaxTokens][kPairs];
-    __shared__ uint64_t turns[kPairs];
-    __shared__ uint8_t axis[kPairs];
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tb;
     const int nt = static_cast<int>(min(static_cast<int64_t>(tb), p.n - t0));
-    // through shared memory: lanes index different entries, which the
-    // parameter bank would serve one address at a time
-    if (threadIdx.x < kPairs) {
-        turns[threadIdx.x] = p.rope.turns[threadIdx.x];
-        axis[threadIdx.x] = p.rope.axis[threadIdx.x];
-    }
-    __syncthreads();
+    const uint64_t* turns = param_address(p.rope.turns);
+    const uint8_t* axis = param_address(p.rope.axis);
     for (int i = threadIdx.x; i < nt * kPairs; i += kRopeThreads) {
         const int t = i / kPairs, c = i % kPairs;
         table[t][c] = turn_cos_sin(__ldg(p.pos + axis[c] * p.pos_stride + t0 + t), turns[c]);
