@@ -2,15 +2,19 @@
 // weight.
 //
 // paged_select_kernel: one block per (sequence, KV head) finds the budget's
-//    threshold among the scores by radix selection, 8 bits of the ordered key a
-//    pass (the keys stay in shared memory while they fit), then lists the kept
-//    indices in ascending order: each warp counts in its own run of scores with
-//    ballots, the counts are summed over the warps, and each warp writes its
-//    run.  Ties at the threshold go to the lowest index.
+//    threshold among the scores by radix selection, 11, 11 and 10 bits of the
+//    ordered key a pass (the keys stay in shared memory while they fit; the
+//    first pass then tells four sizes an octave apart, so that few lanes meet
+//    in one counter), then lists the kept indices in ascending order: each warp
+//    counts in its own run of scores with ballots, the counts are summed over
+//    the warps, and each warp writes its run.  Ties at the threshold go to the
+//    lowest index.
 // paged_gather_kernel: copies the kept tokens to the new pages: bound by
-//    memory.  K rows go 16 bytes a thread; a V row's codes (one per token) go
-//    a byte a lane, 32 kept tokens side by side, so that the loads of a warp
-//    fall into few sectors and its stores into one.
+//    memory.  K rows go 16 bytes a thread.  A V row has one byte per token: for
+//    16 kept tokens at a time the 16-byte pieces that hold them (at most 16,
+//    usually three or four) are brought to shared memory for every dim, the
+//    bytes are picked there, and rows of 64 go out.  (Single bytes from and to
+//    global memory, 32 tokens side by side, took 132 us for 64 lists of 8,192.)
 #include <algorithm>
 
 #include "rc_paged.cuh"
@@ -21,7 +25,8 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kHistCopies = 8;           // histograms a lane group has to itself: neighbours often share a bin
+constexpr int kBins = 2048;
+constexpr int kHistCopies = 2;           // histograms that even and odd lanes have to themselves
 constexpr int kSelCap = 48 * 1024;       // keys kept in shared memory
 
 // Order-preserving key: larger score, larger key; -0 as +0, NaN above all.
@@ -42,8 +47,8 @@ __device__ __forceinline__ int evict_len(const PagedParams& g, int s) {
 
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictParams p, int cap) {
     extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist[kHistCopies][256];
-    __shared__ uint32_t s_prefix, s_want;
+    __shared__ uint32_t hist[kHistCopies][kBins];
+    __shared__ uint32_t s_sum[kSelWarps], s_prefix, s_want;
     __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x, s = blockIdx.y;
@@ -72,41 +77,41 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
     auto key = [&](int i) { return staged ? keys[i] : score_key(__ldg(sc + i)); };
     // ---- the want-th largest key
     uint32_t prefix = 0, left = want;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < kHistCopies * 256; i += kSelThreads) hist[i >> 8][i & 255] = 0;
+    constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? kShift[0] : pass == 1 ? kShift[1] : kShift[2];
+        const int bits = pass == 2 ? kBits[2] : kBits[0];
+        for (int i = tid; i < kHistCopies * kBins; i += kSelThreads) hist[i / kBins][i % kBins] = 0;
         __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+        const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
         for (int i = tid; i < cand; i += kSelThreads) {
             const uint32_t k = key(i);
-            if ((k & mask) == prefix) atomicAdd(&hist[lane & (kHistCopies - 1)][(k >> shift) & 255u], 1u);
+            if ((k & mask) == prefix) atomicAdd(&hist[lane & (kHistCopies - 1)][(k >> shift) & ((1u << bits) - 1u)], 1u);
         }
         __syncthreads();
-        if (warp == 0) {
-            // lane l: bins 255 - 8 l down to 248 - 8 l
-            uint32_t c[8], sum = 0;
+        // thread l: bins 2047 - 2 l and 2046 - 2 l, the highest first
+        uint32_t c[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = 0;
-                for (int k = 0; k < kHistCopies; ++k) c[i] += hist[k][255 - 8 * lane - i];
-                sum += c[i];
-            }
-            uint32_t above = sum;
+        for (int i = 0; i < 2; ++i) c[i] = hist[0][kBins - 1 - 2 * tid - i] + hist[1][kBins - 1 - 2 * tid - i];
+        uint32_t above = c[0] + c[1];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, above, o);
-                if (lane >= o) above += v;
-            }
-            above -= sum;  // keys in higher bins
-            if (above < left && left <= above + sum) {
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, above, o);
+            if (lane >= o) above += v;
+        }
+        if (lane == 31) s_sum[warp] = above;
+        __syncthreads();
+        uint32_t before = lane < warp ? s_sum[lane] : 0u;
+        before = __reduce_add_sync(0xffffffffu, before);
+        above += before - (c[0] + c[1]);  // keys in higher bins
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (above < left && left <= above + c[i]) {
-                        s_prefix = prefix | (static_cast<uint32_t>(255 - 8 * lane - i) << shift);
-                        s_want = left - above;
-                    }
-                    above += c[i];
-                }
+        for (int i = 0; i < 2; ++i) {
+            if (above < left && left <= above + c[i]) {
+                s_prefix = prefix | (static_cast<uint32_t>(kBins - 1 - 2 * tid - i) << shift);
+                s_want = left - above;
             }
+            above += c[i];
         }
         __syncthreads();
         prefix = s_prefix;
@@ -152,11 +157,17 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
 
 constexpr int kGatherTokens = 64;
 constexpr int kGatherThreads = 256;
+constexpr int kGatherPieces = 24;  // 16-byte pieces of a V row in shared memory at a time
 
 template <int D>
 __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(PagedEvictParams p) {
-    __shared__ int64_t src[kGatherTokens];  // row (page, head, place) of each token, -1: none
-    __shared__ int64_t dst[kGatherTokens];
+    constexpr int kRow = 16 * kGatherPieces + 16;  // bytes of a staged row: 16-byte aligned, spread over the banks
+    __shared__ int64_t src[kGatherTokens];         // (page, head, place) of each token, -1: none
+    __shared__ int64_t dst[kGatherTokens / 16];    // of each 16 tokens' destination
+    __shared__ int64_t piece[kGatherTokens];       // (page, head, first place) of each piece
+    __shared__ int place[kGatherTokens];           // 16 x piece + byte of each token, -1: none
+    __shared__ int s_pieces;
+    __shared__ __align__(16) uint8_t in[D * kRow];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.y, s = blockIdx.z, i0 = blockIdx.x * kGatherTokens;
     const int kv = evict_len(p.g, s);
@@ -164,46 +175,103 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(PagedEvict
     if (n <= 0) return;
     const int shift = p.g.page_shift, P = 1 << shift;
     if (tid < kGatherTokens) {
-        int64_t a = -1, b = -1;
+        int64_t a = -1;
         if (tid < n) {
             const int64_t row = static_cast<int64_t>(s) * p.g.kv_heads + h;
-            const int j = __ldg(p.kept + row * p.keep + i0 + tid), i = i0 + tid;
+            const int j = __ldg(p.kept + row * p.keep + i0 + tid);
             const int page = load_page(p.g, s, j >> shift);
-            int to = __ldg(p.dst_table + static_cast<int64_t>(s) * p.dst_pages + (i >> shift));
-            if (to < 0 || to >= p.g.pages) {
-                flag_meta(p.g.status);
-                to = -1;
-            }
-            if (page >= 0 && to >= 0) {
-                a = (static_cast<int64_t>(page) * p.g.kv_heads + h) * P + (j & (P - 1));
-                b = (static_cast<int64_t>(to) * p.g.kv_heads + h) * P + (i & (P - 1));
-            }
+            if (page >= 0) a = (static_cast<int64_t>(page) * p.g.kv_heads + h) * P + (j & (P - 1));
         }
         src[tid] = a;
-        dst[tid] = b;
-        if (a >= 0) {
-            p.g.kscale[b] = p.g.kscale[a];
-            p.g.vscale[b] = p.g.vscale[a];
+        if ((tid & 15) == 0) {
+            int64_t b = -1;
+            const int i = i0 + tid;
+            if (tid < n) {
+                const int to = __ldg(p.dst_table + static_cast<int64_t>(s) * p.dst_pages + (i >> shift));
+                if (to >= 0 && to < p.g.pages)
+                    b = (static_cast<int64_t>(to) * p.g.kv_heads + h) * P + (i & (P - 1));
+                else
+                    flag_meta(p.g.status);
+            }
+            dst[tid >> 4] = b;
         }
     }
     __syncthreads();
-    constexpr int kPieces = D / 16;
-    for (int i = tid; i < n * kPieces; i += kGatherThreads) {
-        const int t = i / kPieces, c = i % kPieces;
-        if (src[t] >= 0)
-            *reinterpret_cast<uint4*>(p.g.kcodes + dst[t] * D + 16 * c) =
-                *reinterpret_cast<const uint4*>(p.g.kcodes + src[t] * D + 16 * c);
-    }
-    // V: element (d, place) of page block `b` is byte (b D + d) P + place
+    // the 16-byte pieces of V rows that hold the tokens (which ascend: equal
+    // pieces are neighbours; a token on a bad page has none)
+    if (warp == 0) {
+        int count = 0;
 #pragma unroll
-    for (int k = 0; k < kGatherTokens / 32; ++k) {
-        const int64_t a = src[32 * k + lane], b = dst[32 * k + lane];
-        if (a < 0) continue;
-        const uint8_t* from = p.g.vcodes + (a >> shift) * D * P + (a & (P - 1));
-        uint8_t* to = p.g.vcodes + (b >> shift) * D * P + (b & (P - 1));
-        constexpr int kWarps = kGatherThreads / 32;
-#pragma unroll 8
-        for (int d = warp; d < D; d += kWarps) to[static_cast<int64_t>(d) * P] = from[static_cast<int64_t>(d) * P];
+        for (int k = 0; k < kGatherTokens; k += 32) {
+            const int64_t a = src[k + lane], before = k + lane > 0 ? src[k + lane - 1] : -1;
+            const bool first = a >= 0 && (before < 0 || (before >> 4) != (a >> 4));
+            const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+            const int at = count + __popc(firsts & ((2u << lane) - 1u)) - 1;
+            if (first) piece[at] = a & ~static_cast<int64_t>(15);
+            place[k + lane] = a < 0 ? -1 : 16 * at + static_cast<int>(a & 15);
+            count += __popc(firsts);
+        }
+        if (lane == 0) s_pieces = count;
+    }
+    // scales and K rows meanwhile
+    if (tid >= 64 && tid < 64 + kGatherTokens) {
+        const int t = tid - 64;
+        if (src[t] >= 0 && dst[t >> 4] >= 0) {
+            p.g.kscale[dst[t >> 4] + (t & 15)] = p.g.kscale[src[t]];
+            p.g.vscale[dst[t >> 4] + (t & 15)] = p.g.vscale[src[t]];
+        }
+    }
+    constexpr int kPieces = D / 16;
+#pragma unroll
+    for (int i = tid; i < kGatherTokens * kPieces; i += kGatherThreads) {
+        const int t = i / kPieces, c = i % kPieces;
+        if (src[t] >= 0 && dst[t >> 4] >= 0)
+            *reinterpret_cast<uint4*>(p.g.kcodes + (dst[t >> 4] + (t & 15)) * D + 16 * c) =
+                ldg_nc_na_v4(p.g.kcodes + src[t] * D + 16 * c);
+    }
+    __syncthreads();
+    // V: element (d, place) of (page, head) b is byte (b D + d) P + place.
+    // Thread: tokens 4 w .. 4 w + 3 of the dims tid / 16 + 16 k.
+    const int pieces = s_pieces, w = tid & 15;
+    const int64_t to = dst[w >> 2];
+    for (int first = 0; first < pieces; first += kGatherPieces) {
+        const int here = min(kGatherPieces, pieces - first);
+        // four pieces of a row by neighbouring lanes: they often lie side by side
+        for (int k = tid & 3; k < here; k += 4) {
+            const int64_t b = piece[first + k];
+            const uint8_t* from = p.g.vcodes + (b >> shift) * D * P + (b & (P - 1));
+#pragma unroll
+            for (int d = tid >> 2; d < D; d += kGatherThreads / 4)
+                *reinterpret_cast<uint4*>(in + d * kRow + 16 * k) =
+                    __ldg(reinterpret_cast<const uint4*>(from + (static_cast<uint32_t>(d) << shift)));
+        }
+        __syncthreads();
+        if (to >= 0) {
+            int at[4];
+            bool have[4], all = true;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int v = place[4 * w + x];
+                have[x] = v >= 16 * first && v < 16 * (first + here);
+                at[x] = have[x] ? v - 16 * first : 0;
+                all &= have[x];
+            }
+            uint8_t* out = p.g.vcodes + (to >> shift) * D * P + (to & (P - 1)) + 4 * (w & 3);
+#pragma unroll 4
+            for (int d = tid >> 4; d < D; d += kGatherThreads / 16) {
+                const uint8_t* row = in + d * kRow;
+                uint8_t* o = out + (static_cast<uint32_t>(d) << shift);
+                if (all) {
+                    *reinterpret_cast<uint32_t*>(o) = row[at[0]] | (row[at[1]] << 8) | (row[at[2]] << 16) |
+                                                      (static_cast<uint32_t>(row[at[3]]) << 24);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (have[x]) o[x] = row[at[x]];
+                }
+            }
+        }
+        __syncthreads();
     }
 }
 
