@@ -157,10 +157,10 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
 
 constexpr int kGatherTokens = 64;
 constexpr int kGatherThreads = 256;
-constexpr int kGatherPieces = 24;  // 16-byte pieces of a V row in shared memory at a time
+constexpr int kGatherPieces = 16;  // 16-byte pieces of a V row in shared memory at a time
 
 template <int D>
-__global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(PagedEvictParams p) {
+__global__ void __launch_bounds__(kGatherThreads, 6) paged_gather_kernel(PagedEvictParams p) {
     constexpr int kRow = 16 * kGatherPieces + 16;  // bytes of a staged row: 16-byte aligned, spread over the banks
     __shared__ int64_t src[kGatherTokens];         // (page, head, place) of each token, -1: none
     __shared__ int64_t dst[kGatherTokens / 16];    // of each 16 tokens' destination

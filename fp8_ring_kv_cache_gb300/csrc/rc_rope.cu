@@ -76,10 +76,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_axes_kernel(const __grid_co
 template <typename T>
 cudaError_t launch_t(const RopeAxesParams& p, int D, cudaStream_t s) {
     const int64_t pieces = p.n * p.heads * D * static_cast<int64_t>(sizeof(T)) / 16;
-    // tokens of a block: enough blocks to fill the card first, then larger
-    // blocks (fewer angle phases)
+    // Tokens of a block: enough blocks to fill the card first, then up to 2,048
+    // pieces (34,065 tokens x 16 heads x 128 in fp32: 1,024 pieces 85.5 us, 2,048
+    // 82.1 us, 4,096 84.2 us; 757 tokens x 48 heads in bf16: one token 5.0 us,
+    // two 5.5, four 6.6)
     int tb = 1;
-    while (tb < kRopeMaxTokens && p.n / (2 * tb) >= 152 * 4 && pieces / p.n * tb < 4 * kRopeThreads) tb *= 2;
+    while (tb < kRopeMaxTokens && p.n / (2 * tb) >= 152 * 4 && pieces / p.n * tb < 8 * kRopeThreads) tb *= 2;
     const int64_t grid = (p.n + tb - 1) / tb;
     if (D == 128)
         rope_axes_kernel<T, 128><<<static_cast<unsigned>(grid), kRopeThreads, 0, s>>>(p, tb);
