@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kRowsWarps = 4;
 constexpr int kRowsThreads = kRowsWarps * 32;
-constexpr int kChunk = 64;  // cached tokens of a warp's step
+constexpr int kChunk = 64;      // cached tokens of a warp's step
+constexpr int kMaxSplits = 32;  // of a sequence
 
 // One split's result for a row tile of 8 NR rows in the workspace: O [rows][D],
 // then max and sum [rows] each.
@@ -368,24 +369,62 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
     if (!last) return;
     if (tid == 0) p.counters[slot] = 0;
     __threadfence();
+    // the splits' weights first, some lanes a row; then O with many loads on the way
+    constexpr int kLanes = kRowsThreads / kRowTile;  // of a row: 8 or 16, in one warp
+    constexpr int kBatch = 16;                       // loads on the way
+    static_assert(kMaxSplits % kBatch == 0 && kMaxSplits % kLanes == 0, "weights up to the last batch's end");
+    static_assert(kRowsWarps * (D + 4) >= kMaxSplits, "the weights fit where the warps' O was");
+    float* weight = &so[0][0][0];  // [split][row]
+    {
+        const int r = tid / kLanes, k0 = tid % kLanes;
+        constexpr int K = kMaxSplits / kLanes;
+        float m[K], l[K], M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int k = k0 + i * kLanes;
+            const float* b = part + static_cast<size_t>(k) * part_floats<D, NR>() + kRowTile * D + r;
+            const bool have = k < nsplit && r < rows_here;
+            m[i] = have ? __ldcg(b) : -INFINITY;
+            l[i] = have ? __ldcg(b + kRowTile) : 0.f;
+            M = fmaxf(M, m[i]);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const float f = join_weight(m[i], M);
+            L += f * l[i];
+            weight[(k0 + i * kLanes) * kRowTile + r] = f;
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (k0 == 0) {
+            sm[0][r] = M;
+            sl[0][r] = L;
+        }
+    }
+    __syncthreads();
     for (int i = tid; i < rows_here * (D / 4); i += kRowsThreads) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-        float M = -INFINITY;
-        for (int k = 0; k < nsplit; ++k)
-            M = fmaxf(M, __ldcg(part + static_cast<size_t>(k) * part_floats<D, NR>() + kRowTile * D + r));
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float L = 0.f;
-        for (int k = 0; k < nsplit; ++k) {
-            const float* b = part + static_cast<size_t>(k) * part_floats<D, NR>();
-            const float f = join_weight(__ldcg(b + kRowTile * D + r), M);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(b + r * D + d));
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
-            L += f * __ldcg(b + kRowTile * D + kRowTile + r);
+        const float* from = part + r * D + d;
+        for (int k0 = 0; k0 < nsplit; k0 += kBatch) {
+            float4 v[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                v[u] = k0 + u < nsplit ? __ldcg(reinterpret_cast<const float4*>(
+                                             from + static_cast<size_t>(k0 + u) * part_floats<D, NR>()))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float f = weight[(k0 + u) * kRowTile + r];  // 0 behind the last split
+                acc.x += f * v[u].x;
+                acc.y += f * v[u].y;
+                acc.z += f * v[u].z;
+                acc.w += f * v[u].w;
+            }
         }
-        store_out(r, d, acc, M, L);
+        store_out(r, d, acc, sm[0][r], sl[0][r]);
     }
 }
 
@@ -395,13 +434,21 @@ cudaError_t launch_rows(PagedAttnParams& p, size_t part_floats_max, int max_coun
     p.row_tiles = static_cast<int>((rows + 8 * NR - 1) / (8 * NR));
     const int64_t slots = static_cast<int64_t>(p.g.seqs) * p.row_tiles * p.g.kv_heads;
     if (static_cast<int64_t>(p.row_tiles) * p.g.kv_heads > 65535) return cudaErrorInvalidValue;
-    // Splits: enough blocks for several on each of the 152 SMs, at least one
-    // step of every warp each, at most 32 (the last block reads them all), and
-    // as many as the workspace holds.
+    // Splits: sixteen blocks an SM, which evens out sequences of different
+    // lengths (8 query heads' groups of 6 x 32 sequences of 61 to 16,381 tokens:
+    // 6 blocks an SM 119 us, 12 102, 16 99, 24 101, 48 106), at most 32, which
+    // the last block can still join quickly, and as many as the workspace holds.
+    // A block takes two steps of every warp at least (64 sequences x 1,000
+    // tokens x 8 heads: one step 41 us, two 37), or one while each block has an
+    // SM, or half of one with 8 rows, to itself (one sequence of 4,000 tokens:
+    // one step 8.6 us, two 11.1; with 16 rows 11.0 and 13.6; 8,000 tokens with
+    // 16 rows 15.5 and 13.6).  512 tokens stay whole (337 tokens: 6.5 us, as two
+    // splits 7.8).
     const int step = kRowsWarps * kChunk;
-    int64_t want = (152 * 24 + slots - 1) / slots;
-    want = std::min<int64_t>(want, 32);
-    want = std::min<int64_t>(want, (p.g.max_kv + step - 1) / step);
+    const int64_t steps = (p.g.max_kv + step - 1) / step;
+    int64_t want = std::min<int64_t>((152 * 16 + slots - 1) / slots, kMaxSplits);
+    const int least = steps > 2 && std::min<int64_t>(steps, kMaxSplits) * slots <= (NR == 1 ? 2 : 1) * 152 ? 1 : 2;
+    want = std::min<int64_t>(want, (steps + least - 1) / least);
     want = std::min<int64_t>(want, static_cast<int64_t>(part_floats_max / (slots * part_floats<D, NR>())));
     if (slots > max_counters || want < 1) want = 1;
     const int per = static_cast<int>((p.g.max_kv + want - 1) / want);
@@ -415,8 +462,12 @@ cudaError_t launch_rows(PagedAttnParams& p, size_t part_floats_max, int max_coun
 template <int D>
 cudaError_t launch_attention_d(PagedAttnParams& p, size_t part_floats_max, int max_counters, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
-    // up to one row tile per KV head the reading of the codes is what counts;
-    // with more rows each tile would read them again
+    // Up to 16 rows per KV head the reading of the codes is what counts; with
+    // more, each tile of 16 would read them again, and the tcgen05 kernel, whose
+    // time hardly grows up to 128 rows, is the faster one (32 sequences x 8,000
+    // tokens x 8 KV heads x 128: 8 rows 97 against 252 us, 16 rows 126 against
+    // 252, 17 rows 254 with tcgen05).  Tiles of 8 rows save half the products
+    // (the same with 1 row: 95 us as a tile of 8, 124 us as one of 16).
     if (rows <= 8) return launch_rows<D, 1>(p, part_floats_max, max_counters, s);
     if (rows <= 16) return launch_rows<D, 2>(p, part_floats_max, max_counters, s);
     return launch_paged_tc(p, D, part_floats_max, s);

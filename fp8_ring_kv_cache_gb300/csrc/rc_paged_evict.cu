@@ -27,7 +27,9 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kHistCopies = 2;           // histograms that even and odd lanes have to themselves
-constexpr int kSelCap = 48 * 1024;       // keys kept in shared memory
+// Keys kept in shared memory (64 lists of 32,749, 1,024 of each kept: 107 us,
+// 118 us when every pass reads the scores again).
+constexpr int kSelCap = 48 * 1024;
 
 // Order-preserving key: larger score, larger key; -0 as +0, NaN above all.
 __device__ __forceinline__ uint32_t score_key(float x) {

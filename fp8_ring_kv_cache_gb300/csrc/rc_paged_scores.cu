@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kScoreWarps = 4;
 constexpr int kScoreTokens = 32;  // of a warp
-constexpr int kScoreRowsMax = 128;
+constexpr int kScoreRowsMax = 32;  // of the kernels here
 
 constexpr int kFewChunk = 64;  // cached tokens of a warp's step
 
@@ -251,8 +251,11 @@ template <int D>
 cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
     if (rows <= 16) {
-        // ranges of the cached tokens: several blocks on each SM, a step of every
-        // warp at least
+        // Up to 16 rows stay in registers (the sequences above: 8 rows 60 us, 123 us
+        // with the kernel for some tiles; 16 rows 64 and 127).  Ranges of the
+        // cached tokens: twelve blocks an SM, a step of every warp at least (16
+        // sequences of 509 to 8,191 tokens x 8 heads: 6 blocks an SM 21.6 us, 12
+        // 19.5, 24 21.8, 48 20.6)
         const int step = kScoreWarps * kFewChunk;
         const int64_t steps = (p.g.max_kv + step - 1) / step, lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
         const int64_t want = std::min(steps, std::max<int64_t>(1, (152 * 12 + lists - 1) / lists));
@@ -273,8 +276,11 @@ cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_paged_scores(const PagedScoreParams& p, int D, cudaStream_t s) {
-    // up to a few row tiles the warps' own products keep up with the reading of
-    // the codes; with more rows the tensor cores' do
+    // Up to two row tiles of 16 the warps' own products keep up with the reading
+    // of the codes; with more rows the tcgen05 kernel is the faster one, whose
+    // time is the same up to 128 rows (32 sequences x 8,000 tokens x 8 KV heads x
+    // 128: 32 rows 162 against 192 us, 64 rows 237 against 192; one sequence of
+    // 60,000 tokens: 42 against 46, 60 against 46).
     if (static_cast<int64_t>(p.g.max_new) * p.group > kScoreRowsMax) return launch_paged_scores_tc(p, D, s);
     return D == 128 ? launch_d<128>(p, s) : launch_d<64>(p, s);
 }
