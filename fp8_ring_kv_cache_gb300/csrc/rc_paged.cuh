@@ -18,7 +18,7 @@ struct RopePlanDev {
 // A generic address of a kernel's (__grid_constant__) parameter bytes, whose
 // origin the compiler does not see: lanes that read different entries of an
 // array there go through the data cache together, where the constant bank
-// would serve one address at a time (4 us of the 22 us that a chunk's write took).
+// would serve one address at a time (a chunk's write then took 22 us, not 15.6).
 template <typename T>
 __device__ __forceinline__ const T* param_address(const T* p) {
     asm volatile("mov.b64 %0, %0;" : "+l"(p));

@@ -55,6 +55,17 @@ void copy_plan(RopePlanDev* d, const rc_rope_plan* plan) {
     std::memcpy(d->axis, plan->axis, sizeof(d->axis));
 }
 
+// theta / 2 pi * 2^64, rounded, for theta in (2^-32, 1] radians: integers, so that
+// every machine gives the same (theta is m 2^(e - 53) with a 53-bit m; 2^76 / 2 pi
+// has 74 bits).
+uint64_t turns_of(double theta) {
+    constexpr unsigned __int128 kInv = (static_cast<unsigned __int128>(0x28be60db9391054aull) << 12) | 0x7f1u;
+    int e = 0;
+    const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(theta, &e), 53));
+    const int shift = 53 - e + 12;  // 64 .. 97
+    return static_cast<uint64_t>((m * kInv + (static_cast<unsigned __int128>(1) << (shift - 1))) >> shift);
+}
+
 bool stride_ok(int64_t stride, int64_t row, int unit) { return stride >= row && stride % unit == 0; }
 
 // The pool's and the batch's host fields and pointers; fills g.
@@ -117,9 +128,7 @@ int rc_rope_plan_init(rc_rope_plan* plan, int head_dim, int axes, const int* sec
         for (int r = 0; r < sections[a]; ++r, ++i) {
             const double theta = (flags & RC_ROPE_SHARED_FREQS) ? std::pow(base, -2.0 * i / head_dim)
                                                                 : std::pow(base, -static_cast<double>(r) / sections[a]);
-            // theta <= 1 radian, under 1 / 6 of a turn: no overflow
-            const long double turns = static_cast<long double>(theta) / 6.283185307179586476925286766559L;
-            plan->turns[i] = static_cast<uint64_t>(turns * 18446744073709551616.0L + 0.5L);
+            plan->turns[i] = turns_of(theta);
             plan->axis[i] = static_cast<uint8_t>(a);
         }
     return RC_OK;

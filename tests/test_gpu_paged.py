@@ -698,3 +698,80 @@ def test_refused_tensors(rc):
     with pytest.raises(ValueError):     # shifted over itself
         rc.rc_rope_axes(wide[:2], pos, rope, out=wide[1:])
     st.cache.sync()
+
+
+# ------------------------------------------------------------------ borders of the kernels' shares of the work
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [1, 7, 8, 9, 16])
+@pytest.mark.parametrize("kv", [512, 513, 1279, 4351, 8193])
+def test_attend_few_rows_splits(rc, kv, group, dim):
+    st = Setup(rc, [(1, kv)], 1, dim, 64, seed=kv + group)
+    st.check_attend(bf16(st.rng, 1, group, dim), True)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("seqs,group", [([(40, 3000)], 1), ([(17, 513), (17, 4097)], 1), ([(100, 2500)], 3), ([(257, 1300), (1, 5)], 1)])
+def test_attend_some_rows_splits(rc, seqs, group, dim, causal):
+    st = Setup(rc, seqs, 1, dim, 32, seed=sum(k for _, k in seqs) + group)
+    st.check_attend(bf16(st.rng, st.tokens, group, dim), causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,seqs,group", [
+    (64, [(8, 300)], 4), (128, [(33, 300)], 1), (128, [(16, 257), (3, 700)], 3),   # 32, 33 and 48 rows
+    (64, [(500, 700)], 2), (128, [(385, 385)], 1), (128, [(431, 1100), (33, 33)], 2),  # several blocks of rows
+])
+def test_accumulate_many_rows(rc, seqs, group, dim, causal):
+    st = Setup(rc, seqs, 1, dim, 16, seed=sum(k for _, k in seqs) + group + 2)
+    check_scores(st, bf16(st.rng, st.tokens, group, dim), causal, in_place=dim == 64)
+
+
+def test_two_caches_on_the_same_pages_at_once(rc):
+    """Two streams, each with a workspace of its own, read one pool's pages at the same time."""
+    st = Setup(rc, [(1, 6000), (60, 900), (1, 77)], 2, 128, 32, seed=81)
+    other = rc.PagedKVCache(st.cache.kcodes, st.cache.vcodes, st.cache.kscale, st.cache.vscale)
+    q = bf16(st.rng, st.tokens, 6, 128).cuda()
+    want, wlse = st.attend(q, True)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    res = []
+    for i in range(8):
+        cache = (st.cache, other)[i % 2]
+        out, lse = torch.zeros_like(want), torch.zeros_like(wlse)
+        streams[i % 2].wait_stream(torch.cuda.current_stream())
+        cache.attend(st.batch, q, out, lse=lse, stream=streams[i % 2])
+        res.append((out, lse))
+    for cache, stream in zip((st.cache, other), streams):
+        cache.sync(stream=stream)
+    torch.cuda.synchronize()
+    n = st.meta["q_start"][-1]
+    assert all(torch.equal(o[:n], want[:n]) and torch.equal(x[:n], wlse[:n]) for o, x in res)
+
+
+def test_a_wait_that_runs_out_is_reported_and_forgotten(rc):
+    """With a limit of 0 the first wait that is not already over gives up: the call reports RC_ERR_TIMEOUT, frees what
+    it holds and the next call with the limit restored is right."""
+    st = Setup(rc, [(300, 2000)], 2, 128, 64, seed=91)
+    q = bf16(st.rng, st.tokens, 4, 128)
+    good, lse = st.attend(q.cuda(), True)
+    sc = torch.zeros((1, 2, st.max_kv), device="cuda")
+    st.cache.accumulate(st.batch, q.cuda(), lse, sc)
+    st.cache.sync()
+    for call in (lambda: st.cache.attend(st.batch, q.cuda(), torch.zeros_like(good)),
+                 lambda: st.cache.accumulate(st.batch, q.cuda(), lse, sc, out=torch.zeros_like(sc))):
+        rc.rc_paged_set_wait_limit(0)
+        try:
+            call()
+            with pytest.raises(rc.RcError) as e:
+                st.cache.sync()
+        finally:
+            rc.rc_paged_set_wait_limit(2_000_000_000)
+        assert e.value.status == rc.RC_ERR_TIMEOUT
+        st.cache.sync()
+        again, lse2 = st.attend(q.cuda(), True)
+        assert torch.equal(again, good) and torch.equal(lse2, lse)
+        sc2 = torch.zeros_like(sc)
+        st.cache.accumulate(st.batch, q.cuda(), lse, sc2)
+        st.cache.sync()
+        assert torch.equal(sc2, sc)

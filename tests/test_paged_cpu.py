@@ -2,6 +2,8 @@
 checks, which come before any device work (the addresses here are never read)."""
 import ctypes
 import functools
+import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -190,3 +192,18 @@ def test_the_tests_own_definitions():
     assert (amax[inside] <= 448 * s[inside]).all() and (amax[inside & (amax > 0)] > 224 * s[inside & (amax > 0)]).all()
     assert scale[3] == 127 and scale[4] == 127 - 5 and scale.min() >= 3 and scale.max() <= 134
     assert pu.quantise(np.array([[1.0, np.inf]]))[1][0] == 255
+
+
+@pytest.mark.parametrize("base,sections,shared", [(10000.0, (64,), False), (10000.0, (24, 20, 20), False),
+                                                  (500000.0, (32,), False), (1e9, (64,), False), (10000.0, (12, 10, 10), True)])
+def test_plan_turns_are_the_rounded_frequencies(rc, base, sections, shared):
+    """turns = frequency / 2 pi * 2^64: within half a unit of the last place (and the constant's own 2^-12) of the double."""
+    plan = rc.RopeAxes(sections, base=base, shared_freqs=shared).plan
+    two_pi = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582")
+    i = 0
+    for axis, w in enumerate(sections):
+        for r in range(w):
+            theta = math.pow(base, -2.0 * i / (2 * sum(sections))) if shared else math.pow(base, -r / w)
+            assert abs(plan.turns[i] - Fraction(theta) * 2 ** 64 / two_pi) <= Fraction(1, 2) + Fraction(1, 2 ** 12)
+            assert plan.axis[i] == axis
+            i += 1
