@@ -16,8 +16,9 @@
 //                  time, so each scheduler has four of them (with two it took
 //                  111 us for 757 x 5,788 tokens x 48 heads).  They also bring
 //                  the query rows.
-//   warps 20 .. 23 read K's codes from the pages (a pair of tiles ahead, in
-//                  registers) and make them bf16 operand tiles
+//   warps 20 .. 27 read K's codes from the pages (a pair of tiles ahead, in
+//                  registers) and make them bf16 operand tiles, four warps for
+//                  each tile of a pair
 // With the queries kept, K is read and converted once per 384 rows, and the
 // queries once per block: keeping K instead would read them for every 128
 // tokens (430 MB of cache traffic for 757 x 5,788 tokens x 48 heads).
@@ -29,9 +30,9 @@ namespace rc {
 
 namespace {
 
-// 768 threads launched with 80 registers each; the warpgroups share them
-// 40 + 4 x 88 + 88.
-constexpr int kStThreads = 768;
+// 896 threads launched with 72 registers each; the warpgroups share them
+// 40 + 4 x 80 + 2 x 72.
+constexpr int kStThreads = 896;
 constexpr int kStSums = 512;  // threads of the four groups
 constexpr int kStTile = 128;
 constexpr int kStQTiles = 3;  // query tiles in shared memory
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         }
     } else if (wg <= 4) {
         // ------------------------------------------------------------ sums
-        regs_inc<88>();
+        regs_inc<80>();
         const int place = wg - 1, g = place >> 1, a = place & 1, quad = warp & 3;
         const int st = tid - 128;  // number among the groups' threads
         const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * place;
@@ -313,19 +314,18 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         }
     } else {
         // ------------------------------------------------------------ K
-        // Thread ct: the pieces of 16 dims ct % 4 (+ 4 in the second 64 dims) of
-        // the rows ct / 4 + 32 m of each tile.  Lane l < 16 of a warp
-        // looks up the block of 16 tokens l of the pair.
-        regs_inc<88>();
-        const int ct = tid - 5 * 128;
+        // Each warpgroup has one tile of every pair.  Thread ct: the pieces of 16
+        // dims ct % 4 (+ 4 in the second 64 dims) of the rows ct / 4 + 32 m.  Lane
+        // l < 8 of a warp looks up the block of 16 tokens l of the tile.
+        const int ct = tid & 127, a = wg - 5;
         constexpr int NB = D / 64;
         const int rr = ct >> 2, pb = p.g.page_shift - 4;
         const uint8_t* kbase = p.g.kcodes + (rr & 15) * D + 16 * (ct & 3);
         const uint8_t* sbase = p.g.kscale + (rr & 15);
         const uint32_t* table =
             reinterpret_cast<const uint32_t*>(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages);
-        uint4 kr[2][4 * NB];
-        uint32_t ks[2][4];
+        uint4 kr[4 * NB];
+        uint32_t ks[4];
         // the next pair with work after (rb, pair); pair = -1 starts; rb = blocks ends
         auto advance = [&](int& rb, int& pair) {
             do {
@@ -335,34 +335,32 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 }
             } while (rb < w.blocks && !w.has(rb, pair));
         };
+        auto token = [&](int pair) { return j0 + (2 * pair + a) * kStTile + 16 * (lane & 7); };
         auto entry = [&](int rb, int pair) {
-            const int t = j0 + pair * 2 * kStTile + 16 * (lane & 15);
+            const int t = token(pair);
             return rb < w.blocks && t < q.kv ? static_cast<int>(ldg_early(table + (t >> p.g.page_shift))) : 0;
         };
         // (blocks behind the end, or on a bad page, read block 0: their sums are not used)
         auto block_of = [&](int rb, int pair, int page) {
-            const int t = j0 + pair * 2 * kStTile + 16 * (lane & 15);
+            const int t = token(pair);
             if (rb >= w.blocks || t >= q.kv) return 0u;
             const uint32_t at = static_cast<uint32_t>(check_page(p.g, page) ? page : 0) * p.g.kv_heads + h;
             return (at << pb) + (static_cast<uint32_t>(t >> 4) & ((1u << pb) - 1u));
         };
-        auto fetch = [&](int g, uint32_t blk) {
+        auto fetch = [&](int m, uint32_t blk) {
+            const uint64_t at = __shfl_sync(0xffffffffu, blk, (rr >> 4) + 2 * m);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const uint64_t at = __shfl_sync(0xffffffffu, blk, 8 * g + (rr >> 4) + 2 * m);
-#pragma unroll
-                for (int x = 0; x < NB; ++x) kr[g][m * NB + x] = ldg_nc_na_v4(kbase + at * (16 * D) + 64 * x);
-                ks[g][m] = ldg_early(sbase + at * 16);
-            }
+            for (int x = 0; x < NB; ++x) kr[m * NB + x] = ldg_nc_na_v4(kbase + at * (16 * D) + 64 * x);
+            ks[m] = ldg_early(sbase + at * 16);
         };
         int rb = 0, pair = -1, pc = 0;
-        int uses[4] = {0, 0, 0, 0};  // of each buffer so far
+        int uses[2] = {0, 0};  // of each buffer of the tile so far
         advance(rb, pair);
         int rb1 = rb, pair1 = pair;
         if (rb < w.blocks) {
             const uint32_t blk = block_of(rb, pair, entry(rb, pair));
-            fetch(0, blk);
-            fetch(1, blk);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) fetch(m, blk);
             advance(rb1, pair1);
         }
         int ahead = entry(rb1, pair1);
@@ -372,31 +370,29 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             int rb2 = rb1, pair2 = pair1;
             if (rb1 < w.blocks) advance(rb2, pair2);
             ahead = entry(rb2, pair2);
+            const bool there = a == 0 || w.second(pair);
+            const int buf = 2 * (pc & 1) + a;  // (the group of the pair, the tile of the pair)
+            if (there) ok = warp_wait(&bars[S_K_EMPTY + buf], (uses[pc & 1]++ & 1) ^ 1, ab, kDevTimeoutConvert);
+            uint8_t* dst = smem + Lay::kK + buf * Lay::kTile;
+            uint8_t* lo = dst + bktile_off(rr, 16 * (ct & 3));
+            uint8_t* hi = dst + bktile_off(rr, 16 * (ct & 3) + 8);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                if (ok && (g == 0 || w.second(pair))) {
-                    const int buf = 2 * (pc & 1) + g;  // (the group of the pair, the tile of the pair)
-                    ok = warp_wait(&bars[S_K_EMPTY + buf], (uses[buf]++ & 1) ^ 1, ab, kDevTimeoutConvert);
-                    if (ok) {
-                        uint8_t* dst = smem + Lay::kK + buf * Lay::kTile;
-                        uint8_t* lo = dst + bktile_off(rr, 16 * (ct & 3));
-                        uint8_t* hi = dst + bktile_off(rr, 16 * (ct & 3) + 8);
+            for (int m = 0; m < 4; ++m) {
+                if (ok && there) {
+                    const uint32_t f1 = scale_factor(ks[m]);
+                    const uint32_t f[8] = {f1, f1, f1, f1, f1, f1, f1, f1};
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const uint32_t f1 = scale_factor(ks[g][m]);
-                            const uint32_t f[8] = {f1, f1, f1, f1, f1, f1, f1, f1};
-#pragma unroll
-                            for (int x = 0; x < NB; ++x) {
-                                const int off = x * (kStTile * 128) + m * (32 * 128);
-                                put16(lo + off, hi + off, kr[g][m * NB + x], f);
-                            }
-                        }
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars[S_K_FULL + buf]);
+                    for (int x = 0; x < NB; ++x) {
+                        const int off = x * (kStTile * 128) + m * (32 * 128);
+                        put16(lo + off, hi + off, kr[m * NB + x], f);
                     }
                 }
-                fetch(g, blk);
+                fetch(m, blk);  // the next pair's rows, into the registers just freed
+            }
+            if (ok && there) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[S_K_FULL + buf]);
             }
             ++pc;
             rb = rb1;
