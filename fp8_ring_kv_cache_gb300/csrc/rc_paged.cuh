@@ -117,6 +117,10 @@ __device__ __forceinline__ uint32_t codes02(uint32_t w) {
 __device__ __forceinline__ uint32_t codes13(uint32_t w) {
     return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
 }
+// The pairs (c0, c1) and (c2, c3): the bytes are first put at the tops of the halves.
+__device__ __forceinline__ uint32_t codes_apart(uint32_t t) { return (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u); }
+__device__ __forceinline__ uint32_t codes01(uint32_t w) { return codes_apart(__byte_perm(w, 0u, 0x1404)); }
+__device__ __forceinline__ uint32_t codes23(uint32_t w) { return codes_apart(__byte_perm(w, 0u, 0x3424)); }
 __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -2,24 +2,23 @@
 // query rows, on the tensor cores (tcgen05).
 //
 // Transposed: S^T = K Q^T, so a thread holds one cached token's scores (a lane of
-// TMEM) and its sum over the queries runs in one register, in one order; no two
-// threads add to one entry.  A block has a range of the cached tokens of one
-// (sequence, KV head) and goes over the head's query rows in blocks of up to
-// 384, which stay in shared memory as three tiles while the cached tokens stream
-// past, in pairs of tiles of 128:
-//   warps 0, 1     issue the products of the pairs with an even, an odd number
-//                  (one lane each); warp 0 owns TMEM: four places of 128 x 128
-//                  scores, one for each tile of two pairs
-//   warps 4 .. 19  four groups, one a place: exp2(S c - lse) and the sum over the
-//                  columns, a token a thread.  One warp's chain of load, product
-//                  sum, exponential and add leaves the units idle most of the
-//                  time, so each scheduler has four of them (with two it took
-//                  111 us for 757 x 5,788 tokens x 48 heads).  They also bring
-//                  the query rows.
-//   warps 20 .. 27 read K's codes from the pages (a pair of tiles ahead, in
-//                  registers) and make them bf16 operand tiles, four warps for
-//                  each tile of a pair
-// With the queries kept, K is read and converted once per 384 rows, and the
+// TMEM).  A block has a range of the cached tokens of one (sequence, KV head) and
+// goes over the head's query rows in blocks of up to 768, which stay in shared
+// memory as six tiles while the cached tokens stream past in tiles of 128.  The
+// operand with the cached tokens is in TMEM, not in shared memory: each thread of
+// the converters has a token's row, which is a lane there.
+//   warp 0         issues the products (one lane) and owns TMEM: three places of
+//                  128 x 128 scores and two K tiles
+//   warps 4 .. 15  three groups, one a place: exp2(S c - lse) and the sum over the
+//                  columns, a token a thread.  The units (K tile, query tile) go
+//                  to the groups in turn; a group's sums of a K tile are put in
+//                  shared memory, and the groups take turns in adding the three
+//                  up, always in the same order: no two threads add to one entry.
+//                  They also bring the query rows (by cp.async).
+//   warps 16 .. 23 read K's codes from the pages (two tiles ahead, in registers),
+//                  make them bf16 (exactly: scales are powers of two) and put
+//                  them in TMEM, half of the dims a warpgroup
+// With the queries kept, K is read and converted once per 768 rows, and the
 // queries once per block: keeping K instead would read them for every 128
 // tokens (430 MB of cache traffic for 757 x 5,788 tokens x 48 heads).
 #include <algorithm>
@@ -30,57 +29,60 @@ namespace rc {
 
 namespace {
 
-// 896 threads launched with 72 registers each; the warpgroups share them
-// 40 + 4 x 80 + 2 x 72.
-constexpr int kStThreads = 896;
-constexpr int kStSums = 512;  // threads of the four groups
+// 768 threads launched with 80 registers each; the warpgroups share them
+// 32 + 3 x 112 + 2 x 56 = 6 x 80.
+constexpr int kStThreads = 768;
+constexpr int kStGroups = 3;
+constexpr int kStSums = 128 * kStGroups;  // threads of the groups
 constexpr int kStTile = 128;
-constexpr int kStQTiles = 3;  // query tiles in shared memory
+constexpr int kStQTiles = 6;  // query tiles in shared memory
+constexpr int kStParts = 4;   // K tiles whose sums are in shared memory
+constexpr uint32_t kStTmemK = 128 * kStGroups;
 
 enum : int {
-    S_K_FULL = 0,    // [4] buffer 2 (pair & 1) + tile of the pair: K tile converted
-    S_K_EMPTY = 4,   // [4] its products have finished
-    S_S_FULL = 8,    // [4] scores of the K tile and a query tile in TMEM
-    S_S_FREE = 12,   // [4] the group has read them
-    S_Q_FULL = 16,   // the block's query rows are in place
-    S_Q_EMPTY = 17,  // every group has the scores of the block before
-    S_DRAIN = 18,
-    S_COUNT = 19
+    S_K_FULL = 0,      // [2] K tile converted
+    S_K_EMPTY = 2,     // [2] its products have finished
+    S_S_FULL = 4,      // [3] scores of a unit in TMEM
+    S_S_FREE = 7,      // [3] the group has read them
+    S_PART_FULL = 10,  // [4] every group's sums of a K tile are in place
+    S_PART_EMPTY = 14, // [4] they have been added up
+    S_Q_FULL = 18,     // the block's query rows are in place
+    S_Q_EMPTY = 19,    // every group is through with them
+    S_DRAIN = 20,
+    S_COUNT = 21
 };
 
 template <int D>
 struct StLayout {
     static constexpr uint32_t kTile = kStTile * D * 2;
-    static constexpr uint32_t kK = 0;                          // [4]
-    static constexpr uint32_t kQ = 4 * kTile;                  // [3]
-    static constexpr uint32_t kMinus = kQ + kStQTiles * kTile;  // fp32 [3][128]: -lse log2(e)
-    static constexpr uint32_t kBar = kMinus + kStQTiles * kStTile * 4;
+    static constexpr uint32_t kQ = 0;                           // [6]
+    static constexpr uint32_t kMinus = kQ + kStQTiles * kTile;  // fp32 [6][128]: -lse log2(e)
+    static constexpr uint32_t kPart = kMinus + kStQTiles * kStTile * 4;  // fp32 [4][3][128]
+    static constexpr uint32_t kBar = kPart + kStParts * kStGroups * kStTile * 4;
     static constexpr uint32_t kMisc = kBar + 8 * S_COUNT;
     static constexpr uint32_t kTotal = kMisc + 16;
     static constexpr uint32_t kAlloc = kTotal + 1024;
 };
 
 // What a block does, in the same order for every role: for each block of rows,
-// each pair of K tiles that some of its rows see; of those, the query tiles from
-// the first that sees the pair's first token.
+// each K tile that some of its rows see; of those, the query tiles from the first
+// that sees the K tile's first token.
 struct StWork {
-    int j0, end;     // the range's first token, the end of its tokens that exist
-    int kv, old;     // cached tokens; those that every query sees (causal)
-    int rows, group, tiles, per, blocks, pairs;
+    int j0, end;  // the range's first token, the end of its tokens that exist
+    int old;      // tokens that every query sees (causal)
+    int rows, group, tiles, per, blocks, ktiles;
     bool causal;
     __device__ __forceinline__ int first_row(int j) const {  // first row that sees token j (>= rows: none)
         const int64_t r = causal ? static_cast<int64_t>(max(0, j - old)) * group : 0;
         return static_cast<int>(min(r, static_cast<int64_t>(rows)));
     }
-    __device__ __forceinline__ int first_tile(int rb, int pair) const {
-        return max(rb * per, first_row(j0 + pair * 2 * kStTile) / kStTile);
+    __device__ __forceinline__ int first_tile(int rb, int i) const {
+        return max(rb * per, first_row(j0 + i * kStTile) / kStTile);
     }
     __device__ __forceinline__ int end_tile(int rb) const { return min(tiles, rb * per + per); }
-    __device__ __forceinline__ bool has(int rb, int pair) const {
-        return first_row(j0 + pair * 2 * kStTile) < rows && first_tile(rb, pair) < end_tile(rb);
+    __device__ __forceinline__ bool has(int rb, int i) const {
+        return first_row(j0 + i * kStTile) < rows && first_tile(rb, i) < end_tile(rb);
     }
-    // the pair's second tile has tokens
-    __device__ __forceinline__ bool second(int pair) const { return j0 + (2 * pair + 1) * kStTile < end; }
 };
 
 template <int D>
@@ -90,19 +92,18 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + Lay::kMisc);  // [0] tmem, [1] abort
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, quad = warp & 3;
     int b = blockIdx.x;
     const int h = b % p.g.kv_heads;
     b /= p.g.kv_heads;
     const int s = b % p.g.seqs;
-    const int j0 = (b / p.g.seqs) * range;  // (range: a multiple of 256)
+    const int j0 = (b / p.g.seqs) * range;  // (range: a multiple of 128)
     if (j0 >= p.g.max_kv) return;
     const Seq q = load_seq(p.g, s);
     const int64_t row_at = (static_cast<int64_t>(s) * p.g.kv_heads + h) * p.score_stride;
     StWork w;
     w.j0 = j0;
     w.end = min(q.kv, j0 + range);
-    w.kv = q.kv;
     w.old = q.kv - q.n;
     w.rows = q.n * p.group;
     w.group = p.group;
@@ -110,23 +111,29 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
     w.tiles = (w.rows + kStTile - 1) / kStTile;
     w.blocks = (w.tiles + kStQTiles - 1) / kStQTiles;
     w.per = w.blocks > 0 ? (w.tiles + w.blocks - 1) / w.blocks : 1;
-    w.pairs = w.rows > 0 ? max(0, (w.end - j0 + 2 * kStTile - 1) / (2 * kStTile)) : 0;
-    // tokens that no pair has keep their scores
+    w.ktiles = w.rows > 0 ? max(0, (w.end - j0 + kStTile - 1) / kStTile) : 0;
+    // tokens that no tile has keep their scores
     const int stop = min(p.g.max_kv, j0 + range);
-    for (int j = j0 + w.pairs * 2 * kStTile + tid; j < stop; j += kStThreads) p.out[row_at + j] = p.scores[row_at + j];
-    if (w.pairs == 0) return;
+    for (int j = j0 + w.ktiles * kStTile + tid; j < stop; j += kStThreads) p.out[row_at + j] = p.scores[row_at + j];
+    if (w.ktiles == 0) return;
     AbortState ab{reinterpret_cast<volatile uint32_t*>(&misc[1]), p.g.status, p.wait_ns};
 
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&bars[S_K_FULL + i], 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[S_K_FULL + i], 8);
             mbar_init(&bars[S_K_EMPTY + i], 1);
+        }
+        for (int i = 0; i < kStGroups; ++i) {
             mbar_init(&bars[S_S_FULL + i], 1);
             mbar_init(&bars[S_S_FREE + i], 4);
         }
-        mbar_init(&bars[S_Q_FULL], 16);
-        mbar_init(&bars[S_Q_EMPTY], 16);
-        mbar_init(&bars[S_DRAIN], 2);
+        for (int i = 0; i < kStParts; ++i) {
+            mbar_init(&bars[S_PART_FULL + i], kStSums / 32);
+            mbar_init(&bars[S_PART_EMPTY + i], 4);
+        }
+        mbar_init(&bars[S_Q_FULL], kStSums / 32);
+        mbar_init(&bars[S_Q_EMPTY], kStSums / 32);
+        mbar_init(&bars[S_DRAIN], 1);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -140,50 +147,46 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
     const uint32_t tmem = misc[0];
 
     if (wg == 0) {
-        regs_dec<40>();
-        if (warp < 2) {
+        regs_dec<32>();
+        if (warp == 0) {
             // -------------------------------------------------------- products
-            const int g = warp;
             const uint32_t idesc = instr_desc(kFmtBF16, kFmtBF16, 128, 128);
-            const uint64_t dk = smem_desc(smem_u32(smem + Lay::kK), 16, 1024, 2);
-            const uint32_t hi = static_cast<uint32_t>(dk >> 32), k_lo = static_cast<uint32_t>(dk);
-            const uint32_t q_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2));
+            const uint64_t dq = smem_desc(smem_u32(smem + Lay::kQ), 16, 1024, 2);
+            const uint32_t hi = static_cast<uint32_t>(dq >> 32), q_lo = static_cast<uint32_t>(dq);
             bool ok = true;
-            // pairs of all groups; first, second K tiles and units of this one
-            int pc = 0, ka_count = 0, kb_count = 0, uc[2] = {0, 0};
+            int kc = 0, place = 0, phase = 0;  // K tiles; the unit's place and how often it was used before
             for (int rb = 0; rb < w.blocks && ok; ++rb) {
                 ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutMma);
-                for (int pair = 0; pair < w.pairs && ok; ++pair) {
-                    if (!w.has(rb, pair) || (pc++ & 1) != g) continue;
-                    const int q0 = w.first_tile(rb, pair), q1 = w.end_tile(rb), tiles = w.second(pair) ? 2 : 1;
-                    ok = warp_wait(&bars[S_K_FULL + 2 * g], ka_count++ & 1, ab, kDevTimeoutMma);
-                    if (ok && tiles == 2) ok = warp_wait(&bars[S_K_FULL + 2 * g + 1], kb_count++ & 1, ab, kDevTimeoutMma);
+                for (int i = 0; i < w.ktiles && ok; ++i) {
+                    if (!w.has(rb, i)) continue;
+                    const int q0 = w.first_tile(rb, i), q1 = w.end_tile(rb), buf = kc & 1;
+                    ok = warp_wait(&bars[S_K_FULL + buf], (kc >> 1) & 1, ab, kDevTimeoutMma);
                     for (int t = q0; t < q1 && ok; ++t) {
-                        const uint32_t qb = q_lo + (t - rb * w.per) * (Lay::kTile >> 4);
-#pragma unroll
-                        for (int a = 0; a < 2; ++a) {
-                            if (a == tiles || !ok) break;
-                            const int place = 2 * g + a;
-                            ok = warp_wait(&bars[S_S_FREE + place], (uc[a]++ & 1) ^ 1, ab, kDevTimeoutMma);
-                            tc_fence_after();
-                            if (ok && elect_one()) {
-                                const uint32_t d = tmem + 128u * place, ka = k_lo + place * (Lay::kTile >> 4);
-                                mma_f16_ss_at<0, 0>(d, ka, qb, hi, idesc, 0);
-                                mma_f16_ss_at<2, 2>(d, ka, qb, hi, idesc, 1);
-                                mma_f16_ss_at<4, 4>(d, ka, qb, hi, idesc, 1);
-                                mma_f16_ss_at<6, 6>(d, ka, qb, hi, idesc, 1);
-                                if (D == 128) {
-                                    mma_f16_ss_at<1024, 1024>(d, ka, qb, hi, idesc, 1);
-                                    mma_f16_ss_at<1026, 1026>(d, ka, qb, hi, idesc, 1);
-                                    mma_f16_ss_at<1028, 1028>(d, ka, qb, hi, idesc, 1);
-                                    mma_f16_ss_at<1030, 1030>(d, ka, qb, hi, idesc, 1);
-                                }
-                                mma_commit(&bars[S_S_FULL + place]);
-                                if (t + 1 == q1) mma_commit(&bars[S_K_EMPTY + place]);
+                        ok = warp_wait(&bars[S_S_FREE + place], (phase & 1) ^ 1, ab, kDevTimeoutMma);
+                        tc_fence_after();
+                        if (ok && elect_one()) {
+                            const uint32_t d = tmem + 128u * place, ka = tmem + kStTmemK + (D / 2) * buf;
+                            const uint32_t qb = q_lo + (t - rb * w.per) * (Lay::kTile >> 4);
+                            mma_f16_ts_at<0, 0>(d, ka, qb, hi, idesc, 0);
+                            mma_f16_ts_at<8, 2>(d, ka, qb, hi, idesc, 1);
+                            mma_f16_ts_at<16, 4>(d, ka, qb, hi, idesc, 1);
+                            mma_f16_ts_at<24, 6>(d, ka, qb, hi, idesc, 1);
+                            if (D == 128) {
+                                mma_f16_ts_at<32, 1024>(d, ka, qb, hi, idesc, 1);
+                                mma_f16_ts_at<40, 1026>(d, ka, qb, hi, idesc, 1);
+                                mma_f16_ts_at<48, 1028>(d, ka, qb, hi, idesc, 1);
+                                mma_f16_ts_at<56, 1030>(d, ka, qb, hi, idesc, 1);
                             }
-                            __syncwarp();
+                            mma_commit(&bars[S_S_FULL + place]);
+                            if (t + 1 == q1) mma_commit(&bars[S_K_EMPTY + buf]);
+                        }
+                        __syncwarp();
+                        if (++place == kStGroups) {
+                            place = 0;
+                            ++phase;
                         }
                     }
+                    ++kc;
                 }
             }
             // every product has finished before the tensor memory is released
@@ -193,44 +196,49 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             while (!mbar_try_wait(&bars[S_DRAIN], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
         }
-    } else if (wg <= 4) {
+    } else if (wg <= kStGroups) {
         // ------------------------------------------------------------ sums
-        regs_inc<80>();
-        const int place = wg - 1, g = place >> 1, a = place & 1, quad = warp & 3;
+        regs_inc<112>();
+        const int g = wg - 1;
         const int st = tid - 128;  // number among the groups' threads
-        const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * place;
+        const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * g;
         const float2 c2 = make_float2(p.sm_log2, p.sm_log2);
         float* minus = reinterpret_cast<float*>(smem + Lay::kMinus);
-        int pc = 0, n = 0;  // pairs, units of this group
+        float* part = reinterpret_cast<float*>(smem + Lay::kPart) + quad * 32 + lane;
+        // K tiles; units of this group; whose turn the next unit is (0: this
+        // group's); whose the next K tile is
+        int kc = 0, n = 0, turn = g, mine = g;
+        int last = 0;     // the K tile that this group has still to add up: its first token here
+        bool due = false;
+        float old = 0.f;  // and its scores so far
         bool ok = true;
+        // adds up the sums of the K tile number k
+        auto join = [&](int k) {
+            const int slot = k & (kStParts - 1);
+            ok = warp_wait(&bars[S_PART_FULL + slot], (k / kStParts) & 1, ab, kDevTimeoutEpilogue);
+            if (!ok) return;
+            const float* x = part + slot * (kStGroups * kStTile);
+            const float sum = (x[0] + x[kStTile]) + x[2 * kStTile];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[S_PART_EMPTY + slot]);
+            if (last < stop) p.out[row_at + last] = old + (last < w.end ? sum : 0.f);
+            due = false;
+        };
         for (int rb = 0; rb < w.blocks && ok; ++rb) {
             // the block's query rows: thread st has the piece st % kPieces of the
             // rows st / kPieces + i kRows; and lse of each row
             if (rb > 0) ok = warp_wait(&bars[S_Q_EMPTY], (rb - 1) & 1, ab, kDevTimeoutSoftmax);
             if (!ok) break;
-            constexpr int kPieces = D / 8, kRows = kStSums / kPieces, kBatch = 6;
+            constexpr int kPieces = D / 8, kRows = kStSums / kPieces;
             const int first = rb * w.per * kStTile, count = (w.end_tile(rb) - rb * w.per) * kStTile;
-            for (int r0 = st / kPieces; r0 < count; r0 += kBatch * kRows) {
-                uint4 v[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int rw = first + r0 + i * kRows;
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (r0 + i * kRows < count && rw < w.rows) {
-                        const int tok = p.group == 1 ? rw : rw / p.group, head = h * p.group + rw - tok * p.group;
-                        v[i] = ldg_nc_na_v4(p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride +
-                                            static_cast<int64_t>(head) * D + 8 * (st % kPieces));
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int row = r0 + i * kRows;
-                    if (row < count)
-                        *reinterpret_cast<uint4*>(smem + Lay::kQ + (row >> 7) * Lay::kTile +
-                                                  bktile_off(row & 127, 8 * (st % kPieces))) =
-                            make_uint4(__byte_perm(v[i].x, v[i].y, 0x5410), __byte_perm(v[i].x, v[i].y, 0x7632),
-                                       __byte_perm(v[i].z, v[i].w, 0x5410), __byte_perm(v[i].z, v[i].w, 0x7632));
-                }
+#pragma unroll 4
+            for (int row = st / kPieces; row < count; row += kRows) {
+                const int rw = first + row, tok = p.group == 1 ? rw : rw / p.group, head = h * p.group + rw - tok * p.group;
+                const bool have = rw < w.rows;
+                const __nv_bfloat16* src =
+                    have ? p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D : p.q;
+                cp_async16_or_zero(smem + Lay::kQ + (row >> 7) * Lay::kTile + bktile_off(row & 127, 8 * (st % kPieces)),
+                                   src + 8 * (st % kPieces), have);
             }
             for (int row = st; row < count; row += kStSums) {
                 const int rw = first + row;
@@ -242,163 +250,171 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 }
                 minus[row] = m;
             }
+            cp_async_wait_all();
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_Q_FULL]);
             ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutSoftmax);
-            for (int pair = 0; pair < w.pairs && ok; ++pair) {
-                const int jp = j0 + pair * 2 * kStTile;
-                const int j = jp + a * kStTile + quad * 32 + lane;  // the thread's token
-                if (!w.has(rb, pair)) {
-                    // no row of any block sees the pair
-                    if (rb == 0 && g == 0 && w.first_row(jp) >= w.rows && j < stop) p.out[row_at + j] = p.scores[row_at + j];
+            for (int i = 0; i < w.ktiles && ok; ++i) {
+                const int jt = j0 + i * kStTile, j = jt + quad * 32 + lane;  // the tile's first token, the thread's
+                if (!w.has(rb, i)) {
+                    // no row of any block sees the tile
+                    if (rb == 0 && g == 0 && w.first_row(jt) >= w.rows && j < stop) p.out[row_at + j] = p.scores[row_at + j];
                     continue;
                 }
-                if ((pc++ & 1) != g) continue;
-                // the first block of rows that sees the pair starts from the given scores
-                const float* from = rb == w.first_row(jp) / kStTile / w.per ? p.scores : p.out;
+                const int q0 = w.first_tile(rb, i), q1 = w.end_tile(rb);
+                float next_old = 0.f;
+                if (mine == 0 && j < stop) {
+                    // the first block of rows that sees the tile starts from the given scores
+                    const float* from = rb == w.first_row(jt) / kStTile / w.per ? p.scores : p.out;
+                    next_old = from[row_at + j];
+                }
                 float2 acc[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
-                if (a == 0 || w.second(pair)) {
-                    const int q0 = w.first_tile(rb, pair), q1 = w.end_tile(rb);
-                    const int seen = w.first_row(j);  // the first row that sees the token
-                    for (int t = q0; t < q1; ++t, ++n) {
-                        ok = warp_wait(&bars[S_S_FULL + place], n & 1, ab, kDevTimeoutSoftmax);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const float* mt = minus + (t - rb * w.per) * kStTile;
-                        const int lo = seen - t * kStTile;  // columns from this on count
-                        const bool full = __all_sync(0xffffffffu, lo <= 0);
+                const int seen = w.first_row(j);  // the first row that sees the token
+                for (int t = q0; t < q1; ++t) {
+                    const bool ours = turn == 0;
+                    turn = turn == 0 ? kStGroups - 1 : turn - 1;
+                    if (!ours) continue;
+                    ok = warp_wait(&bars[S_S_FULL + g], n++ & 1, ab, kDevTimeoutSoftmax);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float* mt = minus + (t - rb * w.per) * kStTile;
+                    const int lo = seen - t * kStTile;  // columns from this on count
+                    const bool full = __all_sync(0xffffffffu, lo <= 0);
 #pragma unroll 1
-                        for (int c0 = 0; c0 < kStTile; c0 += 32) {
-                            uint32_t v[32];
-                            tmem_ld32(at + c0, v);
-                            if (c0 + 32 == kStTile) {
-                                // the scores are in registers: their place is free
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(&bars[S_S_FREE + place]);
-                            }
-                            float2 x[16];
+                    for (int c0 = 0; c0 < kStTile; c0 += 64) {
+                        uint32_t v[64];
+                        tmem_ld64(at + c0, v);
+                        if (c0 != 0) {
+                            // the scores are in registers: their place is free
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars[S_S_FREE + g]);
+                        }
 #pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                const float4 m = *reinterpret_cast<const float4*>(mt + c0 + 2 * k);
-                                x[k] = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2,
+                        for (int c = 0; c < 64; c += 16) {
+                            float2 x[8];
+#pragma unroll
+                            for (int k = 0; k < 8; k += 2) {
+                                const float4 m = *reinterpret_cast<const float4*>(mt + c0 + c + 2 * k);
+                                x[k] = fma2(make_float2(__uint_as_float(v[c + 2 * k]), __uint_as_float(v[c + 2 * k + 1])), c2,
                                             make_float2(m.x, m.y));
-                                x[k + 1] = fma2(make_float2(__uint_as_float(v[2 * k + 2]), __uint_as_float(v[2 * k + 3])), c2,
-                                                make_float2(m.z, m.w));
+                                x[k + 1] = fma2(make_float2(__uint_as_float(v[c + 2 * k + 2]), __uint_as_float(v[c + 2 * k + 3])),
+                                                c2, make_float2(m.z, m.w));
                             }
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) x[k] = make_float2(ex2(x[k].x), ex2(x[k].y));
+                            for (int k = 0; k < 8; ++k) x[k] = make_float2(ex2(x[k].x), ex2(x[k].y));
                             if (!full) {
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) {
-                                    if (c0 + 2 * k < lo) x[k].x = 0.f;
-                                    if (c0 + 2 * k + 1 < lo) x[k].y = 0.f;
+                                for (int k = 0; k < 8; ++k) {
+                                    if (c0 + c + 2 * k < lo) x[k].x = 0.f;
+                                    if (c0 + c + 2 * k + 1 < lo) x[k].y = 0.f;
                                 }
                             }
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) acc[k & 3] = add2(acc[k & 3], x[k]);
+                            for (int k = 0; k < 8; ++k) acc[k & 3] = add2(acc[k & 3], x[k]);
                         }
                     }
-                    if (!ok) break;
                 }
-                if (j < stop) {
-                    const float2 x = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
-                    p.out[row_at + j] = from[row_at + j] + (j < q.kv ? x.x + x.y : 0.f);
+                if (!ok) break;
+                // this group's share of the K tile
+                const int slot = kc & (kStParts - 1);
+                ok = warp_wait(&bars[S_PART_EMPTY + slot], ((kc / kStParts) & 1) ^ 1, ab, kDevTimeoutEpilogue);
+                if (!ok) break;
+                const float2 x = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+                part[(slot * kStGroups + g) * kStTile] = x.x + x.y;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[S_PART_FULL + slot]);
+                // the K tile before, which every group has left by now or soon will have
+                if (due) join(kc - 1);
+                if (mine == 0) {
+                    due = true;
+                    last = j;
+                    old = next_old;
                 }
+                mine = mine == 0 ? kStGroups - 1 : mine - 1;
+                ++kc;
             }
+            if (due && ok) join(kc - 1);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_Q_EMPTY]);
         }
     } else {
         // ------------------------------------------------------------ K
-        // Each warpgroup has one tile of every pair.  Thread ct: the pieces of 16
-        // dims ct % 4 (+ 4 in the second 64 dims) of the rows ct / 4 + 32 m.  Lane
-        // l < 8 of a warp looks up the block of 16 tokens l of the tile.
-        const int ct = tid & 127, a = wg - 5;
-        constexpr int NB = D / 64;
-        const int rr = ct >> 2, pb = p.g.page_shift - 4;
-        const uint8_t* kbase = p.g.kcodes + (rr & 15) * D + 16 * (ct & 3);
-        const uint8_t* sbase = p.g.kscale + (rr & 15);
+        // A thread has D / 2 of the dims of one token a tile.
+        regs_dec<56>();
+        const int ct = tid & 127, half = wg - 1 - kStGroups;
+        constexpr int NB = D / 32;  // 16-byte pieces of the codes
+        const int shift = p.g.page_shift, place = (1 << shift) - 1;
+        const uint8_t* kbase = p.g.kcodes + half * (D / 2);
         const uint32_t* table =
             reinterpret_cast<const uint32_t*>(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages);
-        uint4 kr[4 * NB];
-        uint32_t ks[4];
-        // the next pair with work after (rb, pair); pair = -1 starts; rb = blocks ends
-        auto advance = [&](int& rb, int& pair) {
+        const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kStTmemK + half * (D / 4);
+        // the next K tile with work after (rb, i); i = -1 starts; rb = blocks ends
+        struct Step {
+            int rb, i;
+        };
+        auto advance = [&](Step& x) {
+            if (x.rb >= w.blocks) return;
             do {
-                if (++pair == w.pairs) {
-                    pair = 0;
-                    ++rb;
+                if (++x.i == w.ktiles) {
+                    x.i = 0;
+                    ++x.rb;
                 }
-            } while (rb < w.blocks && !w.has(rb, pair));
+            } while (x.rb < w.blocks && !w.has(x.rb, x.i));
         };
-        auto token = [&](int pair) { return j0 + (2 * pair + a) * kStTile + 16 * (lane & 7); };
-        auto entry = [&](int rb, int pair) {
-            const int t = token(pair);
-            return rb < w.blocks && t < q.kv ? static_cast<int>(ldg_early(table + (t >> p.g.page_shift))) : 0;
+        auto entry = [&](const Step& x) {
+            const int t = j0 + x.i * kStTile + ct;
+            return x.rb < w.blocks && t < q.kv ? static_cast<int>(ldg_early(table + (t >> shift))) : 0;
         };
-        // (blocks behind the end, or on a bad page, read block 0: their sums are not used)
-        auto block_of = [&](int rb, int pair, int page) {
-            const int t = token(pair);
-            if (rb >= w.blocks || t >= q.kv) return 0u;
-            const uint32_t at = static_cast<uint32_t>(check_page(p.g, page) ? page : 0) * p.g.kv_heads + h;
-            return (at << pb) + (static_cast<uint32_t>(t >> 4) & ((1u << pb) - 1u));
-        };
-        auto fetch = [&](int m, uint32_t blk) {
-            const uint64_t at = __shfl_sync(0xffffffffu, blk, (rr >> 4) + 2 * m);
+        uint4 kr[2][NB];
+        uint32_t ks[2];
+        // (tokens behind the end, or on a bad page, read the first token of page 0: their sums are not used)
+        auto fetch = [&](uint4 (&k)[NB], uint32_t& scale, const Step& x, int page) {
+            const int t = j0 + x.i * kStTile + ct;
+            const bool have = x.rb < w.blocks && t < q.kv && check_page(p.g, page);
+            const uint64_t row = have ? (static_cast<uint64_t>(static_cast<uint32_t>(page) * p.g.kv_heads + h) << shift) + (t & place) : 0u;
+            const uint4* src = reinterpret_cast<const uint4*>(kbase + row * D);
 #pragma unroll
-            for (int x = 0; x < NB; ++x) kr[m * NB + x] = ldg_nc_na_v4(kbase + at * (16 * D) + 64 * x);
-            ks[m] = ldg_early(sbase + at * 16);
+            for (int c = 0; c < NB; ++c) k[c] = __ldg(src + c);
+            scale = ldg_early(p.g.kscale + row);
         };
-        int rb = 0, pair = -1, pc = 0;
-        int uses[2] = {0, 0};  // of each buffer of the tile so far
-        advance(rb, pair);
-        int rb1 = rb, pair1 = pair;
-        if (rb < w.blocks) {
-            const uint32_t blk = block_of(rb, pair, entry(rb, pair));
-#pragma unroll
-            for (int m = 0; m < 4; ++m) fetch(m, blk);
-            advance(rb1, pair1);
-        }
-        int ahead = entry(rb1, pair1);
+        Step now{0, -1};
+        advance(now);
+        Step next = now;
+        fetch(kr[0], ks[0], next, entry(next));
+        advance(next);
+        fetch(kr[1], ks[1], next, entry(next));
+        advance(next);
+        int ahead = entry(next);
         bool ok = true;
-        while (ok && rb < w.blocks) {
-            const uint32_t blk = block_of(rb1, pair1, ahead);
-            int rb2 = rb1, pair2 = pair1;
-            if (rb1 < w.blocks) advance(rb2, pair2);
-            ahead = entry(rb2, pair2);
-            const bool there = a == 0 || w.second(pair);
-            const int buf = 2 * (pc & 1) + a;  // (the group of the pair, the tile of the pair)
-            if (there) ok = warp_wait(&bars[S_K_EMPTY + buf], (uses[pc & 1]++ & 1) ^ 1, ab, kDevTimeoutConvert);
-            uint8_t* dst = smem + Lay::kK + buf * Lay::kTile;
-            uint8_t* lo = dst + bktile_off(rr, 16 * (ct & 3));
-            uint8_t* hi = dst + bktile_off(rr, 16 * (ct & 3) + 8);
+        for (int kc = 0; ok && now.rb < w.blocks; kc += 2) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                if (ok && there) {
-                    const uint32_t f1 = scale_factor(ks[m]);
-                    const uint32_t f[8] = {f1, f1, f1, f1, f1, f1, f1, f1};
+            for (int buf = 0; buf < 2; ++buf) {
+                if (!ok || now.rb >= w.blocks) break;
+                ok = warp_wait(&bars[S_K_EMPTY + buf], ((kc >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t f = scale_factor(ks[buf]);
 #pragma unroll
-                    for (int x = 0; x < NB; ++x) {
-                        const int off = x * (kStTile * 128) + m * (32 * 128);
-                        put16(lo + off, hi + off, kr[m * NB + x], f);
-                    }
+                for (int c = 0; c < NB; ++c) {
+                    const uint4 k = kr[buf][c];
+                    const uint32_t v[8] = {bf2_mul(codes01(k.x), f), bf2_mul(codes23(k.x), f), bf2_mul(codes01(k.y), f),
+                                           bf2_mul(codes23(k.y), f), bf2_mul(codes01(k.z), f), bf2_mul(codes23(k.z), f),
+                                           bf2_mul(codes01(k.w), f), bf2_mul(codes23(k.w), f)};
+                    tmem_st8(to + (D / 2) * buf + 8 * c, v);
                 }
-                fetch(m, blk);  // the next pair's rows, into the registers just freed
-            }
-            if (ok && there) {
-                fence_async_smem();
+                fetch(kr[buf], ks[buf], next, ahead);  // two tiles on, into the registers just freed
+                advance(next);
+                ahead = entry(next);
+                tmem_st_wait();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[S_K_FULL + buf]);
+                advance(now);
             }
-            ++pc;
-            rb = rb1;
-            pair = pair1;
-            rb1 = rb2;
-            pair1 = pair2;
         }
     }
 
@@ -422,11 +438,11 @@ cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
     // set-up takes as long as several tiles: one sequence of 8,000 tokens x 8 KV
     // heads, 128 ranges of two tiles 15.6 us, 256 of one 22.7), at least two
     // tiles each.
-    const int64_t rows = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
-    const int64_t pairs = (p.g.max_kv + 255) / 256;
-    const int64_t ranges = std::min<int64_t>(pairs, std::max<int64_t>(1, 152 / rows));
-    const int range = static_cast<int>((pairs + ranges - 1) / ranges) * 256;
-    const int64_t blocks = (p.g.max_kv + range - 1) / range * rows;
+    const int64_t lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
+    const int64_t tiles = (p.g.max_kv + kStTile - 1) / kStTile;
+    const int64_t ranges = std::min<int64_t>((tiles + 1) / 2, std::max<int64_t>(1, 152 / lists));
+    const int range = static_cast<int>((tiles + ranges - 1) / ranges) * kStTile;
+    const int64_t blocks = (p.g.max_kv + range - 1) / range * lists;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     paged_scores_tc_kernel<D><<<static_cast<unsigned>(blocks), kStThreads, smem, s>>>(p, range);
     return cudaGetLastError();
