@@ -182,6 +182,12 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// 32-byte read-only global load (32-byte aligned).
+__device__ __forceinline__ void ldg_nc_32(const void* p, uint4& a, uint4& b) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+}
 // 16-byte read-only global load that does not allocate in L1 (the data is
 // used once; allocating would evict lines the SM's shared memory traffic needs).
 __device__ __forceinline__ uint4 ldg_nc_na_v4(const void* p) {

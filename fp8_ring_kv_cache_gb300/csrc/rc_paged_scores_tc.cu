@@ -69,12 +69,12 @@ struct StLayout {
 // that sees the K tile's first token.
 struct StWork {
     int j0, end;  // the range's first token, the end of its tokens that exist
-    int old;      // tokens that every query sees (causal)
+    int old, n;   // tokens that every query sees (causal), new tokens
     int rows, group, tiles, per, blocks, ktiles;
     bool causal;
     __device__ __forceinline__ int first_row(int j) const {  // first row that sees token j (>= rows: none)
-        const int64_t r = causal ? static_cast<int64_t>(max(0, j - old)) * group : 0;
-        return static_cast<int>(min(r, static_cast<int64_t>(rows)));
+        if (!causal || j <= old) return 0;
+        return j - old < n ? (j - old) * group : rows;
     }
     __device__ __forceinline__ int first_tile(int rb, int i) const {
         return max(rb * per, first_row(j0 + i * kStTile) / kStTile);
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
     w.j0 = j0;
     w.end = min(q.kv, j0 + range);
     w.old = q.kv - q.n;
+    w.n = q.n;
     w.rows = q.n * p.group;
     w.group = p.group;
     w.causal = p.causal != 0;
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 float next_old = 0.f;
                 if (mine == 0 && j < stop) {
                     // the first block of rows that sees the tile starts from the given scores
-                    const float* from = rb == w.first_row(jt) / kStTile / w.per ? p.scores : p.out;
+                    const float* from = rb == 0 || w.first_row(jt) >= rb * w.per * kStTile ? p.scores : p.out;
                     next_old = from[row_at + j];
                 }
                 float2 acc[4];
@@ -346,9 +347,10 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         // A thread has D / 2 of the dims of one token a tile.
         regs_dec<56>();
         const int ct = tid & 127, half = wg - 1 - kStGroups;
-        constexpr int NB = D / 32;  // 16-byte pieces of the codes
+        constexpr int NB = D / 32;  // 16-byte pieces of the codes, read in pairs
         const int shift = p.g.page_shift, place = (1 << shift) - 1;
         const uint8_t* kbase = p.g.kcodes + half * (D / 2);
+        const bool wide = (reinterpret_cast<uintptr_t>(p.g.kcodes) & 31u) == 0;  // 32-byte loads are aligned
         const uint32_t* table =
             reinterpret_cast<const uint32_t*>(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages);
         const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kStTmemK + half * (D / 4);
@@ -376,9 +378,16 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             const int t = j0 + x.i * kStTile + ct;
             const bool have = x.rb < w.blocks && t < q.kv && check_page(p.g, page);
             const uint64_t row = have ? (static_cast<uint64_t>(static_cast<uint32_t>(page) * p.g.kv_heads + h) << shift) + (t & place) : 0u;
-            const uint4* src = reinterpret_cast<const uint4*>(kbase + row * D);
+            const uint8_t* src = kbase + row * D;
 #pragma unroll
-            for (int c = 0; c < NB; ++c) k[c] = __ldg(src + c);
+            for (int c = 0; c < NB; c += 2) {
+                if (wide) {
+                    ldg_nc_32(src + 16 * c, k[c], k[c + 1]);
+                } else {
+                    k[c] = __ldg(reinterpret_cast<const uint4*>(src + 16 * c));
+                    k[c + 1] = __ldg(reinterpret_cast<const uint4*>(src + 16 * c + 16));
+                }
+            }
             scale = ldg_early(p.g.kscale + row);
         };
         Step now{0, -1};

@@ -775,3 +775,29 @@ def test_a_wait_that_runs_out_is_reported_and_forgotten(rc):
         st.cache.accumulate(st.batch, q.cuda(), lse, sc2)
         st.cache.sync()
         assert torch.equal(sc2, sc)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_pages_on_a_16_byte_boundary(rc, dim):
+    """Pages whose address is a multiple of 16 bytes but not of 32 give the same bits."""
+    st = Setup(rc, [(3, 200), (150, 600)], 2, dim, 16, seed=95)
+    q = bf16(st.rng, st.tokens, 4, dim).cuda()
+
+    def moved(t):
+        flat = torch.zeros(t.numel() + 64, dtype=torch.uint8, device="cuda")
+        at = 16 + (-flat.data_ptr()) % 32
+        new = flat[at:at + t.numel()].view(t.shape)
+        assert new.data_ptr() % 32 == 16
+        return new.copy_(t)
+
+    res = []
+    for cache in (st.cache, rc.PagedKVCache(*(moved(getattr(st.cache, x)) for x in ("kcodes", "vcodes", "kscale", "vscale")))):
+        out, lse = torch.zeros_like(q), torch.zeros((st.tokens, 4), device="cuda")
+        sc = torch.zeros((2, 2, st.max_kv), device="cuda")
+        cache.attend(st.batch, q, out, lse=lse)
+        cache.accumulate(st.batch, q, lse, sc)
+        k = bf16(np.random.default_rng(1), st.tokens, 2, dim).cuda()
+        cache.write(st.batch, k, k, torch.zeros((1, st.tokens), dtype=torch.int32, device="cuda"), rc.RopeAxes((dim // 2,)))
+        cache.sync()
+        res.append((out, lse, sc, cache.kcodes, cache.vcodes, cache.kscale, cache.vscale))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
