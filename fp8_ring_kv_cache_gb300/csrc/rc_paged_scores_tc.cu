@@ -67,13 +67,13 @@ struct StLayout {
 // What a block does, in the same order for every role: for each block of rows,
 // each K tile that some of its rows see; of those, the query tiles from the first
 // that sees the K tile's first token.
+template <bool CAUSAL>
 struct StWork {
     int j0, end;  // the range's first token, the end of its tokens that exist
     int old, n;   // tokens that every query sees (causal), new tokens
     int rows, group, tiles, per, blocks, ktiles;
-    bool causal;
     __device__ __forceinline__ int first_row(int j) const {  // first row that sees token j (>= rows: none)
-        if (!causal || j <= old) return 0;
+        if (!CAUSAL || j <= old) return 0;
         return j - old < n ? (j - old) * group : rows;
     }
     __device__ __forceinline__ int first_tile(int rb, int i) const {
@@ -85,7 +85,7 @@ struct StWork {
     }
 };
 
-template <int D>
+template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedScoreParams p, int range) {
     using Lay = StLayout<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -101,14 +101,13 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
     if (j0 >= p.g.max_kv) return;
     const Seq q = load_seq(p.g, s);
     const int64_t row_at = (static_cast<int64_t>(s) * p.g.kv_heads + h) * p.score_stride;
-    StWork w;
+    StWork<CAUSAL> w;
     w.j0 = j0;
     w.end = min(q.kv, j0 + range);
     w.old = q.kv - q.n;
     w.n = q.n;
     w.rows = q.n * p.group;
     w.group = p.group;
-    w.causal = p.causal != 0;
     w.tiles = (w.rows + kStTile - 1) / kStTile;
     w.blocks = (w.tiles + kStQTiles - 1) / kStQTiles;
     w.per = w.blocks > 0 ? (w.tiles + w.blocks - 1) / w.blocks : 1;
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                     tc_fence_after();
                     const float* mt = minus + (t - rb * w.per) * kStTile;
                     const int lo = seen - t * kStTile;  // columns from this on count
-                    const bool full = __all_sync(0xffffffffu, lo <= 0);
+                    const bool full = !CAUSAL || __all_sync(0xffffffffu, lo <= 0);
 #pragma unroll 1
                     for (int c0 = 0; c0 < kStTile; c0 += 64) {
                         uint32_t v[64];
@@ -436,12 +435,12 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
     }
 }
 
-template <int D>
+template <int D, bool CAUSAL>
 cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
     static std::atomic<uint64_t> configured{0};
     constexpr uint32_t smem = StLayout<D>::kAlloc;
     static_assert(smem <= 227 * 1024, "shared memory over the sm_103 limit");
-    cudaError_t e = smem_limit_once(paged_scores_tc_kernel<D>, smem, configured);
+    cudaError_t e = smem_limit_once(paged_scores_tc_kernel<D, CAUSAL>, smem, configured);
     if (e != cudaSuccess) return e;
     // Ranges of cached tokens: as many blocks as fill the SMs once (a block's
     // set-up takes as long as several tiles: one sequence of 8,000 tokens x 8 KV
@@ -453,14 +452,15 @@ cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
     const int range = static_cast<int>((tiles + ranges - 1) / ranges) * kStTile;
     const int64_t blocks = (p.g.max_kv + range - 1) / range * lists;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    paged_scores_tc_kernel<D><<<static_cast<unsigned>(blocks), kStThreads, smem, s>>>(p, range);
+    paged_scores_tc_kernel<D, CAUSAL><<<static_cast<unsigned>(blocks), kStThreads, smem, s>>>(p, range);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_paged_scores_tc(const PagedScoreParams& p, int D, cudaStream_t s) {
-    return D == 128 ? launch_d<128>(p, s) : launch_d<64>(p, s);
+    if (D == 128) return p.causal ? launch_d<128, true>(p, s) : launch_d<128, false>(p, s);
+    return p.causal ? launch_d<64, true>(p, s) : launch_d<64, false>(p, s);
 }
 
 }  // namespace rc
