@@ -11,7 +11,7 @@
 //                  128 x 128 scores and two K tiles
 //   warps 4 .. 15  three groups, one a place: exp2(S c - lse) and the sum over the
 //                  columns, a token a thread.  The units (K tile, query tile) go
-//                  to the groups in turn; a group's sums of a K tile are put in
+//                  to the groups in turn; a group's sums of a pair of K tiles are put in
 //                  shared memory, and the groups take turns in adding the three
 //                  up, always in the same order: no two threads add to one entry.
 //                  They also bring the query rows (by cp.async).
@@ -36,7 +36,8 @@ constexpr int kStGroups = 3;
 constexpr int kStSums = 128 * kStGroups;  // threads of the groups
 constexpr int kStTile = 128;
 constexpr int kStQTiles = 6;  // query tiles in shared memory
-constexpr int kStParts = 4;   // K tiles whose sums are in shared memory
+constexpr int kStParts = 4;   // pairs of K tiles whose sums are in shared memory
+constexpr int kStPair = 2 * kStTile;
 constexpr uint32_t kStTmemK = 128 * kStGroups;
 
 enum : int {
@@ -44,7 +45,7 @@ enum : int {
     S_K_EMPTY = 2,     // [2] its products have finished
     S_S_FULL = 4,      // [3] scores of a unit in TMEM
     S_S_FREE = 7,      // [3] the group has read them
-    S_PART_FULL = 10,  // [4] every group's sums of a K tile are in place
+    S_PART_FULL = 10,  // [4] every group's sums of a pair of K tiles are in place
     S_PART_EMPTY = 14, // [4] they have been added up
     S_Q_FULL = 18,     // the block's query rows are in place
     S_Q_EMPTY = 19,    // every group is through with them
@@ -57,8 +58,8 @@ struct StLayout {
     static constexpr uint32_t kTile = kStTile * D * 2;
     static constexpr uint32_t kQ = 0;                           // [6]
     static constexpr uint32_t kMinus = kQ + kStQTiles * kTile;  // fp32 [6][128]: -lse log2(e)
-    static constexpr uint32_t kPart = kMinus + kStQTiles * kStTile * 4;  // fp32 [4][3][128]
-    static constexpr uint32_t kBar = kPart + kStParts * kStGroups * kStTile * 4;
+    static constexpr uint32_t kPart = kMinus + kStQTiles * kStTile * 4;  // fp32 [4][3][256]
+    static constexpr uint32_t kBar = kPart + kStParts * kStGroups * kStPair * 4;
     static constexpr uint32_t kMisc = kBar + 8 * S_COUNT;
     static constexpr uint32_t kTotal = kMisc + 16;
     static constexpr uint32_t kAlloc = kTotal + 1024;
@@ -205,23 +206,30 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         const float2 c2 = make_float2(p.sm_log2, p.sm_log2);
         float* minus = reinterpret_cast<float*>(smem + Lay::kMinus);
         float* part = reinterpret_cast<float*>(smem + Lay::kPart) + quad * 32 + lane;
-        // K tiles; units of this group; whose turn the next unit is (0: this
-        // group's); whose the next K tile is
-        int kc = 0, n = 0, turn = g, mine = g;
-        int last = 0;     // the K tile that this group has still to add up: its first token here
+        // pairs of K tiles; units of this group; whose turn the next unit is (0:
+        // this group's); whose the next pair is
+        int pc = 0, n = 0, turn = g, mine = g;
+        int last = 0;                // the pair that this group has still to add up: its first token here
         bool due = false;
-        float old = 0.f;  // and its scores so far
+        float old[2] = {0.f, 0.f};  // and its scores so far
         bool ok = true;
-        // adds up the sums of the K tile number k
+        const int tail = min(stop, j0 + w.ktiles * kStTile);
+        // adds up the sums of the pair number k
         auto join = [&](int k) {
             const int slot = k & (kStParts - 1);
             ok = warp_wait(&bars[S_PART_FULL + slot], (k / kStParts) & 1, ab, kDevTimeoutEpilogue);
             if (!ok) return;
-            const float* x = part + slot * (kStGroups * kStTile);
-            const float sum = (x[0] + x[kStTile]) + x[2 * kStTile];
+            const float* x = part + slot * (kStGroups * kStPair);
+            float sum[2];
+#pragma unroll
+            for (int a = 0; a < 2; ++a, x += kStTile) sum[a] = (x[0] + x[kStPair]) + x[2 * kStPair];
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_PART_EMPTY + slot]);
-            if (last < stop) p.out[row_at + last] = old + (last < w.end ? sum : 0.f);
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const int j = last + a * kStTile;
+                if (j < tail) p.out[row_at + j] = old[a] + (j < w.end ? sum[a] : 0.f);
+            }
             due = false;
         };
         for (int rb = 0; rb < w.blocks && ok; ++rb) {
@@ -255,89 +263,97 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_Q_FULL]);
             ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutSoftmax);
-            for (int i = 0; i < w.ktiles && ok; ++i) {
-                const int jt = j0 + i * kStTile, j = jt + quad * 32 + lane;  // the tile's first token, the thread's
+            for (int i = 0; i < w.ktiles && ok; i += 2) {
+                const int jt = j0 + i * kStTile, j = jt + quad * 32 + lane;  // the pair's first token, the thread's first
                 if (!w.has(rb, i)) {
-                    // no row of any block sees the tile
-                    if (rb == 0 && g == 0 && w.first_row(jt) >= w.rows && j < stop) p.out[row_at + j] = p.scores[row_at + j];
+                    // no row of any block sees the pair
+                    if (rb == 0 && g == 0 && w.first_row(jt) >= w.rows)
+                        for (int a = j; a < min(tail, jt + kStPair); a += kStTile) p.out[row_at + a] = p.scores[row_at + a];
                     continue;
                 }
-                const int q0 = w.first_tile(rb, i), q1 = w.end_tile(rb);
-                float next_old = 0.f;
-                if (mine == 0 && j < stop) {
+                float next_old[2] = {0.f, 0.f};
+                if (mine == 0) {
                     // the first block of rows that sees the tile starts from the given scores
-                    const float* from = rb == 0 || w.first_row(jt) >= rb * w.per * kStTile ? p.scores : p.out;
-                    next_old = from[row_at + j];
-                }
-                float2 acc[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
-                const int seen = w.first_row(j);  // the first row that sees the token
-                for (int t = q0; t < q1; ++t) {
-                    const bool ours = turn == 0;
-                    turn = turn == 0 ? kStGroups - 1 : turn - 1;
-                    if (!ours) continue;
-                    ok = warp_wait(&bars[S_S_FULL + g], n++ & 1, ab, kDevTimeoutSoftmax);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const float* mt = minus + (t - rb * w.per) * kStTile;
-                    const int lo = seen - t * kStTile;  // columns from this on count
-                    const bool full = !CAUSAL || __all_sync(0xffffffffu, lo <= 0);
-#pragma unroll 1
-                    for (int c0 = 0; c0 < kStTile; c0 += 64) {
-                        uint32_t v[64];
-                        tmem_ld64(at + c0, v);
-                        if (c0 != 0) {
-                            // the scores are in registers: their place is free
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars[S_S_FREE + g]);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 64; c += 16) {
-                            float2 x[8];
-#pragma unroll
-                            for (int k = 0; k < 8; k += 2) {
-                                const float4 m = *reinterpret_cast<const float4*>(mt + c0 + c + 2 * k);
-                                x[k] = fma2(make_float2(__uint_as_float(v[c + 2 * k]), __uint_as_float(v[c + 2 * k + 1])), c2,
-                                            make_float2(m.x, m.y));
-                                x[k + 1] = fma2(make_float2(__uint_as_float(v[c + 2 * k + 2]), __uint_as_float(v[c + 2 * k + 3])),
-                                                c2, make_float2(m.z, m.w));
-                            }
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) x[k] = make_float2(ex2(x[k].x), ex2(x[k].y));
-                            if (!full) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    if (c0 + c + 2 * k < lo) x[k].x = 0.f;
-                                    if (c0 + c + 2 * k + 1 < lo) x[k].y = 0.f;
-                                }
-                            }
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) acc[k & 3] = add2(acc[k & 3], x[k]);
-                        }
+                    for (int a = 0; a < 2; ++a) {
+                        const float* from = rb == 0 || w.first_row(jt + a * kStTile) >= rb * w.per * kStTile ? p.scores : p.out;
+                        if (j + a * kStTile < tail) next_old[a] = from[row_at + j + a * kStTile];
                     }
                 }
+                const int slot = pc & (kStParts - 1);
+                ok = warp_wait(&bars[S_PART_EMPTY + slot], ((pc / kStParts) & 1) ^ 1, ab, kDevTimeoutEpilogue);
+                // this group's share of the pair, a tile at a time
+#pragma unroll 1
+                for (int a = 0; a < 2 && ok; ++a) {
+                    float2 acc[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
+                    const bool there = i + a < w.ktiles && (a == 0 || w.has(rb, i + a));
+                    const int q0 = there ? w.first_tile(rb, i + a) : 0, q1 = there ? w.end_tile(rb) : 0;
+                    const int seen = w.first_row(j + a * kStTile);  // the first row that sees the token
+                    for (int t = q0; t < q1; ++t) {
+                        const bool ours = turn == 0;
+                        turn = turn == 0 ? kStGroups - 1 : turn - 1;
+                        if (!ours) continue;
+                        ok = warp_wait(&bars[S_S_FULL + g], n++ & 1, ab, kDevTimeoutSoftmax);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const float* mt = minus + (t - rb * w.per) * kStTile;
+                        const int lo = seen - t * kStTile;  // columns from this on count
+                        const bool full = !CAUSAL || __all_sync(0xffffffffu, lo <= 0);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kStTile; c0 += 64) {
+                            uint32_t v[64];
+                            tmem_ld64(at + c0, v);
+                            if (c0 != 0) {
+                                // the scores are in registers: their place is free
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&bars[S_S_FREE + g]);
+                            }
+#pragma unroll
+                            for (int c = 0; c < 64; c += 16) {
+                                float2 x[8];
+#pragma unroll
+                                for (int k = 0; k < 8; k += 2) {
+                                    const float4 m = *reinterpret_cast<const float4*>(mt + c0 + c + 2 * k);
+                                    x[k] = fma2(make_float2(__uint_as_float(v[c + 2 * k]), __uint_as_float(v[c + 2 * k + 1])), c2,
+                                                make_float2(m.x, m.y));
+                                    x[k + 1] = fma2(make_float2(__uint_as_float(v[c + 2 * k + 2]), __uint_as_float(v[c + 2 * k + 3])),
+                                                    c2, make_float2(m.z, m.w));
+                                }
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) x[k] = make_float2(ex2(x[k].x), ex2(x[k].y));
+                                if (!full) {
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) {
+                                        if (c0 + c + 2 * k < lo) x[k].x = 0.f;
+                                        if (c0 + c + 2 * k + 1 < lo) x[k].y = 0.f;
+                                    }
+                                }
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) acc[k & 3] = add2(acc[k & 3], x[k]);
+                            }
+                        }
+                    }
+                    const float2 x = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+                    part[(slot * kStGroups + g) * kStPair + a * kStTile] = x.x + x.y;
+                }
                 if (!ok) break;
-                // this group's share of the K tile
-                const int slot = kc & (kStParts - 1);
-                ok = warp_wait(&bars[S_PART_EMPTY + slot], ((kc / kStParts) & 1) ^ 1, ab, kDevTimeoutEpilogue);
-                if (!ok) break;
-                const float2 x = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
-                part[(slot * kStGroups + g) * kStTile] = x.x + x.y;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[S_PART_FULL + slot]);
-                // the K tile before, which every group has left by now or soon will have
-                if (due) join(kc - 1);
+                // the pair before, which every group has left by now or soon will have
+                if (due) join(pc - 1);
                 if (mine == 0) {
                     due = true;
                     last = j;
-                    old = next_old;
+                    old[0] = next_old[0];
+                    old[1] = next_old[1];
                 }
                 mine = mine == 0 ? kStGroups - 1 : mine - 1;
-                ++kc;
+                ++pc;
             }
-            if (due && ok) join(kc - 1);
+            if (due && ok) join(pc - 1);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_Q_EMPTY]);
         }
