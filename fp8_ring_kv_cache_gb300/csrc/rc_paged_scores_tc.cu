@@ -15,9 +15,9 @@
 //                  shared memory, and the groups take turns in adding the three
 //                  up, always in the same order: no two threads add to one entry.
 //                  They also bring the query rows (by cp.async).
-//   warps 16 .. 23 read K's codes from the pages (two tiles ahead, in registers),
-//                  make them bf16 (exactly: scales are powers of two) and put
-//                  them in TMEM, half of the dims a warpgroup
+//   warps 16 .. 23 read K's codes from the pages (a warpgroup's next tile is in its
+//                  registers), make them bf16 (exactly: scales are powers of two)
+//                  and put them in TMEM, a tile a warpgroup
 // With the queries kept, K is read and converted once per 768 rows, and the
 // queries once per block: keeping K instead would read them for every 128
 // tokens (430 MB of cache traffic for 757 x 5,788 tokens x 48 heads).
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[S_K_FULL + i], 8);
+            mbar_init(&bars[S_K_FULL + i], 4);
             mbar_init(&bars[S_K_EMPTY + i], 1);
         }
         for (int i = 0; i < kStGroups; ++i) {
@@ -359,16 +359,15 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         }
     } else {
         // ------------------------------------------------------------ K
-        // A thread has D / 2 of the dims of one token a tile.
+        // The warpgroups take the K tiles in turn; a thread has one token of a tile.
         regs_dec<56>();
-        const int ct = tid & 127, half = wg - 1 - kStGroups;
-        constexpr int NB = D / 32;  // 16-byte pieces of the codes, read in pairs
+        const int ct = tid & 127, buf = wg - 1 - kStGroups;
+        constexpr int NB = D / 16;  // 16-byte pieces of the codes, read in pairs
         const int shift = p.g.page_shift, place = (1 << shift) - 1;
-        const uint8_t* kbase = p.g.kcodes + half * (D / 2);
         const bool wide = (reinterpret_cast<uintptr_t>(p.g.kcodes) & 31u) == 0;  // 32-byte loads are aligned
         const uint32_t* table =
             reinterpret_cast<const uint32_t*>(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages);
-        const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kStTmemK + half * (D / 4);
+        const uint32_t to = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kStTmemK + (D / 2) * buf;
         // the next K tile with work after (rb, i); i = -1 starts; rb = blocks ends
         struct Step {
             int rb, i;
@@ -386,59 +385,63 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             const int t = j0 + x.i * kStTile + ct;
             return x.rb < w.blocks && t < q.kv ? static_cast<int>(ldg_early(table + (t >> shift))) : 0;
         };
-        uint4 kr[2][NB];
-        uint32_t ks[2];
-        // (tokens behind the end, or on a bad page, read the first token of page 0: their sums are not used)
-        auto fetch = [&](uint4 (&k)[NB], uint32_t& scale, const Step& x, int page) {
+        uint4 k[NB];
+        uint32_t scale;
+        // pieces c, c + 1 of the row (tokens behind the end, or on a bad page, read the first token of page 0: their sums are not used)
+        auto row_of = [&](const Step& x, int page) {
             const int t = j0 + x.i * kStTile + ct;
             const bool have = x.rb < w.blocks && t < q.kv && check_page(p.g, page);
-            const uint64_t row = have ? (static_cast<uint64_t>(static_cast<uint32_t>(page) * p.g.kv_heads + h) << shift) + (t & place) : 0u;
-            const uint8_t* src = kbase + row * D;
-#pragma unroll
-            for (int c = 0; c < NB; c += 2) {
-                if (wide) {
-                    ldg_nc_32(src + 16 * c, k[c], k[c + 1]);
-                } else {
-                    k[c] = __ldg(reinterpret_cast<const uint4*>(src + 16 * c));
-                    k[c + 1] = __ldg(reinterpret_cast<const uint4*>(src + 16 * c + 16));
-                }
-            }
-            scale = ldg_early(p.g.kscale + row);
+            return have ? (static_cast<uint64_t>(static_cast<uint32_t>(page) * p.g.kv_heads + h) << shift) + (t & place) : 0u;
         };
-        Step now{0, -1};
-        advance(now);
-        Step next = now;
-        fetch(kr[0], ks[0], next, entry(next));
+        auto fetch = [&](int c, const uint8_t* src) {
+            if (wide) {
+                ldg_nc_32(src + 16 * c, k[c], k[c + 1]);
+            } else {
+                k[c] = __ldg(reinterpret_cast<const uint4*>(src + 16 * c));
+                k[c + 1] = __ldg(reinterpret_cast<const uint4*>(src + 16 * c + 16));
+            }
+        };
+        auto put = [&](int c, uint32_t f) {
+            const uint32_t v[8] = {bf2_mul(codes01(k[c].x), f), bf2_mul(codes23(k[c].x), f), bf2_mul(codes01(k[c].y), f),
+                                   bf2_mul(codes23(k[c].y), f), bf2_mul(codes01(k[c].z), f), bf2_mul(codes23(k[c].z), f),
+                                   bf2_mul(codes01(k[c].w), f), bf2_mul(codes23(k[c].w), f)};
+            tmem_st8(to + 8 * c, v);
+        };
+        Step now{0, -1}, next;
+        for (int i = 0; i <= buf; ++i) advance(now);
+        {
+            const uint64_t row = row_of(now, entry(now));
+#pragma unroll
+            for (int c = 0; c < NB; c += 2) fetch(c, p.g.kcodes + row * D);
+            scale = ldg_early(p.g.kscale + row);
+        }
+        next = now;
         advance(next);
-        fetch(kr[1], ks[1], next, entry(next));
         advance(next);
         int ahead = entry(next);
         bool ok = true;
-        for (int kc = 0; ok && now.rb < w.blocks; kc += 2) {
+        for (int n = 0; ok && now.rb < w.blocks; ++n) {
+            const uint64_t row = row_of(next, ahead);
+            const Step after = next;
+            advance(next);
+            advance(next);
+            ahead = entry(next);
+            ok = warp_wait(&bars[S_K_EMPTY + buf], (n & 1) ^ 1, ab, kDevTimeoutConvert);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t f = scale_factor(scale);
+            scale = ldg_early(p.g.kscale + row);
 #pragma unroll
-            for (int buf = 0; buf < 2; ++buf) {
-                if (!ok || now.rb >= w.blocks) break;
-                ok = warp_wait(&bars[S_K_EMPTY + buf], ((kc >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t f = scale_factor(ks[buf]);
-#pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                    const uint4 k = kr[buf][c];
-                    const uint32_t v[8] = {bf2_mul(codes01(k.x), f), bf2_mul(codes23(k.x), f), bf2_mul(codes01(k.y), f),
-                                           bf2_mul(codes23(k.y), f), bf2_mul(codes01(k.z), f), bf2_mul(codes23(k.z), f),
-                                           bf2_mul(codes01(k.w), f), bf2_mul(codes23(k.w), f)};
-                    tmem_st8(to + (D / 2) * buf + 8 * c, v);
-                }
-                fetch(kr[buf], ks[buf], next, ahead);  // two tiles on, into the registers just freed
-                advance(next);
-                ahead = entry(next);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[S_K_FULL + buf]);
-                advance(now);
+            for (int c = 0; c < NB; c += 2) {
+                put(c, f);
+                put(c + 1, f);
+                fetch(c, p.g.kcodes + row * D);  // the warpgroup's next tile, into the registers just freed
             }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[S_K_FULL + buf]);
+            now = after;
         }
     }
 
