@@ -199,6 +199,21 @@ __global__ void __launch_bounds__(kGatherThreads, 6) paged_gather_kernel(PagedEv
         }
     }
     __syncthreads();
+    // K rows and scales are on their way while the pieces of V are listed
+    constexpr int kPieces = D / 16, kCopies = kGatherTokens * kPieces / kGatherThreads;
+    uint4 krow[kCopies];
+#pragma unroll
+    for (int x = 0; x < kCopies; ++x) {
+        const int i = tid + x * kGatherThreads, t = i / kPieces, c = i % kPieces;
+        krow[x] = src[t] >= 0 ? ldg_nc_na_v4(p.g.kcodes + src[t] * D + 16 * c) : make_uint4(0, 0, 0, 0);
+    }
+    const int st = tid - 64;  // the token whose scales this thread copies
+    const bool scales = st >= 0 && st < kGatherTokens && src[st] >= 0 && dst[st >> 4] >= 0;
+    uint8_t kscale = 0, vscale = 0;
+    if (scales) {
+        kscale = __ldg(p.g.kscale + src[st]);
+        vscale = __ldg(p.g.vscale + src[st]);
+    }
     // the 16-byte pieces of V rows that hold the tokens (which ascend: equal
     // pieces are neighbours; a token on a bad page has none)
     if (warp == 0) {
@@ -215,28 +230,12 @@ __global__ void __launch_bounds__(kGatherThreads, 6) paged_gather_kernel(PagedEv
         }
         if (lane == 0) s_pieces = count;
     }
-    // scales and K rows meanwhile
-    if (tid >= 64 && tid < 64 + kGatherTokens) {
-        const int t = tid - 64;
-        if (src[t] >= 0 && dst[t >> 4] >= 0) {
-            p.g.kscale[dst[t >> 4] + (t & 15)] = p.g.kscale[src[t]];
-            p.g.vscale[dst[t >> 4] + (t & 15)] = p.g.vscale[src[t]];
-        }
-    }
-    constexpr int kPieces = D / 16;
-#pragma unroll
-    for (int i = tid; i < kGatherTokens * kPieces; i += kGatherThreads) {
-        const int t = i / kPieces, c = i % kPieces;
-        if (src[t] >= 0 && dst[t >> 4] >= 0)
-            *reinterpret_cast<uint4*>(p.g.kcodes + (dst[t >> 4] + (t & 15)) * D + 16 * c) =
-                ldg_nc_na_v4(p.g.kcodes + src[t] * D + 16 * c);
-    }
     __syncthreads();
     // V: element (d, place) of (page, head) b is byte (b D + d) P + place.
     // Thread: tokens 4 w .. 4 w + 3 of the dims tid / 16 + 16 k.
     const int pieces = s_pieces, w = tid & 15;
     const int64_t to = dst[w >> 2];
-    for (int first = 0; first < pieces; first += kGatherPieces) {
+    for (int first = 0; first < pieces || first == 0; first += kGatherPieces) {
         const int here = min(kGatherPieces, pieces - first);
         // four pieces of a row by neighbouring lanes: they often lie side by side
         for (int k = tid & 3; k < here; k += 4) {
@@ -244,9 +243,21 @@ __global__ void __launch_bounds__(kGatherThreads, 6) paged_gather_kernel(PagedEv
             const uint8_t* from = p.g.vcodes + (b >> shift) * D * P + (b & (P - 1));
 #pragma unroll
             for (int d = tid >> 2; d < D; d += kGatherThreads / 4)
-                *reinterpret_cast<uint4*>(in + d * kRow + 16 * k) =
-                    __ldg(reinterpret_cast<const uint4*>(from + (static_cast<uint32_t>(d) << shift)));
+                cp_async16(in + d * kRow + 16 * k, from + (static_cast<uint32_t>(d) << shift));
         }
+        if (first == 0) {
+#pragma unroll
+            for (int x = 0; x < kCopies; ++x) {
+                const int i = tid + x * kGatherThreads, t = i / kPieces, c = i % kPieces;
+                if (src[t] >= 0 && dst[t >> 4] >= 0)
+                    *reinterpret_cast<uint4*>(p.g.kcodes + (dst[t >> 4] + (t & 15)) * D + 16 * c) = krow[x];
+            }
+            if (scales) {
+                p.g.kscale[dst[st >> 4] + (st & 15)] = kscale;
+                p.g.vscale[dst[st >> 4] + (st & 15)] = vscale;
+            }
+        }
+        cp_async_wait_all();
         __syncthreads();
         if (to >= 0) {
             int at[4];

@@ -276,12 +276,17 @@ cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_paged_scores(const PagedScoreParams& p, int D, cudaStream_t s) {
-    // Up to two row tiles of 16 the warps' own products keep up with the reading
-    // of the codes; with more rows the tcgen05 kernel is the faster one, whose
-    // time is the same up to 128 rows (32 sequences x 8,000 tokens x 8 KV heads x
-    // 128: 32 rows 162 against 192 us, 64 rows 237 against 192; one sequence of
-    // 60,000 tokens: 42 against 46, 60 against 46).
-    if (static_cast<int64_t>(p.g.max_new) * p.group > kScoreRowsMax) return launch_paged_scores_tc(p, D, s);
+    // Up to two row tiles of 16, while there is not much to read, the kernels here
+    // are done before the tcgen05 kernel has set itself up (8 KV heads x 128, 32
+    // rows: one sequence of 300 tokens 5.2 against 7.8 us, 8,000 tokens 9.8
+    // against 10.5, 64 sequences of 300 19 against 34); then its conversion of K
+    // keeps up better (one sequence of 60,000 tokens 42 against 33, 32 sequences
+    // of 8,000 163 against 146; 16 of 1,000 the same).  With more rows each tile
+    // costs another pass here (one sequence of 8,000, 64 rows: 13.2 against 11.4).
+    const int64_t lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
+    const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
+    const bool much = p.g.max_kv > 4096 && lists * p.g.max_kv > (1 << 17);
+    if (rows > 16 && (rows > kScoreRowsMax || much)) return launch_paged_scores_tc(p, D, s);
     return D == 128 ? launch_d<128>(p, s) : launch_d<64>(p, s);
 }
 
