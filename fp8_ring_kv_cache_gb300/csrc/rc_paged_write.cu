@@ -10,6 +10,12 @@
 // through shared memory to be transposed.  Tokens of the run that are older
 // than the call keep their bytes: a run that is not all new stores the new
 // tokens byte by byte.
+// The codes of K are those of the exact turn: where the fp32 sum is too close to
+// the middle between two codes it is taken again with twice the bits.  757
+// tokens x 48 heads x 128: 15.9 us (28 MB, 4.1 us at the copy rate; with codes of
+// the fp32 sums, some five of which in 4.6 million then are the neighbour's,
+// 13.0 us).  What it spends its time on is the issue of the conversions and the
+// load of K, V and the positions at the start of each block.
 #include "rc_paged.cuh"
 
 namespace rc {
@@ -18,27 +24,73 @@ namespace {
 
 constexpr int kRun = 16;  // tokens of a block: the alignment of a V row's piece
 
-// The lane's 8 values quantised with the row's scale; returns the scale byte.
+// Exponent of the row's scale and its byte, from the largest magnitude as bits:
+// infinities and NaNs are above every number.
 template <int LANES>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint2& codes) {
-    // the largest magnitude as bits: infinities and NaNs are above every number
+__device__ __forceinline__ uint32_t scale_byte(const float (&x)[8], float& inv, bool& bad) {
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool bad = top >= 0x7f800000u;
-    const float amax = __uint_as_float(top);
-    const int e = scale_exponent(amax);
-    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, e in -124 .. 7: exact
-    codes = make_uint2(e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16),
-                       e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16));
-    if (bad) codes = make_uint2(0u, 0u);
+    bad = top >= 0x7f800000u;
+    const int e = scale_exponent(__uint_as_float(top));
+    inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, e in -124 .. 7: exact
     return bad ? 255u : static_cast<uint32_t>(e + 127);
 }
 
+// (cos, sin) of position * frequency as sums of two fp32 numbers each, to 2^-25.6
+// at the worst (four roundings of sin's x^3 terms, under 0.081): the angle, exact
+// in integers, is brought within an eighth of a turn and taken as two fp32
+// numbers, and the Taylor series to x^11 and x^10 there are kept apart from their
+// leading terms.
+struct TurnPair {
+    float2 hi, lo;  // (cos, sin)
+};
+__device__ __forceinline__ TurnPair turn_cos_sin_pair(int pos, uint64_t turns) {
+    const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns;
+    const uint32_t quad = static_cast<uint32_t>((frac + (1ull << 61)) >> 62);
+    const int64_t rest = static_cast<int64_t>(frac - (static_cast<uint64_t>(quad) << 62));  // / 2^64 turns
+    const float top = static_cast<float>(static_cast<int32_t>(rest >> 38)) * 0x1p-23f;      // eighths of a turn: exact
+    const float low = static_cast<float>(static_cast<uint32_t>(rest >> 8) & 0x3fffffffu);
+    constexpr float kH = 0.785398185253143310546875f, kL = -2.18556938e-8f;  // pi / 4
+    const float x0 = __fmul_rn(top, kH);
+    const float x1 = __fadd_rn(__fmaf_rn(top, kH, -x0), __fmaf_rn(top, kL, low * 8.71967125e-17f));  // 2 pi / 2^56
+    const float x = __fadd_rn(x0, x1), xl = __fadd_rn(x1, -__fadd_rn(x, -x0));
+    const float z = __fmul_rn(x, x), zl = __fmaf_rn(x, x, -z);
+    const float S = fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.50521084e-8f, 2.75573192e-6f), -1.98412698e-4f), 8.33333333e-3f),
+                         -1.66666667e-1f);
+    const float sl = fmaf(x * z, S, fmaf(-0.5f * z, xl, xl));
+    const float C = fmaf(z, fmaf(z, fmaf(z, -2.75573192e-7f, 2.48015873e-5f), -1.38888889e-3f), 4.16666667e-2f);
+    const float c0 = __fadd_rn(1.f, -0.5f * z);
+    const float cl = __fadd_rn(__fadd_rn(-0.5f * z, -__fadd_rn(c0, -1.f)), fmaf(z * z, C, -fmaf(x, xl, 0.5f * zl)));
+    float2 s, c;  // (hi, lo)
+    s.x = __fadd_rn(x, sl);
+    s.y = __fadd_rn(sl, -__fadd_rn(s.x, -x));
+    c.x = __fadd_rn(c0, cl);
+    c.y = __fadd_rn(cl, -__fadd_rn(c.x, -c0));
+    const float2 cc = (quad & 1u) ? s : c, ss = (quad & 1u) ? c : s;
+    const float cf = (quad == 1u || quad == 2u) ? -1.f : 1.f, sf = (quad & 2u) ? -1.f : 1.f;
+    TurnPair r;
+    r.hi = make_float2(cf * cc.x, sf * ss.x);
+    r.lo = make_float2(cf * cc.y, sf * ss.y);
+    return r;
+}
+
+// a c + b s with c and s as sums of two numbers (a, b of 8 bits), rounded to odd:
+// a later rounding to fewer bits takes it for the exact sum.
+__device__ __forceinline__ float sum_exactly(float a, float c, float cl, float b, float s, float sl) {
+    const float p = __fmul_rn(a, c), q = __fmul_rn(b, s), d = __fadd_rn(p, q), bb = __fadd_rn(d, -p);
+    const float rest = __fadd_rn(__fadd_rn(p, -__fadd_rn(d, -bb)), __fadd_rn(q, -bb));
+    const float low = __fadd_rn(__fadd_rn(rest, __fmaf_rn(a, c, -p)), __fadd_rn(__fmaf_rn(b, s, -q), fmaf(a, cl, b * sl)));
+    const float y = __fadd_rn(d, low), off = __fadd_rn(low, -__fadd_rn(y, -d));
+    const uint32_t u = __float_as_uint(y);
+    if (off == 0.f || (u & 1u) || (u & 0x7fffffffu) == 0u) return y;
+    return __uint_as_float(((off > 0.f) == (y > 0.f)) ? u | 1u : u - 1u);  // between y and its neighbour: the odd one
+}
+
 template <int D>
-__global__ void __launch_bounds__(kRun* D / 8) paged_write_kernel(const __grid_constant__ PagedWriteParams p, int runs, int heads_per_block) {
+__global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged_write_kernel(const __grid_constant__ PagedWriteParams p, int runs, int heads_per_block) {
     constexpr int LANES = D / 8;  // of one token
     constexpr int kThreads = kRun * LANES;
     constexpr int kRow = D + 16;  // a token's staged codes: 16-byte aligned, rows spread over the banks
@@ -62,12 +114,12 @@ __global__ void __launch_bounds__(kRun* D / 8) paged_write_kernel(const __grid_c
     const bool whole = base >= first && base + kRun <= q.kv;
     const int row = q.q0 + (live ? index - first : 0);
 
-    float2 cs[4];
+    TurnPair cs[4];
     const uint64_t* turns = param_address(p.rope.turns) + 4 * c;
     const uint32_t axes = *reinterpret_cast<const uint32_t*>(param_address(p.rope.axis) + 4 * c);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        cs[i] = turn_cos_sin(__ldg(p.pos + ((axes >> (8 * i)) & 0xffu) * p.pos_stride + row), turns[i]);
+        cs[i] = turn_cos_sin_pair(__ldg(p.pos + ((axes >> (8 * i)) & 0xffu) * p.pos_stride + row), turns[i]);
     const __nv_bfloat16* kr = p.K + row * p.k_stride + c * 8;
     const __nv_bfloat16* vr = p.V + row * p.v_stride + c * 8;
     const int h0 = blockIdx.y * heads_per_block, h1 = min(p.g.kv_heads, h0 + heads_per_block);
@@ -77,12 +129,13 @@ __global__ void __launch_bounds__(kRun* D / 8) paged_write_kernel(const __grid_c
         vw = ldg_nc_na_v4(vr + static_cast<size_t>(h0) * D);
     }
     for (int h = h0; h < h1; ++h) {
-        float k[8], v[8];
+        float k[8], v[8], reach[4];
         const uint32_t ki[4] = {kw.x, kw.y, kw.z, kw.w}, vi[4] = {vw.x, vw.y, vw.z, vw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            rotate_pair(__uint_as_float(ki[i] << 16), __uint_as_float(ki[i] & 0xFFFF0000u), cs[i].x, cs[i].y, k[2 * i],
+            rotate_pair(__uint_as_float(ki[i] << 16), __uint_as_float(ki[i] & 0xFFFF0000u), cs[i].hi.x, cs[i].hi.y, k[2 * i],
                         k[2 * i + 1]);
+            reach[i] = fabsf(__uint_as_float(ki[i] << 16)) + fabsf(__uint_as_float(ki[i] & 0xFFFF0000u));
             v[2 * i] = __uint_as_float(vi[i] << 16);
             v[2 * i + 1] = __uint_as_float(vi[i] & 0xFFFF0000u);
         }
@@ -90,13 +143,41 @@ __global__ void __launch_bounds__(kRun* D / 8) paged_write_kernel(const __grid_c
             kw = ldg_nc_na_v4(kr + static_cast<size_t>(h + 1) * D);
             vw = ldg_nc_na_v4(vr + static_cast<size_t>(h + 1) * D);
         }
-        uint2 kc, vc;
-        const uint32_t kb = quantise<LANES>(k, kc), vb = quantise<LANES>(v, vc);
+        uint32_t kc[4], vc[4];  // pairs of codes
+        float inv;
+        bool bad;
+        const uint32_t kb = scale_byte<LANES>(k, inv, bad);
+        // The fp32 sum is within 2^-22 (|a| + |b|) of the exact one (cos and sin half
+        // an ulp each, 2^-25, and three roundings of 2^-24: 2.1e-7).  Where both ends
+        // of that range have one code it is the exact sum's; the few others (one
+        // pair of 50,000) are summed again.  (A pair of zeros keeps its sign.)
+        uint32_t unsure = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float tol = reach[i] * (inv * 0x1p-22f);
+            kc[i] = e4m3x2(fmaf(k[2 * i], inv, -tol), fmaf(k[2 * i + 1], inv, -tol));
+            if (kc[i] != e4m3x2(fmaf(k[2 * i], inv, tol), fmaf(k[2 * i + 1], inv, tol)) && tol > 0.f) unsure |= 1u << i;
+        }
+        if (bad) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kc[i] = 0u;
+        } else if (unsure) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!(unsure & (1u << i))) continue;
+                const float a = __uint_as_float(ki[i] << 16), b = __uint_as_float(ki[i] & 0xFFFF0000u);
+                const float2 ch = cs[i].hi, cl = cs[i].lo;
+                kc[i] = e4m3x2(sum_exactly(a, ch.x, cl.x, -b, ch.y, cl.y) * inv, sum_exactly(a, ch.y, cl.y, b, ch.x, cl.x) * inv);
+            }
+        }
+        const uint32_t vb = scale_byte<LANES>(v, inv, bad);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vc[i] = bad ? 0u : e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
         const size_t ph = static_cast<size_t>(page) * p.g.kv_heads + h;
         uint8_t* st = stage[(h - h0) & 1];
         if (live) {
-            *reinterpret_cast<uint2*>(p.g.kcodes + (ph * P + off + tok) * D + c * 8) = kc;
-            *reinterpret_cast<uint2*>(st + tok * kRow + c * 8) = vc;
+            *reinterpret_cast<uint2*>(p.g.kcodes + (ph * P + off + tok) * D + c * 8) = make_uint2(kc[0] | (kc[1] << 16), kc[2] | (kc[3] << 16));
+            *reinterpret_cast<uint2*>(st + tok * kRow + c * 8) = make_uint2(vc[0] | (vc[1] << 16), vc[2] | (vc[3] << 16));
             if (c == 0) {
                 p.g.kscale[ph * P + off + tok] = static_cast<uint8_t>(kb);
                 p.g.vscale[ph * P + off + tok] = static_cast<uint8_t>(vb);
@@ -127,12 +208,11 @@ cudaError_t launch_d(const PagedWriteParams& p, cudaStream_t s) {
     const int runs = (p.g.max_new + kRun - 2) / kRun + 1;
     const int64_t blocks = static_cast<int64_t>(p.g.seqs) * runs;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    // Heads of a block: one while that does not fill the card three times, then
-    // up to four, which share the angles and overlap a head's loads with the one
-    // before (757 tokens x 48 heads x 128: one head 15.6 us, two 13.6, four 13.1,
-    // eight 16.6; 64 single tokens x 8 heads: 4.9, 4.6, 4.8, 6.9).
-    int hpb = 1;
-    while (hpb < 4 && blocks * ((p.g.kv_heads + 2 * hpb - 1) / (2 * hpb)) >= 152 * 3) hpb *= 2;
+    // Heads of a block: two, which share the angles and overlap one's loads with
+    // the other's work, four when those still fill the card three times (757
+    // tokens x 48 heads x 128: one head 19.3 us, two 16.6, four 15.9, eight 19.7;
+    // 64 single tokens x 8 heads: 5.8, 5.2, 5.4, 8.0).
+    const int hpb = blocks * ((p.g.kv_heads + 3) / 4) >= 152 * 3 ? 4 : 2;
     dim3 grid(static_cast<unsigned>(blocks), (p.g.kv_heads + hpb - 1) / hpb);
     paged_write_kernel<D><<<grid, kRun * D / 8, 0, s>>>(p, runs, hpb);
     return cudaGetLastError();

@@ -801,3 +801,27 @@ def test_pages_on_a_16_byte_boundary(rc, dim):
         cache.sync()
         res.append((out, lse, sc, cache.kcodes, cache.vcodes, cache.kscale, cache.vscale))
     assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+@pytest.mark.parametrize("dim,sections", [(128, (22, 21, 21)), (64, (32,))])
+def test_write_codes_are_those_of_the_exact_turn(rc, dim, sections):
+    """cos and sin are good to 2^-25.6, all else to far less: a code may be the neighbour's only where the exact value is
+    within 2^-25 (|a| + |b|) of the middle between the two (with fp32 sums that is 2^-22)."""
+    st = Setup(rc, [(900, 900)], 6, dim, 32, seed=97)
+    k = bf16(st.rng, 900, 6, dim)
+    pos = st.rng.integers(0, 200000, (len(sections), 900)).astype(np.int32)
+    st.cache.write(st.batch, k.cuda(), k.cuda(), dev(pos), rc.RopeAxes(sections))
+    st.cache.sync()
+    table = st.meta["table"][0]
+    at = np.arange(900)
+    got = st.cache.kcodes.cpu().numpy()[table[at // 32], :, at % 32].astype(int)
+    scale = st.cache.kscale.cpu().numpy()[table[at // 32], :, at % 32]
+    x = k.double().numpy()
+    y = pu.turn(x, pos, sections)
+    want, wscale = pu.quantise(y)
+    assert np.array_equal(scale, wscale)
+    off = np.nonzero(got != want)
+    factor = 2.0 ** (127.0 - wscale[off[:2]])
+    r = (np.abs(x[..., 0::2]) + np.abs(x[..., 1::2])).repeat(2, -1)[off] * factor
+    mid = (pu.E4M3[got[off]] + pu.E4M3[want[off].astype(int)]) / 2
+    assert (np.abs(y[off] * factor - mid) <= 2.0 ** -25 * r).all()
