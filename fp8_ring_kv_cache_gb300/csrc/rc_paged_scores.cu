@@ -25,9 +25,12 @@ constexpr int kScoreRowsMax = 32;  // of the kernels here
 
 constexpr int kFewChunk = 64;  // cached tokens of a warp's step
 
-// 8 NR rows; a block has `range` cached tokens (a multiple of 256).
+// 8 NR rows; a block has `range` cached tokens (a multiple of 256).  Blocks an SM
+// (8 KV heads x 128, 32 sequences of 8,000 tokens): 8 rows, as many as 78
+// registers allow 59.6 us, 7 45.0, 8 48.4; 16 rows 4 54.5 us, 5 55.8, 6 62.4 (and
+// with head_dim 64 33.8, 32.1, 36.3).
 template <int D, int NR>
-__global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_few_kernel(PagedScoreParams p, int range) {
+__global__ void __launch_bounds__(kScoreWarps * 32, NR == 1 ? 7 : D == 64 ? 5 : 4) paged_scores_few_kernel(PagedScoreParams p, int range) {
     constexpr int CH = D / 64;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int h = blockIdx.y, s = blockIdx.z;
@@ -251,8 +254,9 @@ template <int D>
 cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
     if (rows <= 16) {
-        // Up to 16 rows stay in registers (the sequences above: 8 rows 60 us, 123 us
-        // with the kernel for some tiles; 16 rows 64 and 127).  Ranges of the
+        // Up to 16 rows stay in registers (8 KV heads x 128, 32 sequences of 8,000
+        // tokens: 8 rows 45 us, 123 us with the kernel for some tiles; 16 rows 55
+        // and 127).  Ranges of the
         // cached tokens: twelve blocks an SM, a step of every warp at least (16
         // sequences of 509 to 8,191 tokens x 8 heads: 6 blocks an SM 21.6 us, 12
         // 19.5, 24 21.8, 48 20.6)
