@@ -17,6 +17,11 @@ Use (K, V, Q: CUDA bf16 tensors [n][heads][head_dim]; out: CUDA fp32, same shape
 ``RingKVCache(..., bf16_cache=True)`` keeps the same ring in bf16 (no scales):
 the non-FP8 side of the FP8-versus-bf16 cache comparison.
 
+Caches of many sequences in pages the caller owns, for any number of new tokens and
+grouped query heads (``PagedKVCache``: write, attend, accumulate, evict), and rotary
+positions on several axes with their gradient (``RopeAxes``, ``rc_rope_axes``): see
+``_paged.py``.
+
 Every call is stream-ordered on torch's current stream (or ``stream=``); no
 call after construction allocates device memory.
 """

@@ -15,6 +15,12 @@
 //    usually three or four) are brought to shared memory for every dim, the
 //    bytes are picked there, and rows of 64 go out.  (Single bytes from and to
 //    global memory, 32 tokens side by side, took 132 us for 64 lists of 8,192.)
+//    K rows, scales and V's pieces are on their way together.
+//
+// 8 sequences of 9,001 to 32,749 tokens x 8 heads x 128, 8,192 of each kept: 101 us,
+// 32 of them the selection (64 blocks, as many as there are lists; its passes over
+// the keys follow one another) and 70 the copies: 341 MB at 4.9 TB/s, as the pieces
+// of V are read with the tokens between those that stay.
 #include <algorithm>
 
 #include "rc_paged.cuh"

@@ -5,7 +5,11 @@
 // reading the K codes.  The rows stay in registers while the warps go over the
 // cached tokens 64 at a time, reading K pieces straight into the fp16 products'
 // operands as the attention does; the four lanes that hold a token's rows add up
-// by halves, so that each ends with the sums of two tokens.
+// by halves, so that each ends with the sums of two tokens.  16 sequences of 509
+// to 8,191 tokens x 8 KV heads x 6 query heads x 128: 18 us (76 MB, 11.3 us at the
+// rate of a copy); the start of each block, three loads after one another, is what
+// keeps it from there.
+//
 // paged_scores_rows_kernel, for some tiles of rows.
 // A warp owns 32 cached tokens of one (sequence, KV head), decodes their K rows
 // to bf16 once, into the registers where the matrix instructions want them, and

@@ -21,6 +21,14 @@
 // With the queries kept, K is read and converted once per 768 rows, and the
 // queries once per block: keeping K instead would read them for every 128
 // tokens (430 MB of cache traffic for 757 x 5,788 tokens x 48 heads).
+//
+// 757 queries x 5,788 tokens x 48 heads x 128: 57.4 us, 0.94 PFLOP/s, half of
+// what a library product of bf16 matrices reaches.  Of the 126,000 cycles of a
+// block 12,000 bring the queries; then a unit takes 1,000 where its product needs
+// 530 and its exponentials 510: bound by the chain of a group (wait for the
+// product, 64 columns to registers, exponentials, the other 64, the place handed
+// back), of which shared memory and TMEM have room for three.  With K in shared
+// memory, 384 rows at a time and four groups it took 71 us.
 #include <algorithm>
 
 #include "rc_paged.cuh"

@@ -2,7 +2,9 @@
 // dimension pair of a head turned by angle = position on the pair's axis x the
 // pair's frequency, forward or back.
 //
-// Bound by memory: every value is read and written once, 16 bytes a thread.
+// Bound by memory: every value is read and written once, 16 bytes a thread
+// (34,065 tokens x 16 heads x 128 in fp32: 82 us for 559 MB, the rate of a copy;
+// 757 tokens x 48 heads x 128 in bf16: 4.9 us, half of it the launch).
 // The angles depend on the token alone, so a block computes its tokens' (cos,
 // sin) once into shared memory and all heads read them there.
 #include "rc_paged.cuh"
