@@ -56,7 +56,7 @@ enum : int {
     T_COUNT = 12
 };
 // Named barriers: group i with the product warp (P in TMEM; the group's
-// checker lane has seen V of this unit and K of unit u + 2), and the two
+// watching lane has seen V of this unit and K of unit u + 2), and the two
 // groups at the end.
 constexpr int kNbUnit = 1;  // [2]
 constexpr int kNbJoin = 3;
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
         float m_run = -INFINITY, l_run = 0.f;
         bool poison = false;  // a token whose V is not a number is seen
         bool ok = true;
-        const bool checker = quad == 0 && lane == 0;
+        const bool watcher = quad == 0 && lane == 0;
 
         auto unit = [&](int u) -> bool {
             const int j = tile_of(u);
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             const int jk = tile_of(u + 2);
             const bool want_k = u + 2 < U;
             bool vk = true;
-            if (checker) {
+            if (watcher) {
                 vk = mbar_test(&bars[T_V_FULL + (j & 1)], (j >> 1) & 1);
                 if (want_k) vk = mbar_test(&bars[T_K_FULL + (jk & 1)], (jk >> 1) & 1) && vk;
             }
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             }
             l_run = l_run * alpha + ((ls0.x + ls0.y) + (ls1.x + ls1.y));
             m_run = m_new;
-            if (checker && !vk) {
+            if (watcher && !vk) {
                 if (!mbar_wait(&bars[T_V_FULL + (j & 1)], (j >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
                 if (want_k && !mbar_wait(&bars[T_K_FULL + (jk & 1)], (jk >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
             }

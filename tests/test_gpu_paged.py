@@ -825,3 +825,100 @@ def test_write_codes_are_those_of_the_exact_turn(rc, dim, sections):
     r = (np.abs(x[..., 0::2]) + np.abs(x[..., 1::2])).repeat(2, -1)[off] * factor
     mid = (pu.E4M3[got[off]] + pu.E4M3[want[off].astype(int)]) / 2
     assert (np.abs(y[off] * factor - mid) <= 2.0 ** -25 * r).all()
+
+
+def test_write_at_the_ends_of_the_positions(rc):
+    """Negative positions and those at the ends of int32: K's codes are those of rc_rope_axes' fp32 rows, but for roundings
+    (fp32 sums are within 2^-22 (|a| + |b|) and rounded to 2^-24 once more: two codes at most one step apart)."""
+    st = Setup(rc, [(64, 64)], 2, 128, 16, seed=98)
+    pos = st.rng.integers(-2 ** 31, 2 ** 31, (3, 64)).astype(np.int32)
+    pos[:, 0], pos[:, 1], pos[:, 2] = -2 ** 31, 2 ** 31 - 1, -1
+    k, rope = bf16(st.rng, 64, 2, 128), rc.RopeAxes((22, 21, 21))
+    st.cache.write(st.batch, k.cuda(), k.cuda(), dev(pos), rope)
+    st.cache.sync()
+    y = rc.rc_rope_axes(k.float().cuda(), dev(pos), rope).cpu().double().numpy()
+    table, at = st.meta["table"][0], np.arange(64)
+    got = pu.E4M3[st.cache.kcodes.cpu().numpy()[table[at // 16], :, at % 16]]
+    scale = pu.scale_value(st.cache.kscale.cpu().numpy()[table[at // 16], :, at % 16])[..., None]
+    # half a step of E4M3 (2^-4 relative, 2^-10 at least) and the fp32 rounding
+    assert (np.abs(got * scale - y) <= np.maximum(np.abs(y) * 2.0 ** -4, scale * 2.0 ** -10) * (1 + 2.0 ** -12) + 2.0 ** -21 * np.abs(
+        k.double().numpy()).max()).all()
+
+
+def test_calls_from_two_threads(rc):
+    """Each thread its own stream and workspace, on one pool's pages."""
+    import threading
+    st = Setup(rc, [(1, 3000), (70, 500)], 2, 64, 16, seed=99)
+    q = bf16(st.rng, st.tokens, 4, 64).cuda()
+    want, wlse = st.attend(q, True)
+    sc = torch.zeros((2, 2, st.max_kv), device="cuda")
+    st.cache.accumulate(st.batch, q, wlse, sc)
+    torch.cuda.synchronize()
+    n, bad = st.meta["q_start"][-1], []
+
+    def work():
+        try:
+            cache = rc.PagedKVCache(st.cache.kcodes, st.cache.vcodes, st.cache.kscale, st.cache.vscale)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(30):
+                    out, lse, s2 = torch.zeros_like(want), torch.zeros_like(wlse), torch.zeros_like(sc)
+                    cache.attend(st.batch, q, out, lse=lse)
+                    cache.accumulate(st.batch, q, wlse, s2)
+                    cache.sync()
+                    if not (torch.equal(out[:n], want[:n]) and torch.equal(lse[:n], wlse[:n]) and torch.equal(s2, sc)):
+                        bad.append("results differ")
+        except Exception as e:  # noqa: BLE001 (reported below)
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad[:3]
+
+
+FIRST_IN_A_GRAPH = """
+import torch, fp8_ring_kv_cache_gb300 as rc
+c = rc.PagedKVCache.empty(20, 2, 64, 16)
+q = torch.randn(70, 4, 64, device="cuda").to(torch.bfloat16)
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+pos, rope = torch.arange(70, dtype=torch.int32, device="cuda")[None], rc.RopeAxes((32,))
+one = rc.PagedBatch(i32(*range(10))[None], i32(1), i32(0, 1), tokens=1, max_new=1, max_kv=160)
+c.write(one, q[:1, :2], q[:1, 2:], pos[:, :1], rope)     # one token: other kernels than below
+out, lse, sc = torch.zeros_like(q), torch.zeros(70, 4, device="cuda"), torch.zeros(1, 2, 160, device="cuda")
+c.attend(one, q[:1], out[:1], lse=lse[:1])
+c.sync()
+many = rc.PagedBatch(i32(*range(10))[None], i32(70), i32(0, 70), tokens=70, max_new=70, max_kv=160)
+kept, n, dst = torch.zeros(1, 2, 40, dtype=torch.int32, device="cuda"), i32(0), i32(10, 11, 12)[None]
+def run():
+    sc.zero_()
+    c.write(many, q[:, :2], q[:, 2:], pos, rope)
+    c.attend(many, q, out, lse=lse)
+    c.accumulate(many, q, lse, sc)
+    c.evict(many, sc, keep=40, recent=4, dst_table=dst, kept=kept, kv_len_out=n)
+s = torch.cuda.Stream()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.stream(s):
+    with torch.cuda.graph(g, stream=s):
+        run()
+g.replay()
+c.sync()
+torch.cuda.synchronize()
+a = [x.clone() for x in (out, lse, sc, kept, n, c.kcodes, c.vcodes)]
+run()
+c.sync()
+assert all(torch.equal(x, y) for x, y in zip(a, (out, lse, sc, kept, n, c.kcodes, c.vcodes)))
+print("ok")
+"""
+
+
+def test_kernels_first_used_inside_a_graph(rc):
+    """A process whose first call of many rows, and of accumulate and evict, is a captured one."""
+    import pathlib
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH], cwd=pathlib.Path(__file__).parents[1], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr[-2000:]
