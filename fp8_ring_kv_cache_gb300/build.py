@@ -25,7 +25,7 @@ VARIANTS = [(LIB, OBJ, []), (LIB_BOUNDS, os.path.join(OBJ, "bounds"), ["-DRC_BOU
 SOURCES = ["rc_host.cu", "rc_write.cu", "rc_rotate.cu", "rc_attention.cu", "rc_noalloc.cu", "rc_window.cu",
            "rc_bf16.cu", "rc_fused.cu", "rc_rope.cu", "rc_paged_host.cu", "rc_paged_write.cu", "rc_paged_attn.cu", "rc_paged_tc.cu",
            "rc_paged_scores.cu", "rc_paged_scores_tc.cu", "rc_paged_evict.cu"]
-HEADERS = ["rc_device.cuh", "rc_internal.h", "rc_layout.h", "rc_nvtx.h", "rc_paged.cuh"]
+HEADERS = ["rc_device.cuh", "rc_internal.h", "rc_layout.h", "rc_nvtx.h", "rc_paged.cuh", "rc_paged_bounds.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

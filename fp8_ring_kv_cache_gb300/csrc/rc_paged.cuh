@@ -6,6 +6,7 @@
 #include "rc.h"
 #include "rc_device.cuh"
 #include "rc_internal.h"
+#include "rc_paged_bounds.h"
 
 namespace rc {
 
@@ -54,8 +55,9 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int s) {
     q.kv = __ldg(p.kv_len + s);
     q.q0 = __ldg(p.q_start + s);
     const int end = __ldg(p.q_start + s + 1);
-    q.n = end - q.q0;
-    if (q.kv < 0 || q.kv > p.max_kv || q.q0 < 0 || end < q.q0 || end > p.tokens || q.n > p.max_new) {
+    if (paged_seq_ok(q.kv, q.q0, end, p.tokens, p.max_new, p.max_kv)) {
+        q.n = end - q.q0;
+    } else {
         flag_meta(p.status);
         q.q0 = q.n = q.kv = 0;
     }
@@ -77,7 +79,7 @@ __device__ __forceinline__ uint32_t ldg_early(const uint8_t* p) {
 
 // Whether a page table entry is a page of the pool; flagged if not.
 __device__ __forceinline__ bool check_page(const PagedParams& p, int page) {
-    if (page >= 0 && page < p.pages) return true;
+    if (paged_page_ok(page, p.pages)) return true;
     flag_meta(p.status);
     return false;
 }

@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 
 __device__ __forceinline__ int evict_len(const PagedParams& g, int s) {
     int kv = __ldg(g.kv_len + s);
-    if (kv < 0 || kv > g.max_kv) {
+    if (!paged_len_ok(kv, g.max_kv)) {
         flag_meta(g.status);
         kv = 0;
     }
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kGatherThreads, 6) paged_gather_kernel(PagedEv
             const int i = i0 + tid;
             if (tid < n) {
                 const int to = __ldg(p.dst_table + static_cast<int64_t>(s) * p.dst_pages + (i >> shift));
-                if (to >= 0 && to < p.g.pages)
+                if (paged_page_ok(to, p.g.pages))
                     b = (static_cast<int64_t>(to) * p.g.kv_heads + h) * P + (i & (P - 1));
                 else
                     flag_meta(p.g.status);

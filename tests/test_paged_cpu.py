@@ -207,3 +207,35 @@ def test_plan_turns_are_the_rounded_frequencies(rc, base, sections, shared):
             assert abs(plan.turns[i] - Fraction(theta) * 2 ** 64 / two_pi) <= Fraction(1, 2) + Fraction(1, 2 ** 12)
             assert plan.axis[i] == axis
             i += 1
+
+
+BOUNDS = """
+#include "rc_paged_bounds.h"
+extern "C" int seq_ok(int kv, int q0, int end, int tokens, int max_new, int max_kv) {
+    return paged_seq_ok(kv, q0, end, tokens, max_new, max_kv);
+}
+extern "C" int len_ok(int kv, int max_kv) { return paged_len_ok(kv, max_kv); }
+extern "C" int page_ok(int page, int pages) { return paged_page_ok(page, pages); }
+"""
+
+
+def test_device_side_bounds(tmp_path):
+    """The checks that the kernels make of lengths, rows and pages: every mix of ordinary and extreme values against the
+    same conditions on Python's integers; signed overflow would trap."""
+    import itertools
+    import pathlib
+    import subprocess
+    src, so = tmp_path / "b.cpp", tmp_path / "b.so"
+    src.write_text(BOUNDS)
+    csrc = pathlib.Path(__file__).parents[1] / "fp8_ring_kv_cache_gb300" / "csrc"
+    subprocess.run(["g++", "-O1", "-shared", "-fPIC", "-fsanitize=undefined", "-fsanitize-undefined-trap-on-error", f"-I{csrc}",
+                    str(src), "-o", str(so)], check=True)
+    lib = ctypes.CDLL(str(so))
+    values = (-2 ** 31, -1, 0, 1, 5, 6, 100, 101, 2 ** 31 - 1)
+    for kv, q0, end in itertools.product(values, repeat=3):
+        for tokens, max_new, max_kv in ((0, 0, 0), (5, 5, 100), (100, 6, 5), (2 ** 31 - 1, 2 ** 31 - 1, 1 << 24)):
+            want = 0 <= kv <= max_kv and 0 <= q0 <= end <= tokens and end - q0 <= max_new
+            assert bool(lib.seq_ok(kv, q0, end, tokens, max_new, max_kv)) == want, (kv, q0, end, tokens, max_new, max_kv)
+    for a in values:
+        for b in (0, 1, 6, 2 ** 31 - 1):
+            assert bool(lib.len_ok(a, b)) == (0 <= a <= b) and bool(lib.page_ok(a, b)) == (0 <= a < b)
