@@ -32,6 +32,7 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kBatch = 16;               // scores of a thread on their way
 constexpr int kHistCopies = 2;           // histograms that even and odd lanes have to themselves
 // Keys kept in shared memory (64 lists of 32,749, 1,024 of each kept: 107 us,
 // 118 us when every pass reads the scores again).
@@ -65,23 +66,18 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
     const int64_t row = static_cast<int64_t>(s) * p.g.kv_heads + h;
     const float* sc = p.scores + row * p.score_stride;
     int32_t* kept = p.kept + row * p.keep;
-    float* sout = p.scores_out ? p.scores_out + row * p.keep : nullptr;
     if (h == 0 && tid == 0) p.kv_len_out[s] = len;
     for (int i = len + tid; i < p.keep; i += kSelThreads) {
         kept[i] = -1;
-        if (sout) sout[i] = 0.f;
+        if (p.scores_out) p.scores_out[row * p.keep + i] = 0.f;
     }
     const int cand = kv - recent, want = len - recent;  // candidates, and how many of them stay
     for (int i = (want == cand ? 0 : want) + tid; i < len; i += kSelThreads) {
-        const int j = i < want ? i : cand + i - want;
-        kept[i] = j;
-        if (sout) sout[i] = sc[j];
+        kept[i] = i < want ? i : cand + i - want;
     }
     if (want == cand || want == 0) return;
 
     const bool staged = cand <= cap;
-    if (staged)
-        for (int i = tid; i < cand; i += kSelThreads) keys[i] = score_key(__ldg(sc + i));
     auto key = [&](int i) { return staged ? keys[i] : score_key(__ldg(sc + i)); };
     // ---- the want-th largest key
     uint32_t prefix = 0, left = want;
@@ -93,9 +89,28 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
         for (int i = tid; i < kHistCopies * kBins; i += kSelThreads) hist[i / kBins][i % kBins] = 0;
         __syncthreads();
         const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
-        for (int i = tid; i < cand; i += kSelThreads) {
-            const uint32_t k = key(i);
+        auto count = [&](uint32_t k) {
             if ((k & mask) == prefix) atomicAdd(&hist[lane & (kHistCopies - 1)][(k >> shift) & ((1u << bits) - 1u)], 1u);
+        };
+        if (pass == 0) {
+            // the scores, many on their way at a time
+            for (int i0 = tid; i0 < cand; i0 += kBatch * kSelThreads) {
+                float x[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    x[u] = i0 + u * kSelThreads < cand ? __ldg(sc + i0 + u * kSelThreads) : 0.f;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = i0 + u * kSelThreads;
+                    if (i >= cand) break;
+                    const uint32_t k = score_key(x[u]);
+                    if (staged) keys[i] = k;
+                    count(k);
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int i = tid; i < cand; i += kSelThreads) count(key(i));
         }
         __syncthreads();
         // thread l: bins 2047 - 2 l and 2046 - 2 l, the highest first
@@ -130,6 +145,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
     const int seg = (cand + kSelThreads - 1) / kSelThreads * 32;  // scores of a warp
     const int a = min(cand, warp * seg), b = min(cand, a + seg);
     int gt = 0, eq = 0;
+#pragma unroll 4
     for (int i = a; i < b; i += 32) {
         const uint32_t k = i + lane < b ? key(i + lane) : 0u;
         const bool in = i + lane < b;
@@ -147,6 +163,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
         eq += s_eq[w];
     }
     const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
     for (int i = a; i < b; i += 32) {
         const bool in = i + lane < b;
         const uint32_t k = in ? key(i + lane) : 0u;
@@ -156,7 +173,6 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
         if (take) {
             const int to = gt + __popc(bg & below) + min(e, static_cast<int>(left));
             kept[to] = i + lane;
-            if (sout) sout[to] = __ldg(sc + i + lane);
         }
         gt += __popc(bg);
         eq += __popc(be);
@@ -187,6 +203,7 @@ __global__ void __launch_bounds__(kGatherThreads, 6) paged_gather_kernel(PagedEv
         if (tid < n) {
             const int64_t row = static_cast<int64_t>(s) * p.g.kv_heads + h;
             const int j = __ldg(p.kept + row * p.keep + i0 + tid);
+            if (p.scores_out) p.scores_out[row * p.keep + i0 + tid] = __ldg(p.scores + row * p.score_stride + j);
             const int page = load_page(p.g, s, j >> shift);
             if (page >= 0) a = (static_cast<int64_t>(page) * p.g.kv_heads + h) * P + (j & (P - 1));
         }
