@@ -61,58 +61,52 @@ for _name, _args in {
     getattr(lib, _name).restype = _I
 
 
-def _tensor(t, dtype, shape, what: str, device=None) -> int:
-    """Address of a CUDA tensor of this type and shape, contiguous."""
+def _refuse(t, dtype, shape, what: str, device):
+    """Raise what is wrong with t, the first of: type, place, dtype, shape, device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{what} is on {t.device}, not on {device}")
+
+
+# (a call's checks are most of its time on the host: the usual case asks each thing
+# once; `device` is always a CUDA device)
+def _tensor(t, dtype, shape, what: str, device) -> int:
+    """Address of a CUDA tensor of this type and shape, contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device):
+        _refuse(t, dtype, shape, what, device)
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
     return t.data_ptr()
 
 
 def _rows(t, dtype, n, heads, dim, what: str, device) -> tuple[int, int]:
     """Address and token stride of a [n][heads][dim] tensor whose tokens may lie apart."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{what} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.shape != (n, heads, dim):
-        raise ValueError(f"{what} must have shape {(n, heads, dim)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
-    row = heads * dim
-    st = t.stride()
-    if n and ((st[2] != 1 and dim > 1) or (st[1] != dim and heads > 1)):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (n, heads, dim) and t.device == device):
+        _refuse(t, dtype, (n, heads, dim), what, device)
+    s0, s1, s2 = t.stride()
+    if n and ((s2 != 1 and dim > 1) or (s1 != dim and heads > 1)):
         raise ValueError(f"{what}: a token's heads must be contiguous")
-    stride = st[0] if n > 1 else row
-    return t.data_ptr(), stride
+    return t.data_ptr(), s0 if n > 1 else heads * dim
 
 
 def _positions(t, axes, n, what: str, device) -> tuple[int, int]:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{what} must be a CUDA tensor")
-    if t.dtype != torch.int32:
-        raise TypeError(f"{what} must be torch.int32, got {t.dtype}")
-    if t.shape != (axes, n):
-        raise ValueError(f"{what} must have shape {(axes, n)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
-    st = t.stride()
-    if n > 1 and st[1] != 1:
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == (axes, n) and t.device == device):
+        _refuse(t, torch.int32, (axes, n), what, device)
+    s0, s1 = t.stride()
+    if n > 1 and s1 != 1:
         raise ValueError(f"{what}: an axis' positions must be contiguous")
-    return t.data_ptr(), st[0] if axes > 1 else n
+    return t.data_ptr(), s0 if axes > 1 else n
 
 
 # the raw handle of a device's current stream, and the current device, without the
 # wrapper objects of torch.cuda (a fifth of a short call's time on the host)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _call(device, stream, what: str, fn, *args) -> None:
@@ -122,7 +116,7 @@ def _call(device, stream, what: str, fn, *args) -> None:
         sp = _raw_stream(index)
     else:
         sp = stream if isinstance(stream, int) else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         st = fn(*args, sp)
     else:
         with torch.cuda.device(device):
@@ -146,9 +140,12 @@ class RopeAxes:
 
 def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, stream=None):
     """x [n][heads][head_dim] (bf16 or fp32) turned at positions (int32 [axes][n]); inverse turns back, which is also
-    the gradient: dx = rc_rope_axes(dy, positions, rope, inverse=True).  out defaults to a new tensor and may be x."""
+    the gradient: dx = rc_rope_axes(dy, positions, rope, inverse=True) (autograd does not record the call).  out defaults
+    to a new tensor and may be x."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be a [n][heads][head_dim] tensor")
+    if not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
     n, heads, dim = x.shape
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
@@ -178,8 +175,10 @@ class PagedBatch:
             raise ValueError("page_table must be a [seqs][table_pages] tensor")
         self.seqs, self.table_pages = page_table.shape
         self.device = page_table.device
+        if not page_table.is_cuda:
+            raise TypeError("page_table must be a CUDA tensor")
         c = rc_paged_batch()
-        c.page_table = _tensor(page_table, torch.int32, (self.seqs, self.table_pages), "page_table")
+        c.page_table = _tensor(page_table, torch.int32, (self.seqs, self.table_pages), "page_table", self.device)
         c.kv_len = _tensor(kv_len, torch.int32, (self.seqs,), "kv_len", self.device)
         if q_start is not None:
             c.q_start = _tensor(q_start, torch.int32, (self.seqs + 1,), "q_start", self.device)
@@ -199,8 +198,10 @@ class PagedKVCache:
         self.pages, self.kv_heads, self.page_tokens, self.head_dim = kcodes.shape
         n, h, p, d = kcodes.shape
         self.device = kcodes.device
+        if not kcodes.is_cuda:
+            raise TypeError("kcodes must be a CUDA tensor")
         c = rc_paged_view()
-        c.kcodes = _tensor(kcodes, torch.uint8, (n, h, p, d), "kcodes")
+        c.kcodes = _tensor(kcodes, torch.uint8, (n, h, p, d), "kcodes", self.device)
         c.vcodes = _tensor(vcodes, torch.uint8, (n, h, d, p), "vcodes", self.device)
         c.kscale = _tensor(kscale, torch.uint8, (n, h, p), "kscale", self.device)
         c.vscale = _tensor(vscale, torch.uint8, (n, h, p), "vscale", self.device)
