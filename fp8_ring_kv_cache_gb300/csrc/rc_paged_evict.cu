@@ -184,7 +184,7 @@ constexpr int kGatherThreads = 256;
 constexpr int kGatherPieces = 16;  // 16-byte pieces of a V row in shared memory at a time
 
 template <int D>
-__global__ void __launch_bounds__(kGatherThreads, 6) paged_gather_kernel(PagedEvictParams p) {
+__global__ void __launch_bounds__(kGatherThreads, 1536 / kGatherThreads) paged_gather_kernel(PagedEvictParams p) {
     constexpr int kRow = 16 * kGatherPieces + 16;  // bytes of a staged row: 16-byte aligned, spread over the banks
     __shared__ int64_t src[kGatherTokens];         // (page, head, place) of each token, -1: none
     __shared__ int64_t dst[kGatherTokens / 16];    // of each 16 tokens' destination
@@ -255,8 +255,9 @@ __global__ void __launch_bounds__(kGatherThreads, 6) paged_gather_kernel(PagedEv
     }
     __syncthreads();
     // V: element (d, place) of (page, head) b is byte (b D + d) P + place.
-    // Thread: tokens 4 w .. 4 w + 3 of the dims tid / 16 + 16 k.
-    const int pieces = s_pieces, w = tid & 15;
+    // Thread: tokens 4 w .. 4 w + 3 of some dims.
+    constexpr int kWords = kGatherTokens / 4;
+    const int pieces = s_pieces, w = tid % kWords;
     const int64_t to = dst[w >> 2];
     for (int first = 0; first < pieces || first == 0; first += kGatherPieces) {
         const int here = min(kGatherPieces, pieces - first);
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kGatherThreads, 6) paged_gather_kernel(PagedEv
             }
             uint8_t* out = p.g.vcodes + (to >> shift) * D * P + (to & (P - 1)) + 4 * (w & 3);
 #pragma unroll 4
-            for (int d = tid >> 4; d < D; d += kGatherThreads / 16) {
+            for (int d = tid / kWords; d < D; d += kGatherThreads / kWords) {
                 const uint8_t* row = in + d * kRow;
                 uint8_t* o = out + (static_cast<uint32_t>(d) << shift);
                 if (all) {
