@@ -17,9 +17,9 @@
 //    global memory, 32 tokens side by side, took 132 us for 64 lists of 8,192.)
 //    K rows, scales and V's pieces are on their way together.
 //
-// 8 sequences of 9,001 to 32,749 tokens x 8 heads x 128, 8,192 of each kept: 101 us,
-// 32 of them the selection (64 blocks, as many as there are lists; its passes over
-// the keys follow one another) and 70 the copies: 341 MB at 4.9 TB/s, as the pieces
+// 8 sequences of 9,001 to 32,749 tokens x 8 heads x 128, 8,192 of each kept: 95 us,
+// 24 of them the selection (64 blocks, as many as there are lists; its passes over
+// the keys follow one another) and 71 the copies: 350 MB at 4.9 TB/s, as the pieces
 // of V are read with the tokens between those that stay.
 #include <algorithm>
 
@@ -34,8 +34,8 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBatch = 16;               // scores of a thread on their way
 constexpr int kHistCopies = 2;           // histograms that even and odd lanes have to themselves
-// Keys kept in shared memory (64 lists of 32,749, 1,024 of each kept: 107 us,
-// 118 us when every pass reads the scores again).
+// Keys kept in shared memory (8 sequences of 32,749 tokens x 8 heads, 1,024 of
+// each kept: 11 us less than when every pass reads the scores again).
 constexpr int kSelCap = 48 * 1024;
 
 // Order-preserving key: larger score, larger key; -0 as +0, NaN above all.
@@ -179,6 +179,8 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
     }
 }
 
+// 64 tokens by 256 threads: 95 us for the batch above; 32 by 128 96, 64 by 128
+// 108, 128 by 512 102.
 constexpr int kGatherTokens = 64;
 constexpr int kGatherThreads = 256;
 constexpr int kGatherPieces = 16;  // 16-byte pieces of a V row in shared memory at a time
