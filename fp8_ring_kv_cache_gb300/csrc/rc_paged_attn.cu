@@ -20,7 +20,7 @@
 // Rows first (S = Q K^T) took twice the products and as many moves to keep the
 // unused half of the accumulators in place: 134 us for 32 single tokens
 // (sequences of 61 to 16,381 tokens, 8 KV heads x 6 query heads x 128), which
-// now take 98.5 us: 544 MB, 0.81 of the rate of a copy.  The rest is the start
+// now take 94.5 us: 544 MB, 0.85 of the rate of a copy.  The rest is the start
 // and end of the blocks, and warps that hold too much to be more on an SM.
 // The warps' (max, sum, O) are joined through shared memory; with several
 // splits they go to the workspace, and the block that arrives last at its row
@@ -475,9 +475,10 @@ cudaError_t launch_attention_d(PagedAttnParams& p, size_t part_floats_max, int m
     // Up to 16 rows per KV head the reading of the codes is what counts; with
     // more, each tile of 16 would read them again, and the tcgen05 kernel, whose
     // time hardly grows up to 128 rows, is the faster one (32 sequences x 8,000
-    // tokens x 8 KV heads x 128: 8 rows 97 against 252 us, 16 rows 126 against
-    // 252, 17 rows 254 with tcgen05).  Tiles of 8 rows save half the products
-    // (the same with 1 row: 95 us as a tile of 8, 124 us as one of 16).
+    // tokens x 8 KV heads x 128: 8 rows 95 against 245 us, 16 rows 129 against
+    // 245).  Tiles of 8 rows save half the products
+    // (the same with 1 row: 88 us as a tile of 8; before the
+    // prefetch 95, and 124 as one of 16).
     if (rows <= 8) return launch_rows<D, 1>(p, part_floats_max, max_counters, s);
     if (rows <= 16) return launch_rows<D, 2>(p, part_floats_max, max_counters, s);
     return launch_paged_tc(p, D, part_floats_max, s);

@@ -6,7 +6,7 @@
 // cached tokens 64 at a time, reading K pieces straight into the fp16 products'
 // operands as the attention does; the four lanes that hold a token's rows add up
 // by halves, so that each ends with the sums of two tokens.  16 sequences of 509
-// to 8,191 tokens x 8 KV heads x 6 query heads x 128: 17.6 us (76 MB, 11.3 us at the
+// to 8,191 tokens x 8 KV heads x 6 query heads x 128: 16.9 us (76 MB, 11.3 us at the
 // rate of a copy); the start of each block, three loads after one another, is what
 // keeps it from there.
 //

@@ -23,11 +23,12 @@
 // that order is kept along the summed dims (Q is stored in it) and along the
 // cached tokens (P is packed in it).
 //
-// 757 queries x 5,788 tokens x 48 heads x 128: 107 us, 1.01 PFLOP/s, 0.53 of what
+// 757 queries x 5,788 tokens x 48 heads x 128: 105 us, 1.03 PFLOP/s, 0.54 of what
 // a library product of bf16 matrices reaches; the tensor cores work 47 % of the
 // time.  What bounds it is the chain of a unit (scores to registers, maximum,
 // exponentials, P back, the hand-over to the products), which two groups do not
-// quite hide.
+// quite hide; the converters of K keep up just so (the marks of V rows that are
+// not numbers, some 40 instructions a tile, cost 2 us while one of them made them).
 #include <algorithm>
 #include <type_traits>
 
@@ -70,7 +71,7 @@ struct TcLayout {
     static constexpr uint32_t kV = kK + 2 * kTile;     // [2 buffers][2 halves][D][128 B]
     static constexpr uint32_t kScale = kV + 2 * kTile; // V scale bytes of the last four KV tiles
     static constexpr uint32_t kBar = kScale + 4 * kTileN;
-    static constexpr uint32_t kMisc = kBar + 8 * T_COUNT;  // [0] tmem, [1] abort, [4..7] KV tile holds a V that is not a number
+    static constexpr uint32_t kMisc = kBar + 8 * T_COUNT;  // [0] tmem, [1] abort, [4..11] half of a KV tile holds a V that is not a number
     static constexpr uint32_t kTotal = kMisc + 64;
     static constexpr uint32_t kAlloc = kTotal + 1024;
 };
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
         mbar_init(&bars[T_O_DONE], 1);
         mbar_init(&bars[T_DRAIN], 1);
         misc[1] = 0u;
-        for (int i = 4; i < 8; ++i) misc[i] = 0u;
+        for (int i = 4; i < 12; ++i) misc[i] = 0u;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -268,6 +269,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
         bool ok = true;
         const bool watcher = quad == 0 && lane == 0;
 
+        // whether the row sees a token of the unit's tile whose V is not a number (once its V is known to be in place)
+        auto look = [&](int u) {
+            const int j = tile_of(u);
+            if ((misc[4 + (j & 3)] | misc[8 + (j & 3)]) == 0u) return;
+            const uint8_t* vs = smem + Lay::kScale + (j & 3) * kTileN;
+            for (int k = 0; k < kTileN; ++k) poison |= vs[k] > 134 && k < limit - j * kTileN;
+        };
+
         auto unit = [&](int u) -> bool {
             const int j = tile_of(u);
             // V of this unit and K of unit u + 2, tested now and looked at after the softmax
@@ -322,10 +331,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                 }
                 tmem_st32(s_tm + 32 * half, pk);
             }
-            if (misc[4 + (j & 3)] != 0u) {
-                const uint8_t* vs = smem + Lay::kScale + (j & 3) * kTileN;
-                for (int k = 0; k < kTileN; ++k) poison |= vs[k] > 134 && k < room;
-            }
             tmem_st_wait();
             // rescale the running output when the max moved (the product of
             // unit u - 2 has finished: S of this unit came after it)
@@ -353,6 +358,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             tc_fence_before();
             __syncwarp();
             ok = named_barrier_and(kNbUnit + i, kNbUnitThreads, ok);
+            if (ok) look(u);
         }
         // ------------------------------------------------------------ epilogue
         if (ok && U > 0) ok = warp_wait(&bars[T_O_DONE], 0, ab, kDevTimeoutEpilogue);
@@ -493,7 +499,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             const uint8_t* sbase = p.g.kscale + (rr & 15);
             uint4 kr[KU];
             uint32_t ks[4];
-            uint4 vs = make_uint4(0, 0, 0, 0);  // V scale bytes of the lane's block: only looked at
             // rows rr + 32 m of tile j, whose block is `blk` of lane (rr >> 4) + 2 m
             auto fetch = [&](int m, uint32_t blk) {
                 const uint64_t at = __shfl_sync(0xffffffffu, blk, (rr >> 4) + 2 * m);
@@ -501,15 +506,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                 for (int n = 0; n < NB; ++n) kr[m * NB + n] = ldg_nc_na_v4(kbase + at * (16 * D) + 64 * n);
                 ks[m] = ldg_early(sbase + at * 16);
             };
-            auto fetch_vs = [&](uint32_t blk) {
-                if (ct < 8) vs = ldg_nc_na_v4(p.g.vscale + static_cast<uint64_t>(blk) * 16);
-            };
             int ahead = entry_at(1);
             if (T > 0) {
                 const uint32_t blk = block_of(0, entry_at(0));
 #pragma unroll
                 for (int m = 0; m < 4; ++m) fetch(m, blk);
-                fetch_vs(blk);
             }
             for (int j = 0; j < T; ++j) {
                 const int st = j & 1;
@@ -517,19 +518,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                 ahead = entry_at(j + 2);
                 if (ok) ok = warp_wait(&bars[T_K_EMPTY + st], ((j >> 1) & 1) ^ 1, ab, kDevTimeoutConvert);
                 if (!ok) continue;
-                // A V row that is not a number (scale byte over 134) counts as
-                // 0 in the product; the rows that see it are marked.  Slot
-                // j & 3: the softmax of tile j - 4 has read it (the S whose end
-                // freed this buffer came after that).
-                if (warp == kWgConvertK * 4) {
-                    const uint4 cut = cut16(vs, q.kv - (j0 + j * kTileN + 16 * lane));
-                    if (lane < 8) *reinterpret_cast<uint4*>(smem + Lay::kScale + (j & 3) * kTileN + 16 * lane) = cut;
-                    const bool bad =
-                        __any_sync(0xffffffffu, lane < 8 && (__vcmpgtu4(cut.x, 0x86868686u) | __vcmpgtu4(cut.y, 0x86868686u) |
-                                                             __vcmpgtu4(cut.z, 0x86868686u) | __vcmpgtu4(cut.w, 0x86868686u)) != 0u);
-                    if (lane == 0) misc[4 + (j & 3)] = bad ? 1u : 0u;
-                }
-                fetch_vs(blk);
                 uint8_t* dst = smem + Lay::kK + st * Lay::kTile;
                 uint8_t* lo = dst + bktile_off(rr, 16 * (ct & 3));
                 uint8_t* hi = dst + bktile_off(rr, 16 * (ct & 3) + 8);
@@ -578,8 +566,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                 if (!ok) continue;
                 uint32_t f[8];
                 const uint4 cut = cut16(vs, q.kv - (j0 + j * kTileN + 16 * c));
-                const uint32_t w[4] = {cut.x & ~__vcmpgtu4(cut.x, 0x86868686u), cut.y & ~__vcmpgtu4(cut.y, 0x86868686u),
-                                       cut.z & ~__vcmpgtu4(cut.z, 0x86868686u), cut.w & ~__vcmpgtu4(cut.w, 0x86868686u)};
+                const uint32_t nan[4] = {__vcmpgtu4(cut.x, 0x86868686u), __vcmpgtu4(cut.y, 0x86868686u),
+                                         __vcmpgtu4(cut.z, 0x86868686u), __vcmpgtu4(cut.w, 0x86868686u)};
+                const uint32_t w[4] = {cut.x & ~nan[0], cut.y & ~nan[1], cut.z & ~nan[2], cut.w & ~nan[3]};
+                // A V row that is not a number (scale byte over 134) counts as 0 in
+                // the product; the rows that see it are marked.  Slot j & 3: each
+                // group has looked at tile j - 4 before it handed over P of tile
+                // j - 2, whose product freed this buffer.
+                if ((warp & 1) == 0) {  // (the warps with the tokens' first dims: four blocks of 16 each)
+                    if (lane < 4) *reinterpret_cast<uint4*>(smem + Lay::kScale + (j & 3) * kTileN + 16 * c) = cut;
+                    const bool bad = __any_sync(0xffffffffu, (nan[0] | nan[1] | nan[2] | nan[3]) != 0u);
+                    if (lane == 0) misc[4 + 4 * ((warp >> 1) & 1) + (j & 3)] = bad ? 1u : 0u;
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     f[2 * k] = factors02(w[k]);
