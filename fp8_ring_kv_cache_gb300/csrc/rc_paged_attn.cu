@@ -20,7 +20,7 @@
 // Rows first (S = Q K^T) took twice the products and as many moves to keep the
 // unused half of the accumulators in place: 134 us for 32 single tokens
 // (sequences of 61 to 16,381 tokens, 8 KV heads x 6 query heads x 128), which
-// now take 94.5 us: 544 MB, 0.85 of the rate of a copy.  The rest is the start
+// now take 98.5 us: 544 MB, 0.81 of the rate of a copy.  The rest is the start
 // and end of the blocks, and warps that hold too much to be more on an SM.
 // The warps' (max, sum, O) are joined through shared memory; with several
 // splits they go to the workspace, and the block that arrives last at its row
@@ -178,13 +178,6 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
         for (int n = MT / 2; n < MT; ++n)
 #pragma unroll
             for (int x = 0; x < 2; ++x) vw[n][x] = ldg_nc_na_v4(vp + static_cast<size_t>(16 * n + 8 * x) * P);
-        // the next step's K comes to L2 meanwhile (the 32 ragged sequences 98.3 ->
-        // 94.9 us; V's pages as well: 99.5, and half of them 99.2)
-        const int nblk = jc + kStride + 16 * t;
-        if (g == 0 && nblk < j1 && paged_page_ok(ahead, p.g.pages)) {
-            const size_t at = (static_cast<size_t>(ahead) * p.g.kv_heads + h) * P + (nblk & (P - 1));
-            prefetch_l2(p.g.kcodes + at * D, 16 * D);
-        }
 
         // softmax: scores 2 a + x of m tile i: token kblk + 4 i + 2 (g & 1) + a, row 2 t + x
         const bool full = jc + kChunk <= least;
@@ -475,10 +468,9 @@ cudaError_t launch_attention_d(PagedAttnParams& p, size_t part_floats_max, int m
     // Up to 16 rows per KV head the reading of the codes is what counts; with
     // more, each tile of 16 would read them again, and the tcgen05 kernel, whose
     // time hardly grows up to 128 rows, is the faster one (32 sequences x 8,000
-    // tokens x 8 KV heads x 128: 8 rows 95 against 245 us, 16 rows 129 against
-    // 245).  Tiles of 8 rows save half the products
-    // (the same with 1 row: 88 us as a tile of 8; before the
-    // prefetch 95, and 124 as one of 16).
+    // tokens x 8 KV heads x 128: 8 rows 97 against 245 us, 16 rows 126 against
+    // 245).  Tiles of 8 rows save half the products (the same with 1 row: 95 us as
+    // a tile of 8, 124 us as one of 16).
     if (rows <= 8) return launch_rows<D, 1>(p, part_floats_max, max_counters, s);
     if (rows <= 16) return launch_rows<D, 2>(p, part_floats_max, max_counters, s);
     return launch_paged_tc(p, D, part_floats_max, s);

@@ -6,7 +6,7 @@
 // cached tokens 64 at a time, reading K pieces straight into the fp16 products'
 // operands as the attention does; the four lanes that hold a token's rows add up
 // by halves, so that each ends with the sums of two tokens.  16 sequences of 509
-// to 8,191 tokens x 8 KV heads x 6 query heads x 128: 16.9 us (76 MB, 11.3 us at the
+// to 8,191 tokens x 8 KV heads x 6 query heads x 128: 17.6 us (76 MB, 11.3 us at the
 // rate of a copy); the start of each block, three loads after one another, is what
 // keeps it from there.
 //
@@ -132,10 +132,6 @@ __global__ void __launch_bounds__(kScoreWarps * 32, NR == 1 ? 7 : D == 64 ? 5 : 
                     }
             }
         }
-        // the next step's codes come to L2 meanwhile (17.6 -> 16.9 us)
-        const int nblk = jc + kStride + 16 * t;
-        if (g == 0 && nblk < end && paged_page_ok(ahead, p.g.pages))
-            prefetch_l2(p.g.kcodes + ((static_cast<size_t>(ahead) * p.g.kv_heads + h) * P + (nblk & (P - 1))) * D, 16 * D);
         // over the four lanes t, by halves of what is left: lane t ends with m tile t
         float u[2][2], z[2];
 #pragma unroll
