@@ -15,6 +15,9 @@ structures that describe them, so they are made once and used for many calls:
 
 Every call is stream-ordered on torch's current stream of the tensors' device
 (or ``stream=``), allocates nothing, and runs on that device whichever is current.
+A cache that is constructed here (its workspace, and the pages of ``empty``) is
+ready for calls on any stream; the tensors that a caller passes have to be ready on
+the call's stream, and to live until it is through with them.
 """
 from __future__ import annotations
 
@@ -125,6 +128,14 @@ def _call(device, stream, what: str, fn, *args) -> None:
         _check(st, what)
 
 
+def _filled(device) -> None:
+    """Wait for the fills that were just issued on the device's current stream: the first call on what they fill may be
+    on any stream.  (Inside a capture they are part of the graph, and there is nothing to wait for.)"""
+    with torch.cuda.device(device):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+
+
 class RopeAxes:
     """The plan of several-axes rotary positions: `sections` pairs of each axis (their sum is head_dim / 2)."""
 
@@ -205,12 +216,15 @@ class PagedKVCache:
         c.vcodes = _tensor(vcodes, torch.uint8, (n, h, d, p), "vcodes", self.device)
         c.kscale = _tensor(kscale, torch.uint8, (n, h, p), "kscale", self.device)
         c.vscale = _tensor(vscale, torch.uint8, (n, h, p), "vscale", self.device)
-        if workspace is None:
+        own_workspace = workspace is None
+        if own_workspace:
             workspace = torch.zeros(RC_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
         c.workspace = _tensor(workspace, torch.uint8, (RC_PAGED_WORKSPACE_BYTES,), "workspace", self.device)
         c.pages, c.kv_heads, c.head_dim, c.page_tokens = n, h, d, p
         self.kcodes, self.vcodes, self.kscale, self.vscale, self.workspace = kcodes, vcodes, kscale, vscale, workspace
         self._c, self._ptr = c, ctypes.addressof(c)
+        if own_workspace:
+            _filled(self.device)
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda") -> "PagedKVCache":
