@@ -14,7 +14,8 @@ structures that describe them, so they are made once and used for many calls:
     cache.sync()                                          # raises RcError on bad metadata
 
 Every call is stream-ordered on torch's current stream of the tensors' device
-(or ``stream=``), allocates nothing, and runs on that device whichever is current.
+(or ``stream=``), allocates nothing but the result of ``rc_rope_axes`` without
+``out=``, and runs on that device whichever is current.
 A cache that is constructed here (its workspace, and the pages of ``empty``) is
 ready for calls on any stream; the tensors that a caller passes have to be ready on
 the call's stream, and to live until it is through with them.
@@ -136,6 +137,21 @@ def _filled(device) -> None:
             torch.cuda.current_stream().synchronize()
 
 
+def _empty_on(stream, shape, dtype, device):
+    """A new tensor for a call on `stream`.  Its memory comes from that stream's pool, so that neither work still to be
+    done on what lay there before nor the use of the block after this tensor is dropped can meet the call's kernel; and
+    it is not reused before what the current stream does with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    own = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(own):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if own.cuda_stream != current.cuda_stream:
+        t.record_stream(current)
+    return t
+
+
 class RopeAxes:
     """The plan of several-axes rotary positions: `sections` pairs of each axis (their sum is head_dim / 2)."""
 
@@ -152,7 +168,7 @@ class RopeAxes:
 def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, stream=None):
     """x [n][heads][head_dim] (bf16 or fp32) turned at positions (int32 [axes][n]); inverse turns back, which is also
     the gradient: dx = rc_rope_axes(dy, positions, rope, inverse=True) (autograd does not record the call).  out defaults
-    to a new tensor and may be x."""
+    to a new tensor (of the call's stream, kept from reuse for the current one too) and may be x."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be a [n][heads][head_dim] tensor")
     if not x.is_cuda:
@@ -164,7 +180,7 @@ def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, 
         raise ValueError(f"x has head_dim {dim}, the plan {rope.head_dim}")
     xp, xs = _rows(x, x.dtype, n, heads, dim, "x", x.device)
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
+        out = _empty_on(stream, (n, heads, dim), x.dtype, x.device)
     op, os_ = _rows(out, x.dtype, n, heads, dim, "out", x.device)
     pp, ps = _positions(positions, rope.axes, n, "positions", x.device)
     if out is not x and (xp != op or xs != os_):

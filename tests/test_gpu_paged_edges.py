@@ -3,6 +3,7 @@ switched off, borders of a row's scale.  Tolerances and definitions are those of
 tests/paged_util.py."""
 import gc
 
+import numpy as np
 import pytest
 import torch
 
@@ -72,3 +73,58 @@ def test_a_cache_built_inside_a_capture(rc):  # noqa: F811
         graph.replay()
         cache.sync()
         assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+def turned(rc):  # noqa: F811
+    rng = np.random.default_rng(4)
+    x = bf16(rng, 4096, 8, 128).cuda()
+    pos = torch.arange(4096, dtype=torch.int32, device="cuda")[None]
+    rope = rc.RopeAxes((64,))
+    want = rc.rc_rope_axes(x, pos, rope, out=torch.empty_like(x))
+    torch.cuda.synchronize()
+    gc.collect()
+    torch.cuda.empty_cache()
+    return x, pos, rope, want
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_rope_axes_result_on_another_stream_while_the_current_one_is_busy(rc, handle):  # noqa: F811
+    """The result's memory is not a block that the current stream has still to write."""
+    x, pos, rope, want = turned(rc)
+    stream = torch.cuda.Stream()
+    junk = torch.empty_like(want)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    junk.fill_(7)
+    del junk
+    out = rc.rc_rope_axes(x, pos, rope, stream=stream.cuda_stream if handle else stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_rope_axes_result_that_is_dropped(rc):  # noqa: F811
+    """Its memory is not handed out again on the current stream while the call's kernel has still to write it, nor on the
+    call's stream while the current one has still to read it."""
+    x, pos, rope, want = turned(rc)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(BUSY)
+    out = rc.rc_rope_axes(x, pos, rope, stream=stream)
+    del out
+    other = torch.full_like(want, 3.0)
+    torch.cuda.synchronize()
+    assert (other == 3).all()
+    out = rc.rc_rope_axes(x, pos, rope, stream=stream)
+    torch.cuda.current_stream().wait_stream(stream)
+    torch.cuda._sleep(BUSY)
+    copy = out.clone()
+    del out
+    with torch.cuda.stream(stream):
+        again = torch.full_like(want, 5.0)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want) and (again == 5).all()
+
+
+def test_rope_axes_result_on_the_default_streams_handle(rc):  # noqa: F811
+    x, pos, rope, want = turned(rc)
+    assert torch.equal(rc.rc_rope_axes(x, pos, rope, stream=torch.cuda.default_stream().cuda_stream), want)
