@@ -45,8 +45,12 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// (kv_len_out may be kv_len: the copies write min(kv_len, keep) there while other
+// blocks of theirs read it, which gives both the same number of tokens; the
+// selection, which needs kv_len itself, writes it only where there are no copies,
+// and every length is 0.)
 __device__ __forceinline__ int evict_len(const PagedParams& g, int s) {
-    int kv = __ldg(g.kv_len + s);
+    int kv = g.kv_len[s];
     if (!paged_len_ok(kv, g.max_kv)) {
         flag_meta(g.status);
         kv = 0;
@@ -66,7 +70,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedEvictPar
     const int64_t row = static_cast<int64_t>(s) * p.g.kv_heads + h;
     const float* sc = p.scores + row * p.score_stride;
     int32_t* kept = p.kept + row * p.keep;
-    if (h == 0 && tid == 0) p.kv_len_out[s] = len;
+    if (p.g.max_kv == 0 && h == 0 && tid == 0) p.kv_len_out[s] = len;
     for (int i = len + tid; i < p.keep; i += kSelThreads) {
         kept[i] = -1;
         if (p.scores_out) p.scores_out[row * p.keep + i] = 0.f;
@@ -198,6 +202,7 @@ __global__ void __launch_bounds__(kGatherThreads, 1536 / kGatherThreads) paged_g
     const int h = blockIdx.y, s = blockIdx.z, i0 = blockIdx.x * kGatherTokens;
     const int kv = evict_len(p.g, s);
     const int n = min(kGatherTokens, min(kv, p.keep) - i0);
+    if (i0 == 0 && h == 0 && tid == 0) p.kv_len_out[s] = min(kv, p.keep);
     if (n <= 0) return;
     const int shift = p.g.page_shift, P = 1 << shift;
     if (tid < kGatherTokens) {

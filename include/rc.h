@@ -521,7 +521,7 @@ int rc_paged_accumulate(const rc_paged_view *view, const rc_paged_batch *batch, 
  * is copied whole.  The source pages are only read, so they may be shared;
  * no destination page may be a source page or appear twice.
  *   kept [seqs][kv_heads][keep]: the kept tokens' old indices, ascending; -1 past the end
- *   kv_len_out [seqs]: min(kv_len, keep)
+ *   kv_len_out [seqs]: min(kv_len, keep); may be the batch's kv_len
  *   scores_out (may be NULL) [seqs][kv_heads][keep]: the kept tokens' scores; 0 past the end;
  *       must not overlap scores
  * Errors: RC_ERR_ARG also for keep < 1, recent outside 0 .. keep, or

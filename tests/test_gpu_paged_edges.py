@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_paged import Setup, bf16, rc  # noqa: F401 (rc: the fixture)
+import paged_util as pu
+from test_gpu_paged import Setup, bf16, dev, rc  # noqa: F401 (rc: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +129,43 @@ def test_rope_axes_result_that_is_dropped(rc):  # noqa: F811
 def test_rope_axes_result_on_the_default_streams_handle(rc):  # noqa: F811
     x, pos, rope, want = turned(rc)
     assert torch.equal(rc.rc_rope_axes(x, pos, rope, stream=torch.cuda.default_stream().cuda_stream), want)
+
+
+# ------------------------------------------------------------------ tensors that share memory
+@pytest.mark.parametrize("lens,keep", [([5000, 40, 0, 3000], 700), ([33, 20], 64), ([0, 0], 5), ([60000], 50)])
+def test_evict_shortens_the_lengths_in_place(rc, lens, keep):  # noqa: F811
+    """kv_len_out may be the batch's kv_len: every head selects among the tokens that there were."""
+    hk, page, n = 16, 32, len(lens)
+    rng = np.random.default_rng(5)
+    left = [min(x, keep) for x in lens]
+    pool, meta = pu.make([(0, x) for x in lens + left], hk, 64, page, rng)
+    table, dst = meta["table"][:n], np.ascontiguousarray(meta["table"][n:, :max(1, -(-max(left) // page))])
+    scores = dev(rng.exponential(size=(n, hk, max(lens) + 1)).astype(np.float32))
+    res = []
+    for shared in (False, True):
+        cache = rc.PagedKVCache(*(dev(pool[x]) for x in ("kcodes", "vcodes", "kscale", "vscale")))
+        kv_len = dev(np.array(lens, np.int32))
+        batch = rc.PagedBatch(dev(table), kv_len, max_kv=max(lens))
+        kept = torch.full((n, hk, keep), 99, dtype=torch.int32, device="cuda")
+        out = kv_len if shared else torch.full_like(kv_len, 99)
+        cache.evict(batch, scores, keep=keep, recent=min(keep, 16), dst_table=dev(dst), kept=kept, kv_len_out=out)
+        cache.sync()
+        assert out.tolist() == left
+        res.append((kept, cache.kcodes, cache.vcodes, cache.kscale, cache.vscale))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+    for s in range(n):
+        w = pu.evict(scores[s, hk - 1].cpu().numpy(), lens[s], keep, min(keep, 16))
+        assert res[0][0][s, hk - 1].tolist() == w + [-1] * (keep - len(w))
+
+
+def test_evict_with_bad_lengths_in_place(rc):  # noqa: F811
+    """A length out of bounds is reported and becomes 0; the other sequences are cut."""
+    st = Setup(rc, [(0, 90), (0, 70), (0, 80)], 2, 64, 16, seed=6, max_kv=90)
+    st.kv_len[1] = 91
+    kept = torch.zeros((3, 2, 20), dtype=torch.int32, device="cuda")
+    scores = torch.rand((3, 2, 90), device="cuda")
+    dst = torch.full((3, 2), -1, dtype=torch.int32, device="cuda")  # no page of the pool: nothing is copied
+    st.cache.evict(st.batch, scores, keep=20, recent=4, dst_table=dst, kept=kept, kv_len_out=st.kv_len)
+    with pytest.raises(rc.RcError):
+        st.cache.sync()
+    assert st.kv_len.tolist() == [20, 0, 20] and (kept[1] == -1).all() and (kept[0] >= 0).all()
