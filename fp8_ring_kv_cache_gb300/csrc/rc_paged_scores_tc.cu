@@ -57,8 +57,9 @@ enum : int {
     S_PART_EMPTY = 14, // [4] they have been added up
     S_Q_FULL = 18,     // the block's query rows are in place
     S_Q_EMPTY = 19,    // every group is through with them
-    S_DRAIN = 20,
-    S_COUNT = 21
+    S_L_FULL = 20,     // the block's lse are in place
+    S_DRAIN = 21,
+    S_COUNT = 22
 };
 
 template <int D>
@@ -93,6 +94,18 @@ struct StWork {
         return first_row(j0 + i * kStTile) < rows && first_tile(rb, i) < end_tile(rb);
     }
 };
+
+// A cached token that is not a number also meets rows that add nothing and those
+// past the last: its sum counts only if some other row of the block of rows sees
+// it.  (Out of line: what a rare call needs is not kept in registers otherwise.)
+template <bool CAUSAL>
+__device__ __noinline__ float checked_sum(float sum, const float* minus, const StWork<CAUSAL>& w, int rb, int token) {
+    if (sum == sum) return sum;
+    const int first = rb * w.per * kStTile, end = min(w.end_tile(rb) * kStTile, w.rows);
+    for (int row = max(first, w.first_row(token)); row < end; ++row)
+        if (minus[row - first] != -INFINITY) return sum;
+    return 0.f;
+}
 
 template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedScoreParams p, int range) {
@@ -141,6 +154,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             mbar_init(&bars[S_PART_EMPTY + i], 4);
         }
         mbar_init(&bars[S_Q_FULL], kStSums / 32);
+        mbar_init(&bars[S_L_FULL], kStSums / 32);
         mbar_init(&bars[S_Q_EMPTY], kStSums / 32);
         mbar_init(&bars[S_DRAIN], 1);
         misc[1] = 0u;
@@ -223,7 +237,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         bool ok = true;
         const int tail = min(stop, j0 + w.ktiles * kStTile);
         // adds up the sums of the pair number k
-        auto join = [&](int k) {
+        auto join = [&](int k, int rb) {
             const int slot = k & (kStParts - 1);
             ok = warp_wait(&bars[S_PART_FULL + slot], (k / kStParts) & 1, ab, kDevTimeoutEpilogue);
             if (!ok) return;
@@ -231,6 +245,12 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             float sum[2];
 #pragma unroll
             for (int a = 0; a < 2; ++a, x += kStTile) sum[a] = (x[0] + x[kStPair]) + x[2 * kStPair];
+            // a cached token that is not a number also meets rows that add nothing, and those
+            // past the last
+            if (__any_sync(0xffffffffu, sum[0] + sum[1] != sum[0] + sum[1])) {
+#pragma unroll
+                for (int a = 0; a < 2; ++a) sum[a] = checked_sum<CAUSAL>(sum[a], minus, w, rb, last + a * kStTile);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_PART_EMPTY + slot]);
 #pragma unroll
@@ -247,6 +267,17 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             if (!ok) break;
             constexpr int kPieces = D / 8, kRows = kStSums / kPieces;
             const int first = rb * w.per * kStTile, count = (w.end_tile(rb) - rb * w.per) * kStTile;
+            float lse[2];  // of rows st and st + kStSums; rows past the last, and rows that saw nothing, add nothing
+            static_assert(kStQTiles * kStTile == 2 * kStSums, "two rows a thread");
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int rw = first + st + x * kStSums;
+                lse[x] = INFINITY;
+                if (rw < w.rows) {
+                    const int tok = rw / p.group, head = h * p.group + rw - tok * p.group;
+                    lse[x] = __ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head);
+                }
+            }
 #pragma unroll 4
             for (int row = st / kPieces; row < count; row += kRows) {
                 const int rw = first + row, tok = p.group == 1 ? rw : rw / p.group, head = h * p.group + rw - tok * p.group;
@@ -256,17 +287,36 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 cp_async16_or_zero(smem + Lay::kQ + (row >> 7) * Lay::kTile + bktile_off(row & 127, 8 * (st % kPieces)),
                                    src + 8 * (st % kPieces), have);
             }
-            for (int row = st; row < count; row += kStSums) {
-                const int rw = first + row;
-                float m = -INFINITY;  // rows past the last, and rows that saw nothing, add nothing
-                if (rw < w.rows) {
-                    const int tok = rw / p.group, head = h * p.group + rw - tok * p.group;
-                    m = -__ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head) * 1.4426950408889634f;
-                    if (m == INFINITY) m = -INFINITY;
-                }
-                minus[row] = m;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float m = -lse[x] * 1.4426950408889634f;
+                if (m == INFINITY) m = -INFINITY;
+                if (st + x * kStSums < count) minus[st + x * kStSums] = m;
             }
+            // Queries of rows that add nothing (lse -infinity) are brought as zeros, as what
+            // they hold may not be numbers: each thread's own pieces, once they are there and
+            // every warp has put its rows' lse in place.
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[S_L_FULL]);
+            ok = warp_wait(&bars[S_L_FULL], rb & 1, ab, kDevTimeoutSoftmax);
+            const int last_row = min(count, w.rows - first);
+            bool off = false;
+#pragma unroll 2
+            for (int row = 4 * lane; row < count; row += kStTile) {
+                const float4 m = *reinterpret_cast<const float4*>(minus + row);
+                off |= (m.x == -INFINITY && row < last_row) || (m.y == -INFINITY && row + 1 < last_row) ||
+                       (m.z == -INFINITY && row + 2 < last_row) || (m.w == -INFINITY && row + 3 < last_row);
+            }
+            off = __any_sync(0xffffffffu, off);
             cp_async_wait_all();
+            if (!ok) break;
+            if (off) {
+#pragma unroll 1
+                for (int row = st / kPieces; row < count; row += kRows)
+                    if (minus[row] == -INFINITY)
+                        *reinterpret_cast<uint4*>(smem + Lay::kQ + (row >> 7) * Lay::kTile +
+                                                  bktile_off(row & 127, 8 * (st % kPieces))) = make_uint4(0, 0, 0, 0);
+            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_Q_FULL]);
@@ -351,7 +401,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[S_PART_FULL + slot]);
                 // the pair before, which every group has left by now or soon will have
-                if (due) join(pc - 1);
+                if (due) join(pc - 1, rb);
                 if (mine == 0) {
                     due = true;
                     last = j;
@@ -361,7 +411,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 mine = mine == 0 ? kStGroups - 1 : mine - 1;
                 ++pc;
             }
-            if (due && ok) join(pc - 1);
+            if (due && ok) join(pc - 1, rb);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_Q_EMPTY]);
         }

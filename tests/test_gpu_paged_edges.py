@@ -169,3 +169,52 @@ def test_evict_with_bad_lengths_in_place(rc):  # noqa: F811
     with pytest.raises(rc.RcError):
         st.cache.sync()
     assert st.kv_len.tolist() == [20, 0, 20] and (kept[1] == -1).all() and (kept[0] >= 0).all()
+
+
+# ------------------------------------------------------------------ accumulate: rows that are switched off
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [8, 16, 24, 48, 1000])
+def test_accumulate_rows_switched_off_add_nothing(rc, rows, dim, causal):  # noqa: F811
+    """A row whose lse is -infinity adds nothing, whatever its query holds (NaN, infinities) and whatever it would see (a
+    cached token that is not a number): every entry is what the other rows make it.  Three sequences: some rows off; all
+    rows off; all off, with cached tokens that are not numbers.  With a token that is not a number and a row that sees it,
+    its entry is NaN and no other."""
+    group = 2
+    n = rows // group
+    st = Setup(rc, [(n, n + 150), (n, n + 90), (n, n + 40)], 2, dim, 16, seed=rows + dim)
+    q = bf16(st.rng, st.tokens, 2 * group, dim)
+    off = st.rng.random((st.tokens, 2 * group)) < 0.4
+    off[n:] = True
+    bad = [(0, 20), (0, n + 149), (2, 7), (2, n + 3), (2, n + 39)]  # (sequence, cached token)
+    for s, j in bad:
+        page = st.meta["table"][s][j // 16]
+        st.pool["kscale"][page, :, j % 16] = 255
+        st.pool["kcodes"][page, :, j % 16] = 0
+    st.upload(rc)
+    # the rows that are on: any finite lse (the weights then do not add up to 1)
+    lse = (3 + st.rng.random((st.tokens, 2 * group))).astype(np.float32)
+    lse[off] = -np.inf
+    q[torch.from_numpy(off)] = torch.tensor([float("nan"), float("inf"), float("-inf"), 3e38])[
+        torch.from_numpy(st.rng.integers(0, 4, (int(off.sum()), dim)))].to(torch.bfloat16)
+    scores = st.rng.random((3, 2, st.max_kv)).astype(np.float32)
+    out = torch.full((3, 2, st.max_kv), 7.0, device="cuda")
+    st.cache.accumulate(st.batch, q.cuda(), dev(lse), dev(scores), out=out, causal=causal)
+    st.cache.sync()
+    got = out.cpu().numpy()
+    qn = np.where(off[..., None], 0.0, q.float().numpy())
+    assert np.array_equal(got[1], scores[1]) and np.array_equal(got[2], scores[2])
+    want = pu.accumulate(st.pool, st.meta, qn, lse, scores, causal)[0]
+    kv = n + 150
+    nan = np.isnan(want)
+    # (the last token is seen by the last row alone when causal)
+    for h in range(2):
+        assert nan[h, 20] and nan[h].sum() == 1 + (not causal or not off[n - 1, h * group:(h + 1) * group].all())
+    assert np.array_equal(np.isnan(got[0]), nan)
+    big = max(pu.reach(st.pool, st.meta, qn, 0, head // group, head) for head in range(2 * group))
+    tol = 2.0 ** -16 * (1 + big) * (want - scores[0]) + 2.0 ** -24 * (rows + 8) * want
+    past = want > np.finfo(np.float32).max  # weights of exp(100) and more: over what fp32 holds, which rounds to infinity
+    assert (got[0][past] == np.inf).all()
+    over = np.argwhere(~nan & ~past & ~(np.abs(got[0] - want) <= tol))
+    assert not len(over), [(tuple(i), got[0][tuple(i)], want[tuple(i)], scores[0][tuple(i)], tol[tuple(i)]) for i in over[:5]]
+    assert np.array_equal(got[0][:, kv:], scores[0][:, kv:])
