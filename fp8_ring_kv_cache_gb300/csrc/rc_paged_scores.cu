@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, NR == 1 ? 7 : D == 64 ? 5 : 
             const float keep = up ? u[1][a] : u[0][a], give = up ? u[0][a] : u[1][a];
             z[a] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
         }
-        if (j < stop) p.out[at + j] = old.x + (j < q.kv ? z[0] : 0.f);
-        if (j + 1 < stop) p.out[at + j + 1] = old.y + (j + 1 < q.kv ? z[1] : 0.f);
+        if (j < stop) p.out[at + j] = j < q.kv ? old.x + z[0] : old.x;
+        if (j + 1 < stop) p.out[at + j + 1] = j + 1 < q.kv ? old.y + z[1] : old.y;
     }
     // the rest of the range (behind the last chunk that was written above)
     const int done = end > j0 ? j0 + (end - j0 + kFewChunk - 1) / kFewChunk * kFewChunk : j0;
@@ -250,8 +250,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_scores_rows_kernel(Pag
             b = sum[n][1];
         }
     const int j = 8 * g + 2 * t;
-    if (g < 4 && j0 + j < p.g.max_kv) p.out[at + j] = p.scores[at + j] + a;
-    if (g < 4 && j0 + j + 1 < p.g.max_kv) p.out[at + j + 1] = p.scores[at + j + 1] + b;
+    const int end = rows > 0 ? q.kv : 0;  // tokens from here on keep their scores
+    if (g < 4 && j0 + j < p.g.max_kv) p.out[at + j] = j0 + j < end ? p.scores[at + j] + a : p.scores[at + j];
+    if (g < 4 && j0 + j + 1 < p.g.max_kv) p.out[at + j + 1] = j0 + j + 1 < end ? p.scores[at + j + 1] + b : p.scores[at + j + 1];
 }
 
 template <int D>

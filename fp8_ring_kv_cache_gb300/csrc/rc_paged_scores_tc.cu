@@ -134,9 +134,9 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
     w.blocks = (w.tiles + kStQTiles - 1) / kStQTiles;
     w.per = w.blocks > 0 ? (w.tiles + w.blocks - 1) / w.blocks : 1;
     w.ktiles = w.rows > 0 ? max(0, (w.end - j0 + kStTile - 1) / kStTile) : 0;
-    // tokens that no tile has keep their scores
+    // tokens behind the end keep their scores
     const int stop = min(p.g.max_kv, j0 + range);
-    for (int j = j0 + w.ktiles * kStTile + tid; j < stop; j += kStThreads) p.out[row_at + j] = p.scores[row_at + j];
+    for (int j = (w.ktiles > 0 ? w.end : j0) + tid; j < stop; j += kStThreads) p.out[row_at + j] = p.scores[row_at + j];
     if (w.ktiles == 0) return;
     AbortState ab{reinterpret_cast<volatile uint32_t*>(&misc[1]), p.g.status, p.wait_ns};
 
@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         bool due = false;
         float old[2] = {0.f, 0.f};  // and its scores so far
         bool ok = true;
-        const int tail = min(stop, j0 + w.ktiles * kStTile);
         // adds up the sums of the pair number k
         auto join = [&](int k, int rb) {
             const int slot = k & (kStParts - 1);
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 const int j = last + a * kStTile;
-                if (j < tail) p.out[row_at + j] = old[a] + (j < w.end ? sum[a] : 0.f);
+                if (j < w.end) p.out[row_at + j] = old[a] + sum[a];
             }
             due = false;
         };
@@ -326,7 +325,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 if (!w.has(rb, i)) {
                     // no row of any block sees the pair
                     if (rb == 0 && g == 0 && w.first_row(jt) >= w.rows)
-                        for (int a = j; a < min(tail, jt + kStPair); a += kStTile) p.out[row_at + a] = p.scores[row_at + a];
+                        for (int a = j; a < min(w.end, jt + kStPair); a += kStTile) p.out[row_at + a] = p.scores[row_at + a];
                     continue;
                 }
                 float next_old[2] = {0.f, 0.f};
@@ -335,7 +334,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
                         const float* from = rb == 0 || w.first_row(jt + a * kStTile) >= rb * w.per * kStTile ? p.scores : p.out;
-                        if (j + a * kStTile < tail) next_old[a] = from[row_at + j + a * kStTile];
+                        if (j + a * kStTile < w.end) next_old[a] = from[row_at + j + a * kStTile];
                     }
                 }
                 const int slot = pc & (kStParts - 1);

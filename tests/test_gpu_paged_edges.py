@@ -218,3 +218,26 @@ def test_accumulate_rows_switched_off_add_nothing(rc, rows, dim, causal):  # noq
     over = np.argwhere(~nan & ~past & ~(np.abs(got[0] - want) <= tol))
     assert not len(over), [(tuple(i), got[0][tuple(i)], want[tuple(i)], scores[0][tuple(i)], tol[tuple(i)]) for i in over[:5]]
     assert np.array_equal(got[0][:, kv:], scores[0][:, kv:])
+
+
+# ------------------------------------------------------------------ accumulate: scores that no cached token has
+@pytest.mark.parametrize("new", [1, 4, 12, 24, 200])
+def test_accumulate_copies_what_is_behind_the_end_unchanged(rc, new):  # noqa: F811
+    """Entries kv_len .. max_kv - 1 are copied bit for bit, -0 and NaNs among them."""
+    st = Setup(rc, [(new, new + 70), (new, new + 300), (0, 33)], 2, 64, 16, seed=new, max_kv=560)
+    st.meta["table"] = np.concatenate([st.meta["table"], np.full((3, 35), -1, np.int32)], 1)
+    st.upload(rc)
+    q = bf16(st.rng, st.tokens, 4, 64).cuda()
+    _, lse = st.attend(q, True)
+    bits = st.rng.integers(0, 2 ** 32, (3, 2, 560), dtype=np.uint32)  # any bits: NaNs with payloads, subnormals
+    bits[st.rng.random(bits.shape) < 0.5] = 0x80000000
+    scores = bits.view(np.int32)
+    for in_place in (False, True):
+        sd = dev(scores).view(torch.float32)
+        out = sd if in_place else torch.zeros_like(sd)
+        st.cache.accumulate(st.batch, q, lse, sd, out=None if in_place else out)
+        st.cache.sync()
+        got = out.view(torch.int32).cpu().numpy()
+        for s, kv in enumerate((new + 70, new + 300, 33)):
+            assert np.array_equal(got[s, :, kv:], scores[s, :, kv:]), s
+        assert np.array_equal(got[2], scores[2])  # (no new tokens: nothing is added)
