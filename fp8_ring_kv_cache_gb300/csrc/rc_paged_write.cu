@@ -10,8 +10,10 @@
 // through shared memory to be transposed.  Tokens of the run that are older
 // than the call keep their bytes: a run that is not all new stores the new
 // tokens byte by byte.
-// The codes of K are those of the exact turn: where the fp32 sum is too close to
-// the middle between two codes it is taken again with twice the bits.  757
+// The codes and scales of K are those of the exact turn (to 2^-25 (|a| + |b|), what
+// cos and sin leave): where the fp32 sum is too close to the middle between two codes,
+// or the row's largest to the border between two scales, it is taken again with twice
+// the bits.  757
 // tokens x 48 heads x 128: 15.9 us (28 MB, 4.1 us at the copy rate; with codes of
 // the fp32 sums, some five of which in 4.6 million then are the neighbour's,
 // 13.0 us).  What it spends its time on is the issue of the conversions and the
@@ -25,15 +27,17 @@ namespace {
 constexpr int kRun = 16;  // tokens of a block: the alignment of a V row's piece
 
 // Exponent of the row's scale and its byte, from the largest magnitude as bits:
-// infinities and NaNs are above every number.
+// infinities and NaNs are above every number.  open: whether that is within 8 units of
+// its last place of a border between two scales, 1.75 x 2^k.
 template <int LANES>
-__device__ __forceinline__ uint32_t scale_byte(const float (&x)[8], float& inv, bool& bad) {
+__device__ __forceinline__ uint32_t scale_byte(const float (&x)[8], float& inv, bool& bad, bool* open = nullptr) {
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     bad = top >= 0x7f800000u;
+    if (open) *open |= (top << 9) - ((0x600000u - 8u) << 9) <= 16u << 9;  // (the 23 bits of the fraction)
     const int e = scale_exponent(__uint_as_float(top));
     inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, e in -124 .. 7: exact
     return bad ? 255u : static_cast<uint32_t>(e + 127);
@@ -89,6 +93,43 @@ __device__ __forceinline__ float sum_exactly(float a, float c, float cl, float b
     return __uint_as_float(((off > 0.f) == (y > 0.f)) ? u | 1u : u - 1u);  // between y and its neighbour: the odd one
 }
 
+// K's rows of heads h0 .. h1 - 1 of a warp's tokens written again, all from the exact
+// sums, where the fp32 sums leave the scale of one of them open.  (Out of line, with the
+// angles taken again: what some rows of a million need costs the others little.)
+template <int D>
+__device__ __noinline__ void write_exact_rows(const PagedWriteParams& p, bool live, int h0, int h1, int c, int row, int page, int place) {
+    TurnPair cs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        cs[i] = turn_cos_sin_pair(__ldg(p.pos + p.rope.axis[4 * c + i] * p.pos_stride + row), p.rope.turns[4 * c + i]);
+    for (int h = h0; h < h1; ++h) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.K + row * p.k_stride + static_cast<size_t>(h) * D + c * 8));
+        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = __uint_as_float(in[i] << 16), b = __uint_as_float(in[i] & 0xFFFF0000u);
+            const float2 ch = cs[i].hi, cl = cs[i].lo;
+            if (a == 0.f && b == 0.f) {  // (a pair of zeros keeps its sign)
+                rotate_pair(a, b, ch.x, ch.y, y[2 * i], y[2 * i + 1]);
+            } else {
+                y[2 * i] = sum_exactly(a, ch.x, cl.x, -b, ch.y, cl.y);
+                y[2 * i + 1] = sum_exactly(a, ch.y, cl.y, b, ch.x, cl.x);
+            }
+        }
+        float inv;
+        bool bad;
+        const uint32_t kb = scale_byte<D / 8>(y, inv, bad);
+        if (!live) continue;
+        uint32_t kc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kc[i] = bad ? 0u : e4m3x2(y[2 * i] * inv, y[2 * i + 1] * inv);
+        const size_t at = ((static_cast<size_t>(page) * p.g.kv_heads + h) << p.g.page_shift) + place;
+        *reinterpret_cast<uint2*>(p.g.kcodes + at * D + c * 8) = make_uint2(kc[0] | (kc[1] << 16), kc[2] | (kc[3] << 16));
+        if (c == 0) p.g.kscale[at] = static_cast<uint8_t>(kb);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged_write_kernel(const __grid_constant__ PagedWriteParams p, int runs, int heads_per_block) {
     constexpr int LANES = D / 8;  // of one token
@@ -128,6 +169,7 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged_write_kernel(cons
         kw = ldg_nc_na_v4(kr + static_cast<size_t>(h0) * D);
         vw = ldg_nc_na_v4(vr + static_cast<size_t>(h0) * D);
     }
+    bool open = false;  // a scale of K is
     for (int h = h0; h < h1; ++h) {
         float k[8], v[8], reach[4];
         const uint32_t ki[4] = {kw.x, kw.y, kw.z, kw.w}, vi[4] = {vw.x, vw.y, vw.z, vw.w};
@@ -146,7 +188,10 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged_write_kernel(cons
         uint32_t kc[4], vc[4];  // pairs of codes
         float inv;
         bool bad;
-        const uint32_t kb = scale_byte<LANES>(k, inv, bad);
+        // The fp32 sums are within 2^-22 (|a| + |b|) of the exact ones, and |a| + |b| is at
+        // most twice the larger of the turned pair: the row's largest magnitude is within
+        // 2^-21 of itself, 7 units of the last place at a border between two scales.
+        const uint32_t kb = scale_byte<LANES>(k, inv, bad, &open);
         // The fp32 sum is within 2^-22 (|a| + |b|) of the exact one (cos and sin half
         // an ulp each, 2^-25, and three roundings of 2^-24: 2.1e-7).  Where both ends
         // of that range have one code it is the exact sum's; the few others (one
@@ -200,6 +245,7 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged_write_kernel(cons
             for (int t = a; t < b; ++t) dst[static_cast<size_t>(d) * P + t] = st[t * kRow + d];
         }
     }
+    if (__any_sync(0xffffffffu, open)) write_exact_rows<D>(p, live, h0, h1, c, row, page, off + tok);
 }
 
 template <int D>

@@ -241,3 +241,37 @@ def test_accumulate_copies_what_is_behind_the_end_unchanged(rc, new):  # noqa: F
         for s, kv in enumerate((new + 70, new + 300, 33)):
             assert np.array_equal(got[s, :, kv:], scores[s, :, kv:]), s
         assert np.array_equal(got[2], scores[2])  # (no new tokens: nothing is added)
+
+
+# ------------------------------------------------------------------ write: the row scale next to its border
+# (position, 256 a, 256 b) of the pair with frequency 1: the larger of the turned pair lies within 2.5e-7 of 1.75 * 2^k,
+# the border of a scale, but more than 2^-25 (a + b) from it, and its fp32 sum falls on the other side of it
+BORDER = [(322, 296, 900), (1956, 316, 360), (3677, 872, 206), (3688, 872, 206), (5606, 406, 980), (5976, 274, 936),
+          (6133, 344, 306), (7257, 430, 245), (7844, 916, 224), (11456, 147, 884), (13237, 432, 181), (14577, 450, 196),
+          (15429, 280, 908), (16507, 932, 162), (18909, 378, 334), (19036, 151, 584), (19620, 376, 876), (20062, 416, 197),
+          (20389, 154, 888), (22540, 272, 356), (23047, 288, 384)]
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_write_scales_are_those_of_the_exact_turn(rc, dim):  # noqa: F811
+    """Rows whose largest magnitude is next to the border between two scales have the exact turn's scale and codes."""
+    n = len(BORDER)
+    st = Setup(rc, [(n, n)], 3, dim, 16, seed=dim)
+    k = torch.zeros((n, 3, dim), dtype=torch.float64)
+    for t, (_, a, b) in enumerate(BORDER):
+        for h, f in enumerate((1 / 256, -(2.0 ** 9), 2.0 ** -40)):
+            k[t, h, 0], k[t, h, 1] = a * f, b * f
+    k[:, :, 2:] = 2.0 ** -6 * bf16(st.rng, n, 3, dim - 2).double() * k[:, :, :1].abs()
+    k = k.to(torch.bfloat16)
+    pos = np.array([[p for p, _, _ in BORDER]], np.int32)
+    st.cache.write(st.batch, k.cuda(), k.cuda(), dev(pos), rc.RopeAxes((dim // 2,)))
+    st.cache.sync()
+    y = pu.turn(k.double().numpy(), pos, (dim // 2,))
+    x = np.abs(k.double().numpy())
+    top = np.abs(y).max(-1)
+    border = 1.75 * 2.0 ** np.round(np.log2(top / 1.75))
+    assert (np.abs(top - border) > 2.0 ** -25 * (x[..., 0] + x[..., 1])).all() and (np.abs(top / border - 1) < 2.5e-7).all()
+    codes, scale = pu.quantise(y)
+    table, at = st.meta["table"][0], np.arange(n)
+    assert np.array_equal(st.cache.kscale.cpu().numpy()[table[at // 16], :, at % 16], scale)
+    assert np.array_equal(st.cache.kcodes.cpu().numpy()[table[at // 16], :, at % 16], codes)
