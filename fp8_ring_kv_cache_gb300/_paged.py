@@ -97,6 +97,21 @@ def _rows(t, dtype, n, heads, dim, what: str, device) -> tuple[int, int]:
     return t.data_ptr(), s0 if n > 1 else heads * dim
 
 
+def _rows_meet(a: int, sa: int, b: int, sb: int, n: int, width: int) -> bool:
+    """Whether n rows of `width` bytes, sa bytes apart from address a, share a byte with those sb apart from b."""
+    d = b - a
+    if n < 1 or d >= (n - 1) * sa + width or -d >= (n - 1) * sb + width:
+        return False
+    if n == 1 or sa == sb:  # row j of b begins d + (j - i) s behind row i of a: the largest j - i that is not too far
+        k = min((width - 1 - d) // sa, n - 1)
+        return k > -n and d + k * sa + width > 0
+    for i in range(n):
+        j = min((i * sa - d + width - 1) // sb, n - 1)
+        if j >= 0 and j * sb + width > i * sa - d:
+            return True
+    return False
+
+
 def _positions(t, axes, n, what: str, device) -> tuple[int, int]:
     if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == (axes, n) and t.device == device):
         _refuse(t, torch.int32, (axes, n), what, device)
@@ -184,9 +199,8 @@ def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, 
     op, os_ = _rows(out, x.dtype, n, heads, dim, "out", x.device)
     pp, ps = _positions(positions, rope.axes, n, "positions", x.device)
     if out is not x and (xp != op or xs != os_):
-        size = x.element_size()  # spans of memory from the first to the last token's end
-        xe, oe = xp + ((n - 1) * xs + heads * dim) * size, op + ((n - 1) * os_ + heads * dim) * size
-        if xp < oe and op < xe and n:
+        size = x.element_size()
+        if _rows_meet(xp, xs * size, op, os_ * size, n, heads * dim * size):
             raise ValueError("out overlaps x without being x")
     _call(x.device, stream, "rc_rope_axes", lib.rc_rope_axes, rope._ptr, xp, xs, op, os_,
           RC_BF16 if x.dtype == torch.bfloat16 else RC_F32, n, heads, pp, ps, 1 if inverse else 0)

@@ -1,5 +1,6 @@
 // rc_paged_host.cu -- the C ABI of the several-axes rotary positions and the
 // paged cache (include/rc.h): argument checks, parameter blocks, launches.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -64,6 +65,18 @@ uint64_t turns_of(double theta) {
     const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(theta, &e), 53));
     const int shift = 53 - e + 12;  // 64 .. 97
     return static_cast<uint64_t>((m * kInv + (static_cast<unsigned __int128>(1) << (shift - 1))) >> shift);
+}
+
+// Whether two sets of rows share memory: rows of `width` elements of `size` bytes, `stride` elements apart.
+struct Rows {
+    const void* at;
+    int64_t stride, rows, width;
+};
+bool meet(const Rows& x, const Rows& y, int size) {
+    if (x.rows < 1 || x.width < 1 || y.rows < 1 || y.width < 1) return false;
+    constexpr int64_t kFar = INT64_C(1) << 56;  // rows farther apart than any address (times `size` stays in 64 bits)
+    return paged_rows_meet(reinterpret_cast<uintptr_t>(x.at), std::min(x.stride, kFar) * size, x.rows, x.width * size,
+                           reinterpret_cast<uintptr_t>(y.at), std::min(y.stride, kFar) * size, y.rows, y.width * size);
 }
 
 bool stride_ok(int64_t stride, int64_t row, int unit) { return stride >= row && stride % unit == 0; }
@@ -146,6 +159,9 @@ int rc_rope_axes(const rc_rope_plan* plan, const void* x, int64_t x_stride, void
     const int64_t row = static_cast<int64_t>(heads) * plan->head_dim;
     if (!stride_ok(x_stride, row, unit) || !stride_ok(out_stride, row, unit) || pos_stride < n) return RC_ERR_ARG;
     if (n > 0x7fffffff || row > 0x7fffffff) return RC_ERR_UNSUPPORTED;
+    if (!(x == out && x_stride == out_stride) &&
+        meet({x, x_stride, n, row}, {out, out_stride, n, row}, dtype == RC_BF16 ? 2 : 4))
+        return RC_ERR_ARG;
     const int st = ready();
     if (st != RC_OK) return st;
     RopeAxesParams p{};

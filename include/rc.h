@@ -397,11 +397,11 @@ int rc_rope_plan_init(rc_rope_plan *plan, int head_dim, int axes, const int *sec
  * device [n][heads][head_dim] of dtype RC_BF16 or RC_F32, tokens x_stride /
  * out_stride elements apart (>= heads * head_dim, a multiple of 16 bytes), so
  * a slice of a fused projection's rows can be passed.  out may be x (the same
- * address and stride); other overlaps are not supported.  positions: device
- * int32 [axes][n], axes pos_stride elements apart (>= n).  The arithmetic is
- * fp32, rounded once to dtype.  n = 0 does nothing.
+ * address and stride) or lie between its rows, but share no element with it
+ * otherwise.  positions: device int32 [axes][n], axes pos_stride elements apart
+ * (>= n).  The arithmetic is fp32, rounded once to dtype.  n = 0 does nothing.
  * Errors: RC_ERR_ARG (NULL or unaligned pointers, n < 0, heads < 1, a stride
- * too small or unaligned, a plan that rc_rope_plan_init did not fill).
+ * too small or unaligned, out overlapping x, a plan that rc_rope_plan_init did not fill).
  */
 int rc_rope_axes(const rc_rope_plan *plan, const void *x, int64_t x_stride, void *out, int64_t out_stride,
                  int dtype, int64_t n, int heads, const int32_t *positions, int64_t pos_stride, int inverse,

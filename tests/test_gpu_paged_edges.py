@@ -132,6 +132,25 @@ def test_rope_axes_result_on_the_default_streams_handle(rc):  # noqa: F811
 
 
 # ------------------------------------------------------------------ tensors that share memory
+def test_rope_axes_from_one_slice_of_the_rows_to_another(rc):  # noqa: F811
+    """Queries of a fused projection's rows turned into the place next to them: no element is shared, and none but the
+    result's changes.  One that does share some is refused."""
+    rng = np.random.default_rng(7)
+    n, heads = 61, 4
+    rope, pos = rc.RopeAxes((24, 20, 20)), dev(rng.integers(0, 9000, (3, n)).astype(np.int32))
+    fused = bf16(rng, n, 3 * heads, 128).cuda()
+    before = fused.clone()
+    want = rc.rc_rope_axes(fused[:, :heads].contiguous(), pos, rope)
+    rc.rc_rope_axes(fused[:, :heads], pos, rope, out=fused[:, 2 * heads:])
+    assert torch.equal(fused[:, 2 * heads:], want) and torch.equal(fused[:, :2 * heads], before[:, :2 * heads])
+    flat = fused.view(-1)
+    apart = flat[:n * 2 * heads * 128].view(n, 2 * heads, 128)[:, :heads]   # rows at another distance, over the same memory
+    for out in (fused[:, heads - 1:2 * heads - 1], apart):
+        with pytest.raises(ValueError):
+            rc.rc_rope_axes(fused[:, :heads], pos, rope, out=out)
+    assert torch.equal(fused[:, 2 * heads:], want) and torch.equal(fused[:, :2 * heads], before[:, :2 * heads])
+
+
 @pytest.mark.parametrize("lens,keep", [([5000, 40, 0, 3000], 700), ([33, 20], 64), ([0, 0], 5), ([60000], 50)])
 def test_evict_shortens_the_lengths_in_place(rc, lens, keep):  # noqa: F811
     """kv_len_out may be the batch's kv_len: every head selects among the tokens that there were."""
