@@ -214,6 +214,7 @@ int rc_paged_attend(const rc_paged_view* view, const rc_paged_batch* batch, cons
     if (!Q_bf16 || !out_bf16 || !aligned16(Q_bf16) || !aligned16(out_bf16)) return RC_ERR_ARG;
     const int64_t row = static_cast<int64_t>(heads) * view->head_dim;
     if (!stride_ok(q_stride, row, 8) || !stride_ok(out_stride, row, 8)) return RC_ERR_ARG;
+    if (meet({Q_bf16, q_stride, p.g.tokens, row}, {out_bf16, out_stride, p.g.tokens, row}, 2)) return RC_ERR_ARG;
     if (static_cast<int64_t>(p.g.max_new) * (heads / view->kv_heads) > (1 << 30)) return RC_ERR_UNSUPPORTED;
     st = ready();
     if (st != RC_OK) return st;
@@ -246,6 +247,9 @@ int rc_paged_accumulate(const rc_paged_view* view, const rc_paged_batch* batch, 
     if (heads < 1 || heads > 65535 || heads % view->kv_heads != 0 || score_stride < p.g.max_kv) return RC_ERR_ARG;
     if (p.g.max_kv == 0) return RC_OK;
     if (!scores || !out) return RC_ERR_ARG;
+    const int64_t lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
+    if (scores != out && meet({scores, score_stride, lists, p.g.max_kv}, {out, score_stride, lists, p.g.max_kv}, 4))
+        return RC_ERR_ARG;
     if (p.g.tokens > 0 && (!Q_bf16 || !lse || !aligned16(Q_bf16))) return RC_ERR_ARG;
     if (p.g.tokens > 0 && !stride_ok(q_stride, static_cast<int64_t>(heads) * view->head_dim, 8)) return RC_ERR_ARG;
     if (static_cast<int64_t>(p.g.max_new) * (heads / view->kv_heads) > (1 << 30)) return RC_ERR_UNSUPPORTED;
@@ -279,6 +283,9 @@ int rc_paged_evict(const rc_paged_view* view, const rc_paged_batch* batch, const
     if (static_cast<int64_t>(dst_pages) * view->page_tokens < most) return RC_ERR_ARG;
     if (most > 0 && (!scores || !dst_table)) return RC_ERR_ARG;
     if (keep > (1 << 24)) return RC_ERR_UNSUPPORTED;
+    const int64_t lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
+    if (scores_out && meet({scores, score_stride, lists, p.g.max_kv}, {scores_out, lists * keep, 1, lists * keep}, 4))
+        return RC_ERR_ARG;
     st = ready();
     if (st != RC_OK) return st;
     p.scores = scores;

@@ -493,7 +493,7 @@ int rc_paged_write(const rc_paged_view *view, const rc_paged_batch *batch, const
  * (rc_rope_axes), [tokens][heads][head_dim]; out is bf16 of the same layout;
  * lse (may be NULL) is fp32 [tokens][heads], the natural logarithm of the sum
  * of exp(scores).  A query that sees nothing gets zeros and lse = -infinity.
- * heads must be a multiple of kv_heads; out must not overlap Q.
+ * heads must be a multiple of kv_heads; out must share no element with Q (RC_ERR_ARG).
  */
 int rc_paged_attend(const rc_paged_view *view, const rc_paged_batch *batch, const void *Q_bf16, int64_t q_stride,
                     int heads, void *out_bf16, int64_t out_stride, float *lse, int causal, void *stream);
@@ -504,7 +504,7 @@ int rc_paged_attend(const rc_paged_view *view, const rc_paged_batch *batch, cons
  * that see token j of exp(q . k_j / sqrt(head_dim) - lse).  lse as
  * rc_paged_attend gives it; a row whose lse is -infinity adds nothing.
  * scores, out: device fp32 [seqs][kv_heads][score_stride], score_stride >=
- * max_kv; out may be scores, other overlaps are not supported.  Entries kv_len .. max_kv - 1 are copied
+ * max_kv; out may be scores, other overlaps are refused (RC_ERR_ARG).  Entries kv_len .. max_kv - 1 are copied
  * unchanged, entries past max_kv not touched.  Every entry is summed in one fixed order: the
  * same inputs give the same bits.
  */
@@ -523,7 +523,7 @@ int rc_paged_accumulate(const rc_paged_view *view, const rc_paged_batch *batch, 
  *   kept [seqs][kv_heads][keep]: the kept tokens' old indices, ascending; -1 past the end
  *   kv_len_out [seqs]: min(kv_len, keep); may be the batch's kv_len
  *   scores_out (may be NULL) [seqs][kv_heads][keep]: the kept tokens' scores; 0 past the end;
- *       must not overlap scores
+ *       must not overlap scores (RC_ERR_ARG)
  * Errors: RC_ERR_ARG also for keep < 1, recent outside 0 .. keep, or
  * min(keep, max_kv) tokens that do not fit dst_pages pages.
  */

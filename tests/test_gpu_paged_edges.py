@@ -151,6 +151,31 @@ def test_rope_axes_from_one_slice_of_the_rows_to_another(rc):  # noqa: F811
     assert torch.equal(fused[:, 2 * heads:], want) and torch.equal(fused[:, :2 * heads], before[:, :2 * heads])
 
 
+def test_scores_and_results_between_each_others_rows(rc):  # noqa: F811
+    """Queries and results that alternate in one buffer are as good as separate ones; over each other they are refused."""
+    st = Setup(rc, [(1, 300), (40, 200)], 2, 64, 16, seed=8)
+    n, heads = st.tokens, 4
+    both = torch.zeros((n, 2 * heads, 64), dtype=torch.bfloat16, device="cuda")
+    both[:, :heads] = bf16(st.rng, n, heads, 64).cuda()
+    want, lse = st.attend(both[:, :heads].contiguous(), True)
+    st.cache.attend(st.batch, both[:, :heads], both[:, heads:])
+    st.cache.sync()
+    assert torch.equal(both[:, heads:], want)
+    scores = torch.zeros((4, 2, st.max_kv), device="cuda")
+    kept, length = torch.zeros((2, 2, 8), dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    dst = torch.zeros((2, 1), dtype=torch.int32, device="cuda")
+    for call in (lambda: st.cache.attend(st.batch, both[:, :heads], both[:, heads - 1:2 * heads - 1]),
+                 lambda: st.cache.accumulate(st.batch, both[:, :heads], lse, scores[:2], out=scores[1:3]),
+                 lambda: st.cache.evict(st.batch, scores[:2], keep=8, recent=2, dst_table=dst, kept=kept, kv_len_out=length,
+                                        scores_out=scores.view(-1)[:32].view(2, 2, 8))):
+        with pytest.raises(rc.RcError) as e:
+            call()
+        assert e.value.status == rc.RC_ERR_ARG
+    st.cache.accumulate(st.batch, both[:, :heads], lse, scores[:2], out=scores[2:])
+    st.cache.sync()
+    assert scores[2:].any() and not scores[:2].any()
+
+
 @pytest.mark.parametrize("lens,keep", [([5000, 40, 0, 3000], 700), ([33, 20], 64), ([0, 0], 5), ([60000], 50)])
 def test_evict_shortens_the_lengths_in_place(rc, lens, keep):  # noqa: F811
     """kv_len_out may be the batch's kv_len: every head selects among the tokens that there were."""

@@ -63,3 +63,22 @@ def test_rope_axes_refuses_what_overlaps(rc):  # noqa: F811
     # 5 tokens of 4 heads x 64, bf16: rows of 512 bytes
     for x, xs, out, os in ((A, 256, A + 512, 256), (A, 512, A + 256, 512), (A, 512, A + 496, 512), (A + 2048, 256, A, 264), (A, 512, A, 256)):
         assert rc.lib.rc_rope_axes(p, x, xs, out, os, 0, 5, 4, A, 5, 0, None) == rc.RC_ERR_ARG, (x - A, xs, out - A, os)
+
+
+def test_attend_refuses_results_over_its_queries(rc):  # noqa: F811
+    v, b = structs(rc)  # 5 tokens of 4 heads x 64: rows of 512 bytes
+    for q, qs, out, os in ((A, 256, A, 256), (A, 256, A + 16, 256), (A, 512, A + 496, 512), (A, 512, A, 256), (A + 2048, 256, A, 264)):
+        assert calls(rc, v, b, q=q, qs=qs, out=out, os=os)["attend"]() == rc.RC_ERR_ARG, (q - A, qs, out - A, os)
+
+
+def test_accumulate_refuses_scores_over_each_other(rc):  # noqa: F811
+    v, b = structs(rc)  # 3 sequences x 2 heads, rows of 60 scores
+    for out, stride in ((A + 4, 60), (A + 236, 119), (A - 4, 60), (A + 4 * 60, 60), (A - 4 * 299, 60)):
+        assert calls(rc, v, b, scores=A, out=out, stride=stride)["accumulate"]() == rc.RC_ERR_ARG, (out - A, stride)
+
+
+def test_evict_refuses_scores_over_each_other(rc):  # noqa: F811
+    v, b = structs(rc)  # 3 sequences x 2 heads: rows of 60 scores, 48 of the kept ones in all
+    vp, bp = ctypes.addressof(v), ctypes.addressof(b)
+    for out, stride in ((A, 60), (A + 4 * 359, 60), (A - 4 * 47, 60), (A + 4 * 60, 100)):
+        assert rc.lib.rc_paged_evict(vp, bp, A, stride, 8, 2, A, 1, A, A, out, None) == rc.RC_ERR_ARG, (out - A, stride)
