@@ -200,7 +200,9 @@ def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, 
     pp, ps = _positions(positions, rope.axes, n, "positions", x.device)
     if out is not x and (xp != op or xs != os_):
         size = x.element_size()
-        if _rows_meet(xp, xs * size, op, os_ * size, n, heads * dim * size):
+        row = heads * dim
+        if op < xp + ((n - 1) * xs + row) * size and xp < op + ((n - 1) * os_ + row) * size and \
+                _rows_meet(xp, xs * size, op, os_ * size, n, row * size):
             raise ValueError("out overlaps x without being x")
     _call(x.device, stream, "rc_rope_axes", lib.rc_rope_axes, rope._ptr, xp, xs, op, os_,
           RC_BF16 if x.dtype == torch.bfloat16 else RC_F32, n, heads, pp, ps, 1 if inverse else 0)
