@@ -152,14 +152,17 @@ def _filled(device) -> None:
             torch.cuda.current_stream().synchronize()
 
 
+def _stream(stream, device):
+    return torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+
+
 def _empty_on(stream, shape, dtype, device):
     """A new tensor for a call on `stream`.  Its memory comes from that stream's pool, so that neither work still to be
     done on what lay there before nor the use of the block after this tensor is dropped can meet the call's kernel; and
     it is not reused before what the current stream does with it."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    current = torch.cuda.current_stream(device)
-    own = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    own, current = _stream(stream, device), torch.cuda.current_stream(device)
     with torch.cuda.stream(own):
         t = torch.empty(shape, dtype=dtype, device=device)
     if own.cuda_stream != current.cuda_stream:
@@ -180,10 +183,28 @@ class RopeAxes:
         self._ptr = ctypes.addressof(self.plan)
 
 
+class _Turn(torch.autograd.Function):
+    """The turn with its gradient, the turn back."""
+
+    @staticmethod
+    def forward(ctx, x, positions, rope, inverse):
+        ctx.rope, ctx.inverse = rope, inverse
+        ctx.save_for_backward(positions)
+        return rc_rope_axes(x.detach(), positions, rope, inverse=inverse)
+
+    @staticmethod
+    def backward(ctx, dy):
+        dy = dy.contiguous()  # (a broadcast gradient has no strides that the kernel takes)
+        if dy.data_ptr() % 16:
+            dy = dy.clone()
+        return rc_rope_axes(dy, ctx.saved_tensors[0], ctx.rope, inverse=not ctx.inverse), None, None, None
+
+
 def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, stream=None):
     """x [n][heads][head_dim] (bf16 or fp32) turned at positions (int32 [axes][n]); inverse turns back, which is also
-    the gradient: dx = rc_rope_axes(dy, positions, rope, inverse=True) (autograd does not record the call).  out defaults
-    to a new tensor (of the call's stream, kept from reuse for the current one too) and may be x."""
+    the gradient: dx = rc_rope_axes(dy, positions, rope, inverse=True).  out defaults to a new tensor (of the call's
+    stream, kept from reuse for the current one too) and may be x.  Autograd records the call if x requires a gradient;
+    as with torch's own functions, not with out=, which is refused then."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be a [n][heads][head_dim] tensor")
     if not x.is_cuda:
@@ -193,6 +214,16 @@ def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, 
         raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
     if dim != rope.head_dim:
         raise ValueError(f"x has head_dim {dim}, the plan {rope.head_dim}")
+    if torch.is_grad_enabled() and (x.requires_grad or getattr(out, "requires_grad", False)):
+        if out is not None:
+            raise RuntimeError("rc_rope_axes: out= is not differentiable, but x or out requires a gradient")
+        if stream is None:
+            return _Turn.apply(x, positions, rope, inverse)
+        own, current = _stream(stream, x.device), torch.cuda.current_stream(x.device)
+        with torch.cuda.stream(own):  # (autograd runs the gradient on the stream of the turn)
+            y = _Turn.apply(x, positions, rope, inverse)
+        y.record_stream(current)
+        return y
     xp, xs = _rows(x, x.dtype, n, heads, dim, "x", x.device)
     if out is None:
         out = _empty_on(stream, (n, heads, dim), x.dtype, x.device)
@@ -233,7 +264,8 @@ class PagedBatch:
 
 class PagedKVCache:
     """One layer's pages (uint8 tensors kcodes [pages][kv_heads][P][head_dim], vcodes [pages][kv_heads][head_dim][P],
-    kscale and vscale [pages][kv_heads][P]) and the workspace of the calls on them."""
+    kscale and vscale [pages][kv_heads][P]) and the workspace of the calls on them.  The calls fill tensors that the
+    caller passes; autograd records none of them."""
 
     def __init__(self, kcodes, vcodes, kscale, vscale, workspace=None):
         if not isinstance(kcodes, torch.Tensor) or kcodes.dim() != 4:

@@ -319,3 +319,108 @@ def test_write_scales_are_those_of_the_exact_turn(rc, dim):  # noqa: F811
     table, at = st.meta["table"][0], np.arange(n)
     assert np.array_equal(st.cache.kscale.cpu().numpy()[table[at // 16], :, at % 16], scale)
     assert np.array_equal(st.cache.kcodes.cpu().numpy()[table[at // 16], :, at % 16], codes)
+
+
+# ------------------------------------------------------------------ rotary positions: the gradient
+def rope_case(rc, dtype=torch.float32, n=19, heads=3):  # noqa: F811
+    rng = np.random.default_rng(9)
+    rope = rc.RopeAxes((12, 10, 10))
+    x = torch.from_numpy(rng.standard_normal((n, heads, 64)).astype(np.float32)).to(dtype).cuda().requires_grad_()
+    pos = rng.integers(0, 5000, (3, n)).astype(np.int32)
+    return rng, rope, x, pos, dev(pos)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_axes_gradient_by_autograd(rc, dtype, inverse):  # noqa: F811
+    """The gradient that autograd finds is the definition's adjoint (2^-20 of a pair's size, and bf16's half step), and
+    the hand call's bit for bit."""
+    rng, rope, x, pos, pd = rope_case(rc, dtype)
+    dy = torch.from_numpy(rng.standard_normal(x.shape).astype(np.float32)).to(dtype).cuda()
+    y = rc.rc_rope_axes(x, pd, rope, inverse=inverse)
+    assert y.requires_grad and torch.equal(y.detach(), rc.rc_rope_axes(x.detach(), pd, rope, inverse=inverse))
+    (dx,) = torch.autograd.grad(y, x, dy)
+    assert torch.equal(dx, rc.rc_rope_axes(dy, pd, rope, inverse=not inverse))
+    g = dy.double().cpu().numpy()
+    want = pu.turn(g, pos, rope.sections, sign=1.0 if inverse else -1.0)
+    r = np.repeat(np.abs(g)[..., 0::2] + np.abs(g)[..., 1::2], 2, -1)
+    tol = 2.0 ** -20 * r + (2.0 ** -8 * np.abs(want) if dtype == torch.bfloat16 else 0)
+    assert (np.abs(dx.double().cpu().numpy() - want) <= tol).all()
+
+
+def test_rope_axes_gradient_against_differences_of_a_loss(rc):  # noqa: F811
+    """sum((R x)^3) along a direction: the central difference with step e is the gradient's product with the direction
+    but for e^2 sum (R v)^3 exactly (the loss is a cubic), and the roundings of the values, 2^-20 of their sizes."""
+    rng, rope, x, _, pd = rope_case(rc)
+    y = rc.rc_rope_axes(x, pd, rope)
+    (dx,) = torch.autograd.grad((y.double() ** 3).sum(), x)
+    v = dev(rng.standard_normal(x.shape).astype(np.float32))
+    with torch.no_grad():
+        e = 0.5
+        f = [(rc.rc_rope_axes(x + s * e * v, pd, rope).double() ** 3).sum() for s in (1, -1)]
+        rv = rc.rc_rope_axes(v, pd, rope).double()
+        size = ((x.abs() + v.abs()).double().sum(-1, keepdim=True) ** 3).sum() * 3
+    assert abs((f[0] - f[1]) / (2 * e) - e * e * (rv ** 3).sum() - (dx.double() * v.double()).sum()) <= 2.0 ** -20 * 4 * size
+
+
+def test_rope_axes_gradients_of_every_kind(rc):  # noqa: F811
+    """A broadcast gradient, one that is not aligned, strided x, x used twice, the gradient of a gradient, none at all."""
+    rng, rope, x, _, pd = rope_case(rc)
+    ones = torch.ones_like(x)
+    back = rc.rc_rope_axes(ones, pd, rope, inverse=True)
+    (dx,) = torch.autograd.grad(rc.rc_rope_axes(x, pd, rope).sum(), x)
+    assert torch.equal(dx, back)
+    flat = torch.ones(x.numel() + 1, device="cuda")[1:].view(x.shape)
+    assert flat.data_ptr() % 16
+    (dx,) = torch.autograd.grad(rc.rc_rope_axes(x, pd, rope), x, flat)
+    assert torch.equal(dx, back)
+    fused = torch.zeros((x.shape[0], 8, 64), device="cuda", requires_grad=True)
+    rc.rc_rope_axes(fused[:, 2:5], pd, rope).sum().backward()
+    assert torch.equal(fused.grad[:, 2:5], back) and not fused.grad[:, :2].any() and not fused.grad[:, 5:].any()
+    (dx,) = torch.autograd.grad(rc.rc_rope_axes(x, pd, rope).sum() + rc.rc_rope_axes(x, pd, rope).sum(), x)
+    assert torch.equal(dx, 2 * back)
+    y = rc.rc_rope_axes(x, pd, rope)
+    (dx,) = torch.autograd.grad((y * y).sum() / 2, x, create_graph=True)   # x itself, but for roundings
+    (ddx,) = torch.autograd.grad(dx.sum(), x)
+    assert (ddx - 1).abs().max() <= 2.0 ** -18
+    with torch.no_grad():
+        assert not rc.rc_rope_axes(x, pd, rope).requires_grad
+    assert not rc.rc_rope_axes(x.detach(), pd, rope).requires_grad
+
+
+def test_rope_axes_gradient_on_another_stream_and_in_a_graph(rc):  # noqa: F811
+    rng, rope, x, _, pd = rope_case(rc, n=4000, heads=8)
+    dy = dev(rng.standard_normal(x.shape).astype(np.float32))
+    back = rc.rc_rope_axes(dy, pd, rope, inverse=True)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    y = rc.rc_rope_axes(x, pd, rope, stream=stream)
+    torch.cuda.current_stream().wait_stream(stream)
+    (dx,) = torch.autograd.grad(y, x, dy)
+    torch.cuda.synchronize()
+    assert torch.equal(dx, back)
+    del y, dx
+    leaf = x.detach().clone().requires_grad_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (dx,) = torch.autograd.grad(rc.rc_rope_axes(leaf, pd, rope), leaf, dy)
+    dy.mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dx, 2 * back)
+
+
+def test_rope_axes_refuses_to_lose_a_gradient(rc):  # noqa: F811
+    _, rope, x, _, pd = rope_case(rc)
+    out = torch.zeros_like(x)
+    for a, b in ((x, out.detach()), (x.detach(), out.detach().requires_grad_()), (x * 1, None)):
+        with pytest.raises(RuntimeError):
+            y = a if b is None else b
+            rc.rc_rope_axes(a, pd, rope, out=y)
+    with torch.no_grad():
+        rc.rc_rope_axes(x, pd, rope, out=out)
+    pos = pd.clone()
+    y = rc.rc_rope_axes(x, pos, rope)
+    pos += 1  # the positions of the turn back: autograd notices
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
