@@ -291,11 +291,17 @@ class PagedKVCache:
             _filled(self.device)
 
     @classmethod
-    def empty(cls, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda") -> "PagedKVCache":
+    def empty(cls, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda",
+              workspace=None) -> "PagedKVCache":
+        """New zeroed pages.  Caches whose calls are issued on one stream (a model's layers) can share a workspace:
+        pass the first one's `workspace`; each has one of its own (RC_PAGED_WORKSPACE_BYTES, 64 MB) otherwise."""
         def new(*shape):
             return torch.zeros(shape, dtype=torch.uint8, device=device)
-        return cls(new(pages, kv_heads, page_tokens, head_dim), new(pages, kv_heads, head_dim, page_tokens),
-                   new(pages, kv_heads, page_tokens), new(pages, kv_heads, page_tokens))
+        cache = cls(new(pages, kv_heads, page_tokens, head_dim), new(pages, kv_heads, head_dim, page_tokens),
+                    new(pages, kv_heads, page_tokens), new(pages, kv_heads, page_tokens), workspace)
+        if workspace is not None:
+            _filled(cache.device)
+        return cache
 
     def _batch(self, batch: PagedBatch):
         if batch.device != self.device:

@@ -59,6 +59,35 @@ def test_empty_pages_are_ready_for_any_stream(rc):  # noqa: F811
         assert torch.equal(getattr(cache, x), getattr(plain, x)), x
 
 
+def test_layers_share_a_workspace(rc):  # noqa: F811
+    """Caches of `empty` with one workspace, called in turn on one stream, and ready for any: the bits of separate ones."""
+    st = Setup(rc, [(1, 5000), (90, 700)], 2, 64, 16, seed=10)
+    n, pages, rope = st.tokens, st.cache.pages, rc.RopeAxes((32,))
+    k, q = bf16(st.rng, n, 2, 64).cuda(), bf16(st.rng, n, 4, 64).cuda()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    stream = torch.cuda.Stream()
+    keys = [k * (layer + 1) for layer in range(3)]
+    res = []
+    for shared in (False, True):
+        caches = []
+        torch.cuda.synchronize()
+        for layer in range(3):
+            torch.cuda._sleep(BUSY // 10)
+            caches.append(rc.PagedKVCache.empty(pages, 2, 64, 16, workspace=caches[0].workspace if shared and caches else None))
+            caches[-1].write(st.batch, keys[layer], k, pos, rope, stream=stream)
+            torch.cuda.synchronize()
+        assert len({c.workspace.data_ptr() for c in caches}) == (1 if shared else 3)
+        for c in caches:
+            out, lse = torch.zeros_like(q), torch.zeros((n, 4), device="cuda")
+            c.attend(st.batch, q, out, lse=lse)
+            res.append((c.kcodes, c.vcodes, out, lse))
+        torch.cuda.synchronize()
+    for a, b in zip(res[:3], res[3:]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    with pytest.raises(ValueError):
+        rc.PagedKVCache.empty(4, 2, 64, 16, workspace=caches[0].workspace[1:])
+
+
 def test_a_cache_built_inside_a_capture(rc):  # noqa: F811
     """Its fill is a part of the graph."""
     st = Setup(rc, [(1, 3000)], 2, 64, 16, seed=3)
