@@ -4,8 +4,8 @@
 // new tokens x the query heads that share it): bound by reading the codes, so
 // the warps read them straight into the registers where the matrix
 // instructions want them, with no shared memory and no barrier on the way.
-// A block has one (sequence, KV head, tile of 8 or 16 rows, split of the cached
-// tokens); a warp takes 64 cached tokens at a time, transposed, so that the few
+// A block has one (sequence, KV head, split of the cached tokens) and all its rows, 8
+// or 16 at most; a warp takes 64 cached tokens at a time, transposed, so that the few
 // rows are the short side of the products (m16n8k16):
 //   S^T = K Q^T  in fp16: one conversion makes two codes exact fp16 numbers, the
 //                rows of Q are scaled to fp16's range, and the tokens' scales
@@ -23,8 +23,8 @@
 // now take 98.5 us: 544 MB, 0.81 of the rate of a copy.  The rest is the start
 // and end of the blocks, and warps that hold too much to be more on an SM.
 // The warps' (max, sum, O) are joined through shared memory; with several
-// splits they go to the workspace, and the block that arrives last at its row
-// tile's counter joins them in split order, so results do not depend on timing.
+// splits they go to the workspace, and the block that arrives last at its counter
+// joins them in split order, so results do not depend on timing.
 #include <algorithm>
 
 #include "rc_paged.cuh"
@@ -38,7 +38,7 @@ constexpr int kRowsThreads = kRowsWarps * 32;
 constexpr int kChunk = 64;      // cached tokens of a warp's step
 constexpr int kMaxSplits = 32;  // of a sequence
 
-// One split's result for a row tile of 8 NR rows in the workspace: O [rows][D],
+// One split's result for 8 NR rows in the workspace: O [rows][D],
 // then max and sum [rows] each.
 template <int D, int NR>
 constexpr int part_floats() {
@@ -49,7 +49,7 @@ constexpr int part_floats() {
 // log2 units; -inf: the partial saw nothing).
 __device__ __forceinline__ float join_weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
 
-// 8 NR rows a block (NR 1 or 2).
+// 8 NR rows (NR 1 or 2).
 template <int D, int NR>
 __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kernel(PagedAttnParams p) {
     constexpr int kRowTile = 8 * NR;
@@ -60,16 +60,13 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
     __shared__ int last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int split = blockIdx.x, h = blockIdx.y % p.g.kv_heads, tile = blockIdx.y / p.g.kv_heads, s = blockIdx.z;
+    const int split = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
     const Seq q = load_seq(p.g, s);
-    const int rows = q.n * p.group;
-    if (tile * kRowTile >= rows) return;
-    // tokens that the tile's last row sees
-    const int last_new = min(q.n - 1, (tile * kRowTile + kRowTile - 1) / p.group);
-    const int seen = p.causal ? max(0, q.kv - q.n + last_new + 1) : q.kv;
-    const int nsplit = max(1, (seen + p.split_tokens - 1) / p.split_tokens);
+    const int rows = q.n * p.group;  // at most kRowTile, as max_new new tokens have
+    if (rows == 0) return;
+    const int nsplit = max(1, (q.kv + p.split_tokens - 1) / p.split_tokens);  // (the last row sees every token)
     if (split >= nsplit) return;
-    const int j0 = split * p.split_tokens, j1 = min(seen, j0 + p.split_tokens);
+    const int j0 = split * p.split_tokens, j1 = min(q.kv, j0 + p.split_tokens);
 
     uint32_t qb[NR][D / 16][2];
     float qscale[NR][2];
@@ -81,7 +78,7 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
         bool live[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            const int rr = tile * kRowTile + 8 * r + g;
+            const int rr = 8 * r + g;
             live[r] = rr < rows;
             const int tok = live[r] ? rr / p.group : 0, head = h * p.group + (live[r] ? rr - tok * p.group : 0);
             qrow[r] = p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D;
@@ -91,10 +88,8 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
         }
         query_tile_f16<D, NR>(qrow, live, p.sm_log2, qb, qscale);
     }
-    int least = j1;  // what every row sees
-#pragma unroll
-    for (int r = 0; r < NR; ++r) least = min(least, min(limit[r][0], limit[r][1]));
-    least = __reduce_min_sync(0xffffffffu, least);
+    // what every row sees
+    const int least = min(j1, p.causal ? max(0, q.kv - q.n + 1) : q.kv);
 
     float o[NR][MT][4];
     float m_run[NR][2], l_run[NR][2];
@@ -322,11 +317,10 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
             }
         }
     __syncthreads();
-    const int rows_here = min(kRowTile, rows - tile * kRowTile);
-    const int slot = (s * p.row_tiles + tile) * p.g.kv_heads + h;
+    const int slot = s * p.g.kv_heads + h;
     float* part = p.part + static_cast<size_t>(slot) * p.splits * part_floats<D, NR>();
     auto store_out = [&](int r, int d, float4 v, float M, float L) {
-        const int rr = tile * kRowTile + r, tok = rr / p.group, head = h * p.group + rr - tok * p.group;
+        const int tok = r / p.group, head = h * p.group + r - tok * p.group;
         const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // a sum that is not a number stays one
         *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q.q0 + tok) * p.out_stride +
                                   static_cast<int64_t>(head) * D + d) =
@@ -335,7 +329,7 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
             p.lse[static_cast<int64_t>(q.q0 + tok) * p.heads + head] =
                 L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     };
-    for (int i = tid; i < rows_here * (D / 4); i += kRowsThreads) {
+    for (int i = tid; i < rows * (D / 4); i += kRowsThreads) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         float M = -INFINITY;
 #pragma unroll
@@ -386,7 +380,7 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
         for (int i = 0; i < K; ++i) {
             const int k = k0 + i * kLanes;
             const float* b = part + static_cast<size_t>(k) * part_floats<D, NR>() + kRowTile * D + r;
-            const bool have = k < nsplit && r < rows_here;
+            const bool have = k < nsplit && r < rows;
             m[i] = have ? __ldcg(b) : -INFINITY;
             l[i] = have ? __ldcg(b + kRowTile) : 0.f;
             M = fmaxf(M, m[i]);
@@ -407,7 +401,7 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
         }
     }
     __syncthreads();
-    for (int i = tid; i < rows_here * (D / 4); i += kRowsThreads) {
+    for (int i = tid; i < rows * (D / 4); i += kRowsThreads) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         const float* from = part + r * D + d;
@@ -433,10 +427,7 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
 
 template <int D, int NR>
 cudaError_t launch_rows(PagedAttnParams& p, size_t part_floats_max, int max_counters, cudaStream_t s) {
-    const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
-    p.row_tiles = static_cast<int>((rows + 8 * NR - 1) / (8 * NR));
-    const int64_t slots = static_cast<int64_t>(p.g.seqs) * p.row_tiles * p.g.kv_heads;
-    if (static_cast<int64_t>(p.row_tiles) * p.g.kv_heads > 65535) return cudaErrorInvalidValue;
+    const int64_t slots = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
     // Splits: sixteen blocks an SM, which evens out sequences of different
     // lengths (8 query heads' groups of 6 x 32 sequences of 61 to 16,381 tokens:
     // 6 blocks an SM 119 us, 12 102, 16 99, 24 101, 48 106), at most 32, which
@@ -457,7 +448,7 @@ cudaError_t launch_rows(PagedAttnParams& p, size_t part_floats_max, int max_coun
     const int per = static_cast<int>((p.g.max_kv + want - 1) / want);
     p.split_tokens = std::max(step, (per + step - 1) / step * step);
     p.splits = std::max(1, (p.g.max_kv + p.split_tokens - 1) / p.split_tokens);
-    dim3 grid(p.splits, p.row_tiles * p.g.kv_heads, p.g.seqs);
+    dim3 grid(p.splits, p.g.kv_heads, p.g.seqs);
     paged_rows_kernel<D, NR><<<grid, kRowsThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
