@@ -87,11 +87,12 @@ struct StWork {
         return j - old < n ? (j - old) * group : rows;
     }
     __device__ __forceinline__ int first_tile(int rb, int i) const {
+        if (!CAUSAL) return rb * per;
         return max(rb * per, first_row(j0 + i * kStTile) / kStTile);
     }
     __device__ __forceinline__ int end_tile(int rb) const { return min(tiles, rb * per + per); }
     __device__ __forceinline__ bool has(int rb, int i) const {
-        return first_row(j0 + i * kStTile) < rows && first_tile(rb, i) < end_tile(rb);
+        return !CAUSAL || (first_row(j0 + i * kStTile) < rows && first_tile(rb, i) < end_tile(rb));
     }
 };
 
@@ -322,12 +323,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutSoftmax);
             for (int i = 0; i < w.ktiles && ok; i += 2) {
                 const int jt = j0 + i * kStTile, j = jt + quad * 32 + lane;  // the pair's first token, the thread's first
-                if (!w.has(rb, i)) {
-                    // no row of any block sees the pair
-                    if (rb == 0 && g == 0 && w.first_row(jt) >= w.rows)
-                        for (int a = j; a < min(w.end, jt + kStPair); a += kStTile) p.out[row_at + a] = p.scores[row_at + a];
-                    continue;
-                }
+                if (!w.has(rb, i)) continue;
                 float next_old[2] = {0.f, 0.f};
                 if (mine == 0) {
                     // the first block of rows that sees the tile starts from the given scores
