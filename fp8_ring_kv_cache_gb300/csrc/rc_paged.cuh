@@ -316,6 +316,17 @@ struct RopeAxesParams {
     int heads, inverse;
 };
 
+// Blocks in the x of a grid, from what the host was told.
+constexpr int kWriteRun = 16;    // cached tokens of a block of the write: the alignment of a V row's piece
+constexpr int kAttendRows = 256; // query rows of a block of the tcgen05 attention
+inline int64_t paged_write_runs(const PagedParams& g) {  // that max_new tokens can touch, wherever the first one lies
+    return (static_cast<int64_t>(g.max_new) + kWriteRun - 2) / kWriteRun + 1;
+}
+inline int64_t paged_write_blocks(const PagedParams& g) { return g.seqs * paged_write_runs(g); }
+inline int64_t paged_attend_blocks(const PagedParams& g, int64_t rows) {
+    return (rows + kAttendRows - 1) / kAttendRows * g.seqs * g.kv_heads;
+}
+
 cudaError_t launch_rope_axes(const RopeAxesParams& p, int D, int dtype, cudaStream_t s);
 cudaError_t launch_paged_write(const PagedWriteParams& p, int D, cudaStream_t s);
 cudaError_t launch_paged_attention(PagedAttnParams& p, int D, size_t part_floats, int max_counters, cudaStream_t s);

@@ -14,6 +14,7 @@ namespace {
 
 constexpr size_t kStatusBytes = 256;
 constexpr int kCounters = 16384;
+constexpr int64_t kMaxBlocks = 0x7fffffff;  // of a grid's x
 constexpr size_t kPartOff = kStatusBytes + sizeof(int) * kCounters;
 
 std::atomic<uint64_t> g_wait_ns{2000000000ull};
@@ -191,6 +192,7 @@ int rc_paged_write(const rc_paged_view* view, const rc_paged_batch* batch, const
     if (!K_bf16 || !V_bf16 || !positions || !aligned16(K_bf16) || !aligned16(V_bf16)) return RC_ERR_ARG;
     const int64_t row = static_cast<int64_t>(view->kv_heads) * view->head_dim;
     if (!stride_ok(k_stride, row, 8) || !stride_ok(v_stride, row, 8) || pos_stride < p.g.tokens) return RC_ERR_ARG;
+    if (paged_write_blocks(p.g) > kMaxBlocks) return RC_ERR_UNSUPPORTED;
     st = ready();
     if (st != RC_OK) return st;
     copy_plan(&p.rope, plan);
@@ -215,7 +217,8 @@ int rc_paged_attend(const rc_paged_view* view, const rc_paged_batch* batch, cons
     const int64_t row = static_cast<int64_t>(heads) * view->head_dim;
     if (!stride_ok(q_stride, row, 8) || !stride_ok(out_stride, row, 8)) return RC_ERR_ARG;
     if (meet({Q_bf16, q_stride, p.g.tokens, row}, {out_bf16, out_stride, p.g.tokens, row}, 2)) return RC_ERR_ARG;
-    if (static_cast<int64_t>(p.g.max_new) * (heads / view->kv_heads) > (1 << 30)) return RC_ERR_UNSUPPORTED;
+    const int64_t rows_of_head = static_cast<int64_t>(p.g.max_new) * (heads / view->kv_heads);
+    if (rows_of_head > (1 << 30) || paged_attend_blocks(p.g, rows_of_head) > kMaxBlocks) return RC_ERR_UNSUPPORTED;
     st = ready();
     if (st != RC_OK) return st;
     p.q = static_cast<const __nv_bfloat16*>(Q_bf16);

@@ -522,8 +522,8 @@ cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
     const int64_t tiles = (p.g.max_kv + kStTile - 1) / kStTile;
     const int64_t ranges = std::min<int64_t>((tiles + 1) / 2, std::max<int64_t>(1, 152 / lists));
     const int range = static_cast<int>((tiles + ranges - 1) / ranges) * kStTile;
+    // (one range a list from 152 lists on: at most 65,535 x 1,024)
     const int64_t blocks = (p.g.max_kv + range - 1) / range * lists;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     paged_scores_tc_kernel<D, CAUSAL><<<static_cast<unsigned>(blocks), kStThreads, smem, s>>>(p, range);
     return cudaGetLastError();
 }

@@ -43,6 +43,7 @@ namespace {
 constexpr int kTcThreads = 640;
 constexpr int kTileM = 128, kTileN = 128;
 constexpr int kRowsTc = 2 * kTileM;
+static_assert(kRowsTc == kAttendRows, "the blocks that the host counts");
 constexpr int kWgSoftmax0 = 1, kWgConvertK = 3;
 constexpr uint32_t kTcTmem = 512;
 
@@ -685,8 +686,7 @@ cudaError_t launch_d(PagedAttnParams& p, size_t part_floats_max, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
     p.row_tiles = static_cast<int>((rows + kRowsTc - 1) / kRowsTc);
-    const int64_t blocks = static_cast<int64_t>(p.row_tiles) * p.g.seqs * p.g.kv_heads;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const int64_t blocks = paged_attend_blocks(p.g, rows);
     // Splits: while there are fewer blocks than SMs, down to four KV tiles
     // each (a block's set-up and the join take as long as a few tiles), as many
     // as the workspace holds.  One sequence of 8,000 tokens x 8 KV heads x 128

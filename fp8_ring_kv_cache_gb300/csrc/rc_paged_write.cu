@@ -24,7 +24,7 @@ namespace rc {
 
 namespace {
 
-constexpr int kRun = 16;  // tokens of a block: the alignment of a V row's piece
+constexpr int kRun = kWriteRun;
 
 // Exponent of the row's scale and its byte, from the largest magnitude as bits:
 // infinities and NaNs are above every number.  open: whether that is within 8 units of
@@ -250,10 +250,8 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged_write_kernel(cons
 
 template <int D>
 cudaError_t launch_d(const PagedWriteParams& p, cudaStream_t s) {
-    // runs that max_new tokens can touch, wherever the first one lies
-    const int runs = (p.g.max_new + kRun - 2) / kRun + 1;
-    const int64_t blocks = static_cast<int64_t>(p.g.seqs) * runs;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const int runs = static_cast<int>(paged_write_runs(p.g));
+    const int64_t blocks = paged_write_blocks(p.g);
     // Heads of a block: two, which share the angles and overlap one's loads with
     // the other's work, four when those still fill the card three times (757
     // tokens x 48 heads x 128: one head 19.3 us, two 16.6, four 15.9, eight 19.7;

@@ -433,7 +433,10 @@ int rc_rope_axes(const rc_rope_plan *plan, const void *x, int64_t x_stride, void
  *       of the token-major tensors; its n new tokens are the last n of its
  *       kv_len.  Rows outside every sequence are not touched.
  * max_new and max_kv (host) bound every sequence's n and kv_len; tokens (host) is the
- * row count of the tensors.  Metadata out of these bounds (or a page id that
+ * row count of the tensors.  They size the launches for the largest sequence: where
+ * that takes more than 2^31 - 1 blocks (seqs x max_new / 16 of a write, seqs x
+ * kv_heads x a KV head's query rows / 256 of an attention) a call is refused
+ * (RC_ERR_UNSUPPORTED).  Metadata out of these bounds (or a page id that
  * is not one of the pool's) is found on the device: the sequence (or page) is
  * left out, nothing is read or written out of bounds, and rc_paged_status
  * reports RC_ERR_ARG; that call's results are not valid.

@@ -82,3 +82,13 @@ def test_evict_refuses_scores_over_each_other(rc):  # noqa: F811
     vp, bp = ctypes.addressof(v), ctypes.addressof(b)
     for out, stride in ((A, 60), (A + 4 * 359, 60), (A - 4 * 47, 60), (A + 4 * 60, 100)):
         assert rc.lib.rc_paged_evict(vp, bp, A, stride, 8, 2, A, 1, A, A, out, None) == rc.RC_ERR_ARG, (out - A, stride)
+
+
+def test_calls_that_take_more_blocks_than_a_grid_has(rc):  # noqa: F811
+    """65,535 sequences of which one may have all the rows."""
+    most = 2 ** 31 - 1
+    v, b = structs(rc, None, dict(seqs=65535, tokens=most, max_new=most))
+    assert calls(rc, v, b, ps=most)["write"]() == rc.RC_ERR_UNSUPPORTED
+    assert calls(rc, v, b, out=A + (1 << 45), heads=2, qs=128, os=128)["attend"]() == rc.RC_ERR_UNSUPPORTED   # rows of a head
+    v, b = structs(rc, dict(kv_heads=1024), dict(seqs=65535, tokens=1 << 20, max_new=1 << 14))
+    assert calls(rc, v, b, out=A + (1 << 45), heads=1024, qs=65536, os=65536)["attend"]() == rc.RC_ERR_UNSUPPORTED
