@@ -16,7 +16,9 @@
 //                the B operand of
 //   O^T += V^T P^T  in bf16, whose A operand is a 16-byte piece of a V row: 16
 //                tokens of one dim, with their scales (which fp16 could not
-//                hold).  The tokens of S's rows are chosen to match.
+//                hold).  The tokens of S's rows are chosen to match.  P is rounded
+//                to bf16 for it (the row sums are not): at most 2^-8 of each weight
+//                beside the 2^-8 of the bf16 result.
 // Rows first (S = Q K^T) took twice the products and as many moves to keep the
 // unused half of the accumulators in place: 134 us for 32 single tokens
 // (sequences of 61 to 16,381 tokens, 8 KV heads x 6 query heads x 128), which
@@ -459,7 +461,7 @@ cudaError_t launch_attention_d(PagedAttnParams& p, size_t part_floats_max, int m
     // Up to 16 rows per KV head the reading of the codes is what counts; with
     // more, each tile of 16 would read them again, and the tcgen05 kernel, whose
     // time hardly grows up to 128 rows, is the faster one (32 sequences x 8,000
-    // tokens x 8 KV heads x 128: 8 rows 97 against 245 us, 16 rows 126 against
+    // tokens x 8 KV heads x 128: 8 rows 97 against 245 us, 16 rows 122 against
     // 245).  Tiles of 8 rows save half the products (the same with 1 row: 95 us as
     // a tile of 8, 124 us as one of 16).
     if (rows <= 8) return launch_rows<D, 1>(p, part_floats_max, max_counters, s);

@@ -287,11 +287,12 @@ cudaError_t launch_d(const PagedScoreParams& p, cudaStream_t s) {
 cudaError_t launch_paged_scores(const PagedScoreParams& p, int D, cudaStream_t s) {
     // Up to two row tiles of 16, while there is not much to read, the kernels here
     // are done before the tcgen05 kernel has set itself up (8 KV heads x 128, 32
-    // rows: one sequence of 300 tokens 5.2 against 7.8 us, 8,000 tokens 9.8
-    // against 10.5, 64 sequences of 300 19 against 34); then its conversion of K
-    // keeps up better (one sequence of 60,000 tokens 42 against 33, 32 sequences
-    // of 8,000 163 against 146; 16 of 1,000 the same).  With more rows each tile
-    // costs another pass here (one sequence of 8,000, 64 rows: 13.2 against 11.4).
+    // rows: one sequence of 300 tokens 4.5 against 7.7 us, 8,000 tokens 8.9
+    // against 10.3, 64 sequences of 300 19 against 34); then its conversion of K
+    // keeps up better (one sequence of 60,000 tokens 41 against 33, 32 sequences
+    // of 8,000 162 against 145; 16 of 1,000 14.5 against 15.1).  With more rows each
+    // tile costs another pass here (one sequence of 8,000, 64 rows: 12.8 against
+    // 10.6; 32 of 8,000, 128 rows: 401 against 146).
     const int64_t lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
     const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
     const bool much = p.g.max_kv > 4096 && lists * p.g.max_kv > (1 << 17);

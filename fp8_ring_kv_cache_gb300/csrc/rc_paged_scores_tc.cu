@@ -14,7 +14,8 @@
 //                  to the groups in turn; a group's sums of a pair of K tiles are put in
 //                  shared memory, and the groups take turns in adding the three
 //                  up, always in the same order: no two threads add to one entry.
-//                  They also bring the query rows (by cp.async).
+//                  They also bring the query rows (by cp.async), and zeros in the place of
+//                  those whose lse is -infinity: whatever they hold adds nothing.
 //   warps 16 .. 23 read K's codes from the pages (a warpgroup's next tile is in its
 //                  registers), make them bf16 (exactly: scales are powers of two)
 //                  and put them in TMEM, a tile a warpgroup
@@ -22,7 +23,7 @@
 // queries once per block: keeping K instead would read them for every 128
 // tokens (430 MB of cache traffic for 757 x 5,788 tokens x 48 heads).
 //
-// 757 queries x 5,788 tokens x 48 heads x 128: 57.4 us, 0.94 PFLOP/s, half of
+// 757 queries x 5,788 tokens x 48 heads x 128: 57.8 us, 0.93 PFLOP/s, half of
 // what a library product of bf16 matrices reaches.  Of the 126,000 cycles of a
 // block 12,000 bring the queries; then a unit takes 1,000 where its product needs
 // 530 and its exponentials 510: bound by the chain of a group (wait for the

@@ -497,6 +497,8 @@ int rc_paged_write(const rc_paged_view *view, const rc_paged_batch *batch, const
  * lse (may be NULL) is fp32 [tokens][heads], the natural logarithm of the sum
  * of exp(scores).  A query that sees nothing gets zeros and lse = -infinity.
  * heads must be a multiple of kv_heads; out must share no element with Q (RC_ERR_ARG).
+ * Up to 16 rows per KV head, here and in rc_paged_accumulate, a row of Q is held in
+ * fp16 relative to its largest value: what lies under 2^-32 of that loses bits.
  */
 int rc_paged_attend(const rc_paged_view *view, const rc_paged_batch *batch, const void *Q_bf16, int64_t q_stride,
                     int heads, void *out_bf16, int64_t out_stride, float *lse, int causal, void *stream);
