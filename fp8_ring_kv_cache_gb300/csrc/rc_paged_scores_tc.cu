@@ -57,7 +57,7 @@ enum : int {
     S_PART_FULL = 10,  // [4] every group's sums of a pair of K tiles are in place
     S_PART_EMPTY = 14, // [4] they have been added up
     S_Q_FULL = 18,     // the block's query rows are in place
-    S_Q_EMPTY = 19,    // every group is through with them
+    S_Q_EMPTY = 19,    // every group and the product warp are through with them
     S_L_FULL = 20,     // the block's lse are in place
     S_DRAIN = 21,
     S_COUNT = 22
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         }
         mbar_init(&bars[S_Q_FULL], kStSums / 32);
         mbar_init(&bars[S_L_FULL], kStSums / 32);
-        mbar_init(&bars[S_Q_EMPTY], kStSums / 32);
+        mbar_init(&bars[S_Q_EMPTY], kStSums / 32 + 1);
         mbar_init(&bars[S_DRAIN], 1);
         misc[1] = 0u;
         fence_mbar_init();
@@ -213,6 +213,9 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                     }
                     ++kc;
                 }
+                // (a block of rows that sees none of the range has no products: without this the
+                // groups could be two blocks ahead, and the wait above take one phase for another)
+                if (ok && lane == 0) mbar_arrive(&bars[S_Q_EMPTY]);
             }
             // every product has finished before the tensor memory is released
             if (elect_one()) mma_commit(&bars[S_DRAIN]);

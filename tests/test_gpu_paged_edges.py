@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import paged_util as pu
-from test_gpu_paged import Setup, bf16, dev, rc  # noqa: F401 (rc: the fixture)
+from test_gpu_paged import Setup, bf16, check_scores, dev, rc  # noqa: F401 (rc: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -291,6 +291,13 @@ def test_accumulate_rows_switched_off_add_nothing(rc, rows, dim, causal):  # noq
     over = np.argwhere(~nan & ~past & ~(np.abs(got[0] - want) <= tol))
     assert not len(over), [(tuple(i), got[0][tuple(i)], want[tuple(i)], scores[0][tuple(i)], tol[tuple(i)]) for i in over[:5]]
     assert np.array_equal(got[0][:, kv:], scores[0][:, kv:])
+
+
+@pytest.mark.parametrize("seqs", [[(3000, 3000)], [(2500, 3001), (40, 40)]])
+def test_accumulate_row_blocks_that_see_nothing_of_a_range(rc, seqs):  # noqa: F811
+    """A long prompt's last cached tokens, which the first blocks of 768 query rows do not see."""
+    st = Setup(rc, seqs, 1, 64, 16, seed=11)
+    check_scores(st, bf16(st.rng, st.tokens, 2, 64), True)
 
 
 # ------------------------------------------------------------------ accumulate: scores that no cached token has
