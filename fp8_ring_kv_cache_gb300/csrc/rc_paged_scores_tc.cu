@@ -23,7 +23,7 @@
 // queries once per block: keeping K instead would read them for every 128
 // tokens (430 MB of cache traffic for 757 x 5,788 tokens x 48 heads).
 //
-// 757 queries x 5,788 tokens x 48 heads x 128: 57.8 us, 0.93 PFLOP/s, half of
+// 757 queries x 5,788 tokens x 48 heads x 128: 57.2 us, 0.94 PFLOP/s, half of
 // what a library product of bf16 matrices reaches.  Of the 126,000 cycles of a
 // block 12,000 bring the queries; then a unit takes 1,000 where its product needs
 // 530 and its exponentials 510: bound by the chain of a group (wait for the
@@ -56,9 +56,9 @@ enum : int {
     S_S_FREE = 7,      // [3] the group has read them
     S_PART_FULL = 10,  // [4] every group's sums of a pair of K tiles are in place
     S_PART_EMPTY = 14, // [4] they have been added up
-    S_Q_FULL = 18,     // the block's query rows are in place
+    S_Q_FULL = 18,     // the block's query rows and their lse are in place
     S_Q_EMPTY = 19,    // every group and the product warp are through with them
-    S_L_FULL = 20,     // the block's lse are in place
+    S_Q_READY = 20,    // queries of rows that add nothing are zeros
     S_DRAIN = 21,
     S_COUNT = 22
 };
@@ -109,13 +109,23 @@ __device__ __noinline__ float checked_sum(float sum, const float* minus, const S
     return 0.f;
 }
 
+// Zeros in the place of the queries of rows st and st + kStSums, if they add nothing.
+template <int D>
+__device__ __noinline__ void zero_queries(uint8_t* smem, const float* minus, int st, int rows) {
+    for (int row = st; row < rows; row += kStSums)
+        if (minus[row] == -INFINITY)
+            for (int k = 0; k < D / 8; ++k)
+                *reinterpret_cast<uint4*>(smem + StLayout<D>::kQ + (row >> 7) * StLayout<D>::kTile + bktile_off(row & 127, 8 * k)) =
+                    make_uint4(0, 0, 0, 0);
+}
+
 template <int D, bool CAUSAL>
 __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedScoreParams p, int range) {
     using Lay = StLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
-    uint32_t* misc = reinterpret_cast<uint32_t*>(smem + Lay::kMisc);  // [0] tmem, [1] abort
+    uint32_t* misc = reinterpret_cast<uint32_t*>(smem + Lay::kMisc);  // [0] tmem, [1] abort, [2], [3] zeros are to be put
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, quad = warp & 3;
     int b = blockIdx.x;
     const int h = b % p.g.kv_heads;
@@ -156,10 +166,10 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             mbar_init(&bars[S_PART_EMPTY + i], 4);
         }
         mbar_init(&bars[S_Q_FULL], kStSums / 32);
-        mbar_init(&bars[S_L_FULL], kStSums / 32);
+        mbar_init(&bars[S_Q_READY], kStSums / 32);
         mbar_init(&bars[S_Q_EMPTY], kStSums / 32 + 1);
         mbar_init(&bars[S_DRAIN], 1);
-        misc[1] = 0u;
+        misc[1] = misc[2] = misc[3] = 0u;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             bool ok = true;
             int kc = 0, place = 0, phase = 0;  // K tiles; the unit's place and how often it was used before
             for (int rb = 0; rb < w.blocks && ok; ++rb) {
-                ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutMma);
+                ok = warp_wait(&bars[S_Q_READY], rb & 1, ab, kDevTimeoutMma);
                 for (int i = 0; i < w.ktiles && ok; ++i) {
                     if (!w.has(rb, i)) continue;
                     const int q0 = w.first_tile(rb, i), q1 = w.end_tile(rb), buf = kc & 1;
@@ -271,17 +281,6 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
             if (!ok) break;
             constexpr int kPieces = D / 8, kRows = kStSums / kPieces;
             const int first = rb * w.per * kStTile, count = (w.end_tile(rb) - rb * w.per) * kStTile;
-            float lse[2];  // of rows st and st + kStSums; rows past the last, and rows that saw nothing, add nothing
-            static_assert(kStQTiles * kStTile == 2 * kStSums, "two rows a thread");
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int rw = first + st + x * kStSums;
-                lse[x] = INFINITY;
-                if (rw < w.rows) {
-                    const int tok = rw / p.group, head = h * p.group + rw - tok * p.group;
-                    lse[x] = __ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head);
-                }
-            }
 #pragma unroll 4
             for (int row = st / kPieces; row < count; row += kRows) {
                 const int rw = first + row, tok = p.group == 1 ? rw : rw / p.group, head = h * p.group + rw - tok * p.group;
@@ -291,40 +290,35 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
                 cp_async16_or_zero(smem + Lay::kQ + (row >> 7) * Lay::kTile + bktile_off(row & 127, 8 * (st % kPieces)),
                                    src + 8 * (st % kPieces), have);
             }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float m = -lse[x] * 1.4426950408889634f;
-                if (m == INFINITY) m = -INFINITY;
-                if (st + x * kStSums < count) minus[st + x * kStSums] = m;
+            // Queries of rows that add nothing (lse -infinity) become zeros, as what they hold
+            // may not be numbers.  Whether there are such rows is known once every warp's are
+            // in place (word rb & 1; the other is free until the next block of rows).
+            volatile uint32_t* marks = misc + 2;
+            for (int row = st; row < count; row += kStSums) {
+                const int rw = first + row;
+                float m = -INFINITY;  // rows past the last, and rows that saw nothing, add nothing
+                if (rw < w.rows) {
+                    const int tok = rw / p.group, head = h * p.group + rw - tok * p.group;
+                    m = -__ldg(p.lse + static_cast<int64_t>(q.q0 + tok) * p.heads + head) * 1.4426950408889634f;
+                    if (m == INFINITY) {
+                        m = -INFINITY;
+                        marks[rb & 1] = 1u;
+                    }
+                }
+                minus[row] = m;
             }
-            // Queries of rows that add nothing (lse -infinity) are brought as zeros, as what
-            // they hold may not be numbers: each thread's own pieces, once they are there and
-            // every warp has put its rows' lse in place.
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[S_L_FULL]);
-            ok = warp_wait(&bars[S_L_FULL], rb & 1, ab, kDevTimeoutSoftmax);
-            const int last_row = min(count, w.rows - first);
-            bool off = false;
-#pragma unroll 2
-            for (int row = 4 * lane; row < count; row += kStTile) {
-                const float4 m = *reinterpret_cast<const float4*>(minus + row);
-                off |= (m.x == -INFINITY && row < last_row) || (m.y == -INFINITY && row + 1 < last_row) ||
-                       (m.z == -INFINITY && row + 2 < last_row) || (m.w == -INFINITY && row + 3 < last_row);
-            }
-            off = __any_sync(0xffffffffu, off);
             cp_async_wait_all();
-            if (!ok) break;
-            if (off) {
-#pragma unroll 1
-                for (int row = st / kPieces; row < count; row += kRows)
-                    if (minus[row] == -INFINITY)
-                        *reinterpret_cast<uint4*>(smem + Lay::kQ + (row >> 7) * Lay::kTile +
-                                                  bktile_off(row & 127, 8 * (st % kPieces))) = make_uint4(0, 0, 0, 0);
-            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[S_Q_FULL]);
             ok = warp_wait(&bars[S_Q_FULL], rb & 1, ab, kDevTimeoutSoftmax);
+            if (ok && marks[rb & 1] != 0u) {
+                zero_queries<D>(smem, minus, st, min(count, w.rows - first));
+                fence_async_smem();
+            }
+            if (st == 0) marks[(rb & 1) ^ 1] = 0u;
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&bars[S_Q_READY]);
             for (int i = 0; i < w.ktiles && ok; i += 2) {
                 const int jt = j0 + i * kStTile, j = jt + quad * 32 + lane;  // the pair's first token, the thread's first
                 if (!w.has(rb, i)) continue;

@@ -293,6 +293,29 @@ def test_accumulate_rows_switched_off_add_nothing(rc, rows, dim, causal):  # noq
     assert np.array_equal(got[0][:, kv:], scores[0][:, kv:])
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_accumulate_rows_switched_off_in_some_blocks_of_rows(rc, causal):  # noqa: F811
+    """3,000 rows are brought in four blocks of 768: rows are off in the second and the fourth of them, or in the first."""
+    for where in ((800, 900, 2400, 2500), (10, 11)):
+        st = Setup(rc, [(1500, 1600)], 1, 64, 16, seed=len(where))
+        q = bf16(st.rng, 1500, 2, 64)
+        _, lse = st.attend(q.cuda(), causal)
+        off = np.zeros(3000, bool)
+        for a, b in zip(where[::2], where[1::2]):
+            off[a:b] = True
+        off = torch.from_numpy(off.reshape(1500, 2))
+        lse[off.cuda()] = -np.inf
+        q[off] = float("nan")
+        sc = torch.zeros((1, 1, 1600), device="cuda")
+        st.cache.accumulate(st.batch, q.cuda(), lse, sc, causal=causal)
+        st.cache.sync()
+        qn = np.where(off.numpy()[..., None], 0.0, q.float().numpy())
+        want = pu.accumulate(st.pool, st.meta, qn, lse.cpu().numpy(), np.zeros((1, 1, 1600), np.float32), causal)
+        big = max(pu.reach(st.pool, st.meta, qn, 0, 0, head) for head in range(2))
+        tol = 2.0 ** -16 * (1 + big) * want + 2.0 ** -24 * 3008 * want + 1e-30
+        assert (np.abs(sc.cpu().numpy() - want) <= tol).all()
+
+
 @pytest.mark.parametrize("seqs", [[(3000, 3000)], [(2500, 3001), (40, 40)]])
 def test_accumulate_row_blocks_that_see_nothing_of_a_range(rc, seqs):  # noqa: F811
     """A long prompt's last cached tokens, which the first blocks of 768 query rows do not see."""
