@@ -20,7 +20,9 @@ the non-FP8 side of the FP8-versus-bf16 cache comparison.
 Caches of many sequences in pages the caller owns, for any number of new tokens and
 grouped query heads (``PagedKVCache``: write, attend, accumulate, evict), and rotary
 positions on several axes with their gradient (``RopeAxes``, ``rc_rope_axes``): see
-``_paged.py``.
+``_paged.py``.  The same cache in 4 bits (``PagedKVCache4``: write, attend) and rotary
+positions in other forms: halves, a part of the head, scaled for long contexts
+(``RopeForm``, ``rc_rope_turn``): see ``_paged4.py``.
 
 Every call is stream-ordered on torch's current stream (or ``stream=``); no
 call after construction allocates device memory.
@@ -38,4 +40,7 @@ from ._binding import (  # noqa: F401
 from ._paged import (  # noqa: F401
     RC_PAGED_WORKSPACE_BYTES, RC_ROPE_SHARED_FREQS, PagedBatch, PagedKVCache, RopeAxes, rc_paged_set_wait_limit,
     rc_rope_axes,
+)
+from ._paged4 import (  # noqa: F401
+    PagedKVCache4, RopeForm, rc_rope_turn,
 )

@@ -187,24 +187,21 @@ class _Turn(torch.autograd.Function):
     """The turn with its gradient, the turn back."""
 
     @staticmethod
-    def forward(ctx, x, positions, rope, inverse):
-        ctx.rope, ctx.inverse = rope, inverse
+    def forward(ctx, x, positions, rope, inverse, turn):
+        ctx.rope, ctx.inverse, ctx.turn = rope, inverse, turn
         ctx.save_for_backward(positions)
-        return rc_rope_axes(x.detach(), positions, rope, inverse=inverse)
+        return turn(x.detach(), positions, rope, None, inverse)
 
     @staticmethod
     def backward(ctx, dy):
         dy = dy.contiguous()  # (a broadcast gradient has no strides that the kernel takes)
         if dy.data_ptr() % 16:
             dy = dy.clone()
-        return rc_rope_axes(dy, ctx.saved_tensors[0], ctx.rope, inverse=not ctx.inverse), None, None, None
+        return ctx.turn(dy, ctx.saved_tensors[0], ctx.rope, None, not ctx.inverse), None, None, None, None
 
 
-def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, stream=None):
-    """x [n][heads][head_dim] (bf16 or fp32) turned at positions (int32 [axes][n]); inverse turns back, which is also
-    the gradient: dx = rc_rope_axes(dy, positions, rope, inverse=True).  out defaults to a new tensor (of the call's
-    stream, kept from reuse for the current one too) and may be x.  Autograd records the call if x requires a gradient;
-    as with torch's own functions, not with out=, which is refused then."""
+def _turned(x, positions, rope, out, inverse, stream, what: str, fn, turn):
+    """What rc_rope_axes and rc_rope_turn do; turn: the one of them that asks."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be a [n][heads][head_dim] tensor")
     if not x.is_cuda:
@@ -216,12 +213,12 @@ def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, 
         raise ValueError(f"x has head_dim {dim}, the plan {rope.head_dim}")
     if torch.is_grad_enabled() and (x.requires_grad or getattr(out, "requires_grad", False)):
         if out is not None:
-            raise RuntimeError("rc_rope_axes: out= is not differentiable, but x or out requires a gradient")
+            raise RuntimeError(f"{what}: out= is not differentiable, but x or out requires a gradient")
         if stream is None:
-            return _Turn.apply(x, positions, rope, inverse)
+            return _Turn.apply(x, positions, rope, inverse, turn)
         own, current = _stream(stream, x.device), torch.cuda.current_stream(x.device)
         with torch.cuda.stream(own):  # (autograd runs the gradient on the stream of the turn)
-            y = _Turn.apply(x, positions, rope, inverse)
+            y = _Turn.apply(x, positions, rope, inverse, turn)
         y.record_stream(current)
         return y
     xp, xs = _rows(x, x.dtype, n, heads, dim, "x", x.device)
@@ -235,9 +232,17 @@ def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, 
         if op < xp + ((n - 1) * xs + row) * size and xp < op + ((n - 1) * os_ + row) * size and \
                 _rows_meet(xp, xs * size, op, os_ * size, n, row * size):
             raise ValueError("out overlaps x without being x")
-    _call(x.device, stream, "rc_rope_axes", lib.rc_rope_axes, rope._ptr, xp, xs, op, os_,
+    _call(x.device, stream, what, fn, rope._ptr, xp, xs, op, os_,
           RC_BF16 if x.dtype == torch.bfloat16 else RC_F32, n, heads, pp, ps, 1 if inverse else 0)
     return out
+
+
+def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, stream=None):
+    """x [n][heads][head_dim] (bf16 or fp32) turned at positions (int32 [axes][n]); inverse turns back, which is also
+    the gradient: dx = rc_rope_axes(dy, positions, rope, inverse=True).  out defaults to a new tensor (of the call's
+    stream, kept from reuse for the current one too) and may be x.  Autograd records the call if x requires a gradient;
+    as with torch's own functions, not with out=, which is refused then."""
+    return _turned(x, positions, rope, out, inverse, stream, "rc_rope_axes", lib.rc_rope_axes, rc_rope_axes)
 
 
 class PagedBatch:

@@ -16,6 +16,14 @@ struct RopePlanDev {
     uint8_t axis[kMaxHalfDim];
 };
 
+// What turns, in which layout, by which axes and frequencies (rc_rope_form).
+struct RopeFormDev {
+    uint64_t turns[RC_ROPE_MAX_HEAD_DIM / 2];
+    uint8_t axis[RC_ROPE_MAX_HEAD_DIM / 2];
+    int head_dim, first, dims, layout;
+    float gain;
+};
+
 // A generic address of a kernel's (__grid_constant__) parameter bytes, whose
 // origin the compiler does not see: lanes that read different entries of an
 // array there go through the data cache together, where the constant bank
@@ -205,15 +213,24 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
         : "r"(w));
 }
 
+// The e of the 2^e that a query row is divided by for fp16: 14 <= log2(amax) - e < 15,
+// e kept where 2^e and 2^-e are normal numbers; rows of zeros, and rows that are not
+// finite, are taken as they are.
+__device__ __forceinline__ int row_exponent(float amax) {
+    const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+    return amax > 0.f && amax <= 3.4028235e38f ? max(-126, min(126, e)) : 0;
+}
+
 // Query rows as the B operand of S^T = K Q^T with K's codes as fp16: 8 rows a
 // tile, row lane / 4 of tile r at row[r].  Each row is divided by a power of two
 // that puts its largest magnitude in [2^14, 2^15), so that bf16's 8 bits are
 // exact in fp16 down to 2^-32 of it (what is smaller loses bits that are nothing
-// beside the row's largest).  Product c * 4 + i of the lane (t = lane % 4) holds
-// dims 16 (t + 4 c) + 4 i + {0, 1} and + {2, 3}, as codes_f16 gives them.
+// beside the row's largest).  The lane (t = lane % 4) has RUN neighbouring dims at a
+// time: product c * RUN / 4 + i holds dims RUN (t + 4 c) + 4 i + {0, 1} and + {2, 3},
+// as codes_f16 gives them.
 // scale[r][x]: that power times `factor` for row 2 t + x of tile r, the rows
 // whose scores the lane gets.
-template <int D, int NR>
+template <int D, int NR, int RUN = 16>
 __device__ __forceinline__ void query_tile_f16(const __nv_bfloat16* const (&row)[NR], const bool (&live)[NR], float factor,
                                                uint32_t (&qb)[NR][D / 16][2], float (&scale)[NR][2]) {
     const int t = threadIdx.x & 3;
@@ -222,25 +239,19 @@ __device__ __forceinline__ void query_tile_f16(const __nv_bfloat16* const (&row)
         uint32_t w[D / 8];
         float amax = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (live[r]) {
-                a = __ldg(reinterpret_cast<const uint4*>(row[r] + 16 * (t + 4 * c)));
-                b = __ldg(reinterpret_cast<const uint4*>(row[r] + 16 * (t + 4 * c) + 8));
-            }
-            const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        for (int c = 0; c < D / 8; c += 4) {  // eight dims
+            uint4 a = make_uint4(0, 0, 0, 0);
+            if (live[r]) a = __ldg(reinterpret_cast<const uint4*>(row[r] + RUN * (t + 4 * (2 * c / RUN)) + 2 * c % RUN));
+            const uint32_t x[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                w[8 * c + i] = x[i];
+            for (int i = 0; i < 4; ++i) {
+                w[c + i] = x[i];
                 amax = max3(amax, fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u)));
             }
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^e with 14 <= log2(amax) - e < 15, e kept where 2^e and 2^-e are normal
-        // numbers; rows of zeros, and rows that are not finite, are taken as they are
-        int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
-        e = amax > 0.f && amax <= 3.4028235e38f ? max(-126, min(126, e)) : 0;
+        const int e = row_exponent(amax);
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         const float mine = factor * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
@@ -259,6 +270,15 @@ __device__ __forceinline__ void query_tile_f16(const __nv_bfloat16* const (&row)
 struct PagedWriteParams {
     PagedParams g;
     RopePlanDev rope;
+    const __nv_bfloat16* K;
+    const __nv_bfloat16* V;
+    const int32_t* pos;
+    int64_t k_stride, v_stride, pos_stride;
+};
+
+struct Paged4WriteParams {
+    PagedParams g;
+    RopeFormDev form;  // dims 0: K is stored as it comes
     const __nv_bfloat16* K;
     const __nv_bfloat16* V;
     const int32_t* pos;
@@ -316,6 +336,15 @@ struct RopeAxesParams {
     int heads, inverse;
 };
 
+struct RopeFormParams {
+    RopeFormDev form;
+    const void* x;
+    void* out;
+    int64_t x_stride, out_stride, pos_stride, n;
+    const int32_t* pos;
+    int heads, back;
+};
+
 // Blocks in the x of a grid, from what the host was told.
 constexpr int kWriteRun = 16;    // cached tokens of a block of the write: the alignment of a V row's piece
 constexpr int kAttendRows = 256; // query rows of a block of the tcgen05 attention
@@ -328,11 +357,15 @@ inline int64_t paged_attend_blocks(const PagedParams& g, int64_t rows) {
 }
 
 cudaError_t launch_rope_axes(const RopeAxesParams& p, int D, int dtype, cudaStream_t s);
+cudaError_t launch_rope_form(const RopeFormParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_paged_write(const PagedWriteParams& p, int D, cudaStream_t s);
 cudaError_t launch_paged_attention(PagedAttnParams& p, int D, size_t part_floats, int max_counters, cudaStream_t s);
 cudaError_t launch_paged_tc(PagedAttnParams& p, int D, size_t part_floats, cudaStream_t s);
 cudaError_t launch_paged_scores(const PagedScoreParams& p, int D, cudaStream_t s);
 cudaError_t launch_paged_scores_tc(const PagedScoreParams& p, int D, cudaStream_t s);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int D, cudaStream_t s);
+cudaError_t launch_paged4_write(const Paged4WriteParams& p, int D, cudaStream_t s);
+cudaError_t launch_paged4_attention(PagedAttnParams& p, int D, size_t part_floats, int max_counters, cudaStream_t s);
+cudaError_t launch_paged4_tc(PagedAttnParams& p, int D, size_t part_floats, cudaStream_t s);
 
 }  // namespace rc

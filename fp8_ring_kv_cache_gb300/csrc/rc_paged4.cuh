@@ -1,0 +1,61 @@
+// rc_paged4.cuh -- the 4-bit paged cache's numbers: E2M1 codes, and scale bytes
+// with 5 bits of exponent and 3 of fraction (the top byte but the sign of an fp16
+// number, so that a byte becomes one by a shift).  A code times a scale has at
+// most 6 significant bits and lies between 2^-18 and 61,440: an exact fp16 and
+// bf16 number.
+#pragma once
+#include "rc_paged.cuh"
+
+namespace rc {
+
+constexpr int kBlock4 = 16;              // dims of a scale
+constexpr uint32_t kTopScale4 = 226u;    // 10,240: the largest scale that a row gets
+constexpr uint32_t kFirstNan4 = 248u;    // infinity, and NaN above it
+
+__device__ __forceinline__ float scale4_value(uint32_t b) { return __half2float(__ushort_as_half(static_cast<unsigned short>(b << 7))); }
+
+// Scale bytes 0, 1 and 2, 3 of a word as pairs of fp16 numbers.
+__device__ __forceinline__ uint32_t scales01(uint32_t w) { return __byte_perm(w, 0u, 0x1404) >> 1; }
+__device__ __forceinline__ uint32_t scales23(uint32_t w) { return __byte_perm(w, 0u, 0x3424) >> 1; }
+// Byte `sel & 3` of a word (sel: 0x404 times the byte's number, + 0x0404 ... as below) in both halves.
+__device__ __forceinline__ uint32_t scale_twice(uint32_t w, int byte) {
+    return __byte_perm(w, 0u, 0x0404u | (static_cast<uint32_t>(byte) * 0x1010u)) >> 1;
+}
+
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Eight codes of a word as four pairs of fp16 numbers, in order.
+__device__ __forceinline__ void codes8_f16(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+}
+// Eight numbers as codes (nearest, ties to even, cut at 6), the first in the low bits.
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}\n"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+
+}  // namespace rc

@@ -407,6 +407,77 @@ int rc_rope_axes(const rc_rope_plan *plan, const void *x, int64_t x_stride, void
                  int dtype, int64_t n, int heads, const int32_t *positions, int64_t pos_stride, int inverse,
                  void *stream);
 
+/* ---- rotary positions in other forms ---------------------------------------- */
+/*
+ * The forms that rotary embeddings have beside the one above: the turned pairs
+ * are neighbours or lie half a part apart, a part of the head turns, frequencies
+ * are stretched for contexts longer than a model was trained for, and what is
+ * turned is multiplied by a gain.  Dims first .. first + dims - 1 of a head turn,
+ * the others are copied.  Pair i < dims / 2 is
+ *   RC_ROPE_PAIRS    (first + 2i, first + 2i + 1)
+ *   RC_ROPE_HALVES   (first + i, first + i + dims / 2)
+ * and turns by the token's position on its axis: the first sections[0] pairs by
+ * axis 0, and so on.  Pair number r of an axis with w pairs has the frequency
+ * theta = base^(-r / w), with RC_ROPE_SHARED_FREQS base^(-2i / dims) (w = dims / 2
+ * and r = i below), which `scaling` stretches by `factor` >= 1:
+ *   RC_ROPE_SCALE_NONE    not (factor is not read)
+ *   RC_ROPE_SCALE_LINEAR  theta / factor (positions divided by factor)
+ *   RC_ROPE_SCALE_BASE    base times factor^(w / (w - 1)): the slowest pair's
+ *                         frequency is divided by factor, the fastest one's kept
+ *   RC_ROPE_SCALE_PARTS   theta (k + (1 - k) / factor), where k goes from 0 to 1
+ *                         as the pair's turns in `context` positions,
+ *                         context theta / 2 pi, go from low to high
+ * One token at one axis with RC_ROPE_PAIRS, the whole head and a gain of 1 is
+ * what rc_rope_axes does.
+ */
+#define RC_ROPE_PAIRS 0
+#define RC_ROPE_HALVES 1
+#define RC_ROPE_SCALE_NONE 0
+#define RC_ROPE_SCALE_LINEAR 1
+#define RC_ROPE_SCALE_BASE 2
+#define RC_ROPE_SCALE_PARTS 3
+#define RC_ROPE_MAX_HEAD_DIM 256
+
+typedef struct rc_rope_spec {
+    int head_dim;      /* a multiple of 8, 8 .. RC_ROPE_MAX_HEAD_DIM */
+    int first, dims;   /* the part that turns: both even, dims >= 2, first + dims <= head_dim */
+    int layout;        /* RC_ROPE_PAIRS or RC_ROPE_HALVES */
+    int axes;          /* 1 .. RC_ROPE_MAX_AXES */
+    int sections[RC_ROPE_MAX_AXES]; /* pairs of each axis, dims / 2 in all */
+    unsigned flags;    /* RC_ROPE_SHARED_FREQS */
+    double base;       /* in (1, 1e9] */
+    int scaling;       /* RC_ROPE_SCALE_* */
+    double factor;     /* 1 .. 1e6 */
+    double context;    /* RC_ROPE_SCALE_PARTS: > 0, at most 2^31 */
+    double low, high;  /* RC_ROPE_SCALE_PARTS: 0 <= low < high, at most 2^31 */
+    float gain;        /* 2^-16 .. 16 */
+} rc_rope_spec;
+
+/* What the calls take: plain host data, filled once by rc_rope_form_init. */
+typedef struct rc_rope_form {
+    int head_dim, first, dims, layout, axes;
+    float gain;
+    uint64_t turns[RC_ROPE_MAX_HEAD_DIM / 2]; /* pair i: round(frequency / 2 pi * 2^64) */
+    uint8_t axis[RC_ROPE_MAX_HEAD_DIM / 2];   /* pair i: its axis */
+} rc_rope_form;
+
+/*
+ * Fill *form.  Host only.  Errors: RC_ERR_ARG for a NULL pointer and for what is
+ * out of the ranges above; RC_ERR_UNSUPPORTED for a head_dim that is no multiple of 8
+ * or not in 8 .. RC_ROPE_MAX_HEAD_DIM.
+ */
+int rc_rope_form_init(rc_rope_form *form, const rc_rope_spec *spec);
+
+/*
+ * out[t][h] = gain * (x[t][h] turned at token t's positions) in the part that
+ * turns, x[t][h] elsewhere; with back != 0 turned back instead, with the same gain:
+ * the gradient, dx from dout.  The other arguments, the arithmetic and the
+ * errors are those of rc_rope_axes (its head_dim is the form's).
+ */
+int rc_rope_turn(const rc_rope_form *form, const void *x, int64_t x_stride, void *out, int64_t out_stride,
+                 int dtype, int64_t n, int heads, const int32_t *positions, int64_t pos_stride, int back,
+                 void *stream);
+
 /* ---- the paged cache ------------------------------------------------------ */
 /*
  * One layer's FP8 cache for many sequences, in pages the CALLER owns (as with
@@ -544,6 +615,62 @@ int rc_paged_status(const rc_paged_view *view, void *stream);
 /* Test support: the longest one wait of a later paged call may take, in ns
    (default 2 s; process-wide; as rc_cache_set_wait_limit). */
 int rc_paged_set_wait_limit(uint64_t ns);
+
+/* ---- the paged cache in 4 bits ------------------------------------------------ */
+/*
+ * The paged cache above at 4.5 bits a value: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6 and their negatives) with a scale byte per token, head and 16 dims.  Pages (P =
+ * page_tokens: 16, 32, 64 or 128), device memory, 16-byte aligned:
+ *   kcodes [pages][kv_heads][P][head_dim / 2]  dims 2i (low bits) and 2i + 1 of a token
+ *   vcodes [pages][kv_heads][head_dim][P / 2]  tokens 2i (low bits) and 2i + 1 of a dim
+ *   kscale, vscale [pages][kv_heads][head_dim / 16][P]
+ * A scale byte has 5 bits of exponent and 3 of fraction, without a sign: byte b
+ * stands for the fp16 number with the bits b << 7 (2^-17 to 2^-14 in steps of 2^-17,
+ * then eighths of each power of two).  A block's scale s is the least with max |x| <=
+ * 6 s, at most 10,240 (byte 226), so magnitudes over 61,440 saturate; a code is the
+ * one nearest to x / s (ties to the code with an even number), of the exact turn for K (whose
+ * zeros may have either sign).
+ * Blocks of zeros have scale 0.  Every value is then an exact fp16 and bf16 number.
+ * All scale bytes of a row (a token's K or V of a head) that holds an infinity or a
+ * NaN are 255, its codes 0, and it reads as NaN.  Scale bytes 227 .. 254, and 255 in a part
+ * of a row, are not produced; tokens that have them read as some number, infinity or NaN.
+ *
+ * Metadata (rc_paged_batch), workspace, streams, graphs and what happens to
+ * metadata out of bounds are as for the paged cache; a workspace can serve both
+ * kinds of cache under the same rule.
+ */
+typedef struct rc_paged4_view {
+    uint8_t *kcodes;
+    uint8_t *vcodes;
+    uint8_t *kscale;
+    uint8_t *vscale;
+    void *workspace; /* RC_PAGED_WORKSPACE_BYTES, as in rc_paged_view */
+    int pages;       /* >= 1 */
+    int kv_heads;    /* 1 .. 1024 */
+    int head_dim;    /* 64 or 128 */
+    int page_tokens; /* 16, 32, 64 or 128 */
+} rc_paged4_view;
+
+/*
+ * Write each sequence's new tokens into its pages: K turned at the tokens'
+ * positions (as rc_rope_turn, unrounded), K and V quantised as above.  Arguments and errors as
+ * rc_paged_write, with a form of the cache's head_dim; form NULL: K is stored as it comes, and
+ * positions are not read (may be NULL).
+ */
+int rc_paged4_write(const rc_paged4_view *view, const rc_paged_batch *batch, const void *K_bf16, int64_t k_stride,
+                    const void *V_bf16, int64_t v_stride, const int32_t *positions, int64_t pos_stride,
+                    const rc_rope_form *form, void *stream);
+
+/*
+ * Attention of each sequence's new tokens over its pages; arguments and errors
+ * as rc_paged_attend.  A row of Q is held in fp16 relative to its largest value: what lies under
+ * 2^-32 of that loses bits.
+ */
+int rc_paged4_attend(const rc_paged4_view *view, const rc_paged_batch *batch, const void *Q_bf16, int64_t q_stride,
+                     int heads, void *out_bf16, int64_t out_stride, float *lse, int causal, void *stream);
+
+/* As rc_paged_status, for the calls on this view's workspace. */
+int rc_paged4_status(const rc_paged4_view *view, void *stream);
 
 /* Number of occupied slots of `layer`, or a negative status. */
 int rc_cache_occupancy(const rc_cache *h, int layer);
