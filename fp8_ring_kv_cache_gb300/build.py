@@ -27,7 +27,7 @@ SOURCES = ["rc_host.cu", "rc_write.cu", "rc_rotate.cu", "rc_attention.cu", "rc_n
            "rc_paged_scores.cu", "rc_paged_scores_tc.cu", "rc_paged_evict.cu", "rc_rope_form.cu", "rc_paged4_host.cu", "rc_paged4_write.cu",
            "rc_paged4_attn.cu", "rc_paged4_tc.cu"]
 HEADERS = ["rc_device.cuh", "rc_internal.h", "rc_layout.h", "rc_nvtx.h", "rc_paged.cuh", "rc_paged_bounds.h", "rc_paged_host.h",
-           "rc_paged_rows.cuh", "rc_paged_tc.cuh", "rc_turn_pair.cuh", "rc_paged4.cuh"]
+           "rc_paged_tc.cuh", "rc_turn_pair.cuh", "rc_paged4.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -365,7 +365,7 @@ cudaError_t launch_paged_scores(const PagedScoreParams& p, int D, cudaStream_t s
 cudaError_t launch_paged_scores_tc(const PagedScoreParams& p, int D, cudaStream_t s);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int D, cudaStream_t s);
 cudaError_t launch_paged4_write(const Paged4WriteParams& p, int D, cudaStream_t s);
-cudaError_t launch_paged4_attention(PagedAttnParams& p, int D, size_t part_floats, int max_counters, cudaStream_t s);
+cudaError_t launch_paged4_attention(PagedAttnParams& p, int D, size_t part_floats, cudaStream_t s);
 cudaError_t launch_paged4_tc(PagedAttnParams& p, int D, size_t part_floats, cudaStream_t s);
 
 }  // namespace rc

@@ -17,14 +17,25 @@ __device__ __forceinline__ float scale4_value(uint32_t b) { return __half2float(
 // Scale bytes 0, 1 and 2, 3 of a word as pairs of fp16 numbers.
 __device__ __forceinline__ uint32_t scales01(uint32_t w) { return __byte_perm(w, 0u, 0x1404) >> 1; }
 __device__ __forceinline__ uint32_t scales23(uint32_t w) { return __byte_perm(w, 0u, 0x3424) >> 1; }
-// Byte `sel & 3` of a word (sel: 0x404 times the byte's number, + 0x0404 ... as below) in both halves.
-__device__ __forceinline__ uint32_t scale_twice(uint32_t w, int byte) {
-    return __byte_perm(w, 0u, 0x0404u | (static_cast<uint32_t>(byte) * 0x1010u)) >> 1;
-}
+// Bytes `odd` and 2 + `odd` of a word (odd 0 or 1) as fp16 numbers.
+__device__ __forceinline__ uint32_t scales_apart(uint32_t w, int odd) { return __byte_perm(w, 0u, 0x2404u + 0x1010u * odd) >> 1; }
+// Not 0 if a byte of a word is 248 or more: no number.
+__device__ __forceinline__ uint32_t nan_scales(uint32_t w) { return ((w & 0x78787878u) + 0x08080808u) & w & 0x80808080u; }
 
 __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Both numbers times the lower, or the upper, one of b.
+__device__ __forceinline__ uint32_t half2_mul_lo(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {l, l};\n\tmul.rn.f16x2 %0, %1, t;\n\t}\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_mul_hi(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {h, h};\n\tmul.rn.f16x2 %0, %1, t;\n\t}\n" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

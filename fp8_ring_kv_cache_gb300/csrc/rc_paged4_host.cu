@@ -145,7 +145,7 @@ int rc_paged4_attend(const rc_paged4_view* view, const rc_paged_batch* batch, co
     PagedAttnParams p{};
     int st = check_attend(view, batch, Q_bf16, q_stride, heads, out_bf16, out_stride, lse, causal, &p);
     if (st != RC_OK || p.q == nullptr) return st;
-    return launch_paged4_attention(p, view->head_dim, kPartFloats, kCounters, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch_paged4_attention(p, view->head_dim, kPartFloats, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? RC_OK
                : RC_ERR_CUDA;
 }
