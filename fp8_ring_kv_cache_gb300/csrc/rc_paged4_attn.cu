@@ -98,6 +98,11 @@ struct Piece {
     int mine, first, parts, step, odd, counter;
 };
 
+// Blocks of an SM: registers spilled cost more than fewer warps (one sequence of 131,072 tokens x 8 heads x 128 with a
+// row: 4 blocks of 128 registers 46 us, 3 of 162 41; 32 x 8,000 with 16 rows: 3 blocks 90 us, 2 81).
+constexpr int grid_blocks(int NR) { return NR == 1 ? 4 : 2; }
+constexpr int line_blocks(int NR) { return NR == 1 ? 3 : 2; }
+
 // 8 NR rows (NR 1 or 2).
 template <int D, int NR>
 __device__ __forceinline__ void attend_piece(const PagedAttnParams& p, RowsSmem<D, NR>& sh, const Piece& pc) {
@@ -531,7 +536,7 @@ __device__ __forceinline__ void attend_piece(const PagedAttnParams& p, RowsSmem<
 
 // ---------------------------------------------------------------- a block's place in the grid
 template <int D, int NR>
-__global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 4 : 3) paged4_rows_kernel(PagedAttnParams p) {
+__global__ void __launch_bounds__(kRowsThreads, grid_blocks(NR)) paged4_rows_kernel(PagedAttnParams p) {
     __shared__ __align__(16) RowsSmem<D, NR> sh;
     Piece pc;
     pc.s = blockIdx.z;
@@ -571,7 +576,7 @@ struct Line {
 };
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 4 : 3) paged4_line_kernel(PagedAttnParams p) {
+__global__ void __launch_bounds__(kRowsThreads, line_blocks(NR)) paged4_line_kernel(PagedAttnParams p) {
     __shared__ __align__(16) RowsSmem<D, NR> sh;
     __shared__ Line line;
     __shared__ int64_t u_end;
@@ -685,22 +690,23 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 4 : 3) paged4_line_ker
 
 template <int D, int NR>
 cudaError_t launch_rows(PagedAttnParams& p, cudaStream_t s) {
-    constexpr int kResident = 152 * (NR == 1 ? 4 : 3);  // blocks at once
-    static_assert(2 * kResident * part_floats<D, NR>() * sizeof(float) <= (32u << 20) && kResident <= 16384, "places in the workspace");
+    constexpr int kGrid = 152 * grid_blocks(NR), kLine = 152 * line_blocks(NR);  // blocks at once
+    constexpr int kPlaces = kGrid > 2 * kLine ? kGrid : 2 * kLine;
+    static_assert(kPlaces * part_floats<D, NR>() * sizeof(float) <= (32u << 20) && kPlaces <= 16384, "places in the workspace");
     // The grid's way while all blocks are there at once with four units each at most.  (Two units stay together, but for few
     // blocks.)
     const int64_t lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
     const int64_t units = std::max(1, (p.g.max_kv + kUnit - 1) / kUnit);
-    int64_t splits = std::min<int64_t>(std::max<int64_t>(kResident / lists, 1), units);
+    int64_t splits = std::min<int64_t>(std::max<int64_t>(kGrid / lists, 1), units);
     const int64_t least = units > 2 && lists * splits <= 2 * 152 ? 1 : 2;
     const int64_t per = std::max((units + splits - 1) / splits, least);
     splits = (units + per - 1) / per;
-    if (lists * splits <= kResident && per <= 4) {
+    if (lists * splits <= kGrid && per <= 4) {
         p.split_tokens = static_cast<int>(per) * kUnit;
         p.splits = static_cast<int>(splits);
         paged4_rows_kernel<D, NR><<<dim3(p.splits, p.g.kv_heads, p.g.seqs), kRowsThreads, 0, s>>>(p);
     } else {
-        paged4_line_kernel<D, NR><<<kResident, kRowsThreads, 0, s>>>(p);
+        paged4_line_kernel<D, NR><<<kLine, kRowsThreads, 0, s>>>(p);
     }
     return cudaGetLastError();
 }
