@@ -15,7 +15,7 @@
 // no product of the largest bf16 numbers with the gain overflows.
 // The codes and scales of K are those of the exact turn (to 2^-25 (|a| + |b|), what
 // cos and sin leave): where an fp32 sum is too close to the middle between two codes,
-// or a block's largest to the border between two scales, the warp's rows are summed
+// or a block's largest to the border between two scales, it is (or they are) summed
 // again with twice the bits.
 #include "rc_paged4.cuh"
 #include "rc_turn_pair.cuh"
@@ -55,23 +55,27 @@ __device__ __forceinline__ float reciprocal(float x) {
     return r;
 }
 
-// A quotient of numbers of few bits (8 by 4) that is off by some 2^-22 of itself, cut
-// to 16 bits: one that lies on the middle between two codes is put there again, and
-// no other one can get there.
-__device__ __forceinline__ float to16bits(float q) { return __uint_as_float((__float_as_uint(q) + 0x80u) & ~0xffu); }
+// The codes of quotients by s, r its reciprocal: the remainder of the first product is added in, so that a quotient that
+// is a number of fp32 is that number.  (What lies on the middle between two codes stays there; other quotients of numbers
+// of 8 bits by one of 4 are 2^-9 of themselves away from it.)  Taken with the other sign, a zero keeps its own.
+__device__ __forceinline__ uint32_t codes8_of_quotients(const float2 (&x)[4], float s, float r) {
+    const float2 s2 = make_float2(s, s), r2 = make_float2(-r, -r);
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 q = mul2(x[j], r2), u = fma2(fma2(q, s2, x[j]), r2, q);
+        w[2 * j] = u.x;
+        w[2 * j + 1] = u.y;
+    }
+    return codes8(w) ^ 0x88888888u;
+}
 
 // The code by comparisons with the middles between codes, which are exact (a middle
 // has 3 bits, a scale 4); s is 2^-8 of the scale.
-__device__ __forceinline__ uint32_t codes8_exactly(const float (&y)[8], float s) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = fabsf(y[i]);
-        uint32_t c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) + (a > 2.5f * s) + (a >= 3.5f * s) + (a > 5.f * s);
-        c = s == 0.f ? 0u : c;
-        w |= (c | (__float_as_uint(y[i]) >> 31 << 3)) << (4 * i);
-    }
-    return w;
+__device__ __forceinline__ uint32_t code_exactly(float y, float s) {
+    const float a = fabsf(y);
+    const uint32_t c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) + (a > 2.5f * s) + (a >= 3.5f * s) + (a > 5.f * s);
+    return (s == 0.f ? 0u : c) | (__float_as_uint(y) >> 31 << 3);
 }
 
 // Where dim d turns: its pair, what it is paired with, the sign of that in the sum.
@@ -99,23 +103,17 @@ __device__ __forceinline__ Role role_of(const RopeFormDev& f, int d) {
     return r;
 }
 
-// The exact sums of the lane's dims 8 c .. (rounded to odd) at 2^-8, from the row's K and the token's positions.
-// (Out of line: what one warp of thousands needs costs the others little.)
-__device__ __noinline__ void exact_sums(const Paged4WriteParams& p, const __nv_bfloat16* k, int row, int c, float* y) {
+// The exact sum of dim d (rounded to odd) at 2^-8, from the row's K and the token's positions.  (Out of line: what some
+// values of a hundred thousand need costs the others little.)
+__device__ __noinline__ float exact_sum(const Paged4WriteParams& p, const __nv_bfloat16* k, int row, int d) {
     const float g = p.form.gain * kDown;
-    for (int j = 0; j < 8; ++j) {
-        const int d = 8 * c + j;
-        const Role r = role_of(p.form, d);
-        const float a = __bfloat162float(k[d]), b = __bfloat162float(k[r.partner]);
-        if (!r.turns) {
-            y[j] = a * kDown;
-            continue;
-        }
-        TurnPair t = turn_cos_sin_pair(__ldg(p.pos + p.form.axis[r.pair] * p.pos_stride + row), p.form.turns[r.pair]);
-        const float2 hi = make_float2(__fmul_rn(t.hi.x, g), __fmul_rn(t.hi.y, g));
-        const float2 lo = make_float2(__fmaf_rn(t.hi.x, g, -hi.x) + t.lo.x * g, __fmaf_rn(t.hi.y, g, -hi.y) + t.lo.y * g);
-        y[j] = a == 0.f && b == 0.f ? 0.f : sum_exactly(a, hi.x, lo.x, r.upper ? b : -b, hi.y, lo.y);
-    }
+    const Role r = role_of(p.form, d);
+    const float a = __bfloat162float(k[d]), b = __bfloat162float(k[r.partner]);
+    if (!r.turns) return a * kDown;
+    const TurnPair t = turn_cos_sin_pair(__ldg(p.pos + p.form.axis[r.pair] * p.pos_stride + row), p.form.turns[r.pair]);
+    const float2 hi = make_float2(__fmul_rn(t.hi.x, g), __fmul_rn(t.hi.y, g));
+    const float2 lo = make_float2(__fmaf_rn(t.hi.x, g, -hi.x) + t.lo.x * g, __fmaf_rn(t.hi.y, g, -hi.y) + t.lo.y * g);
+    return a == 0.f && b == 0.f ? 0.f : sum_exactly(a, hi.x, lo.x, r.upper ? b : -b, hi.y, lo.y);
 }
 
 // Eight words, the nibbles of each a token's codes of eight dims, become eight words, the nibbles of each a dim's codes of
@@ -142,18 +140,27 @@ __device__ __forceinline__ void transpose_codes(uint32_t (&w)[8]) {
     }
 }
 
-__device__ __forceinline__ void open_bf16(const uint4& w, float (&x)[8]) {
+__device__ __forceinline__ void open_bf16(const uint4& w, float2 (&x)[4]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
 }
-// Whether a word holds a bf16 infinity or NaN.
-__device__ __forceinline__ bool not_finite(const uint4& w) {
-    auto half = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
-    return half(w.x) || half(w.y) || half(w.z) || half(w.w);
+// The larger of two pairs of numbers of 16 bits, each.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The largest magnitude of eight bf16 numbers, as the bits of one: infinities and NaNs are above every number.
+__device__ __forceinline__ uint32_t largest_bits(const uint4& w) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    const uint32_t m = max_u16x2(max_u16x2(w.x & kAbs, w.y & kAbs), max_u16x2(w.z & kAbs, w.w & kAbs));
+    return max(m & 0xffffu, m >> 16);
+}
+constexpr uint32_t kInfBits = 0x7f80u;
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 template <int D, Partner PART>
@@ -161,9 +168,12 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(con
     constexpr int LANES = D / 8;  // of one token
     constexpr int kThreads = kRun * LANES;
     constexpr int NB = D / kBlock4;
+    constexpr int kCodeJobs = 2 * LANES;  // of a head: V's codes of 8 dims of 8 tokens each
     __shared__ float2 table[kRun * D / 2];
     __shared__ uint32_t scode[kMaxHeads][kRun][LANES + 1];             // V's codes
+    __shared__ uint32_t sold[8][kMaxHeads * kCodeJobs];                // the words that they go into, of a run that is not all new
     __shared__ __align__(16) uint8_t sscale[kMaxHeads][2][NB][kRun];   // K's and V's scale bytes
+    __shared__ uint16_t skey[PART == kAnywhere ? kThreads * 8 : 1];    // K's rows
     const int s = blockIdx.x / runs, run = blockIdx.x % runs;
     const Seq q = load_seq(p.g, s);
     if (q.n == 0) return;
@@ -174,183 +184,244 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(con
     const int first = q.kv - q.n;                         // index of the first new token
     const int base = (first & ~(kRun - 1)) + run * kRun;  // index of the run's first token
     if (base >= q.kv) return;
-    const int page = load_page(p.g, s, base >> p.g.page_shift);
-    if (page < 0) return;
+    const int entry = __ldg(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages + (base >> p.g.page_shift));
     const int P = 1 << p.g.page_shift, off = base & (P - 1);
-    const int tok = threadIdx.x / LANES, c = threadIdx.x % LANES;
+    const int tok = threadIdx.x / LANES, c = threadIdx.x % LANES, lane = threadIdx.x & 31;
     const int index = base + tok;
     const bool live = index >= first && index < q.kv;
     const int row = q.q0 + (live ? index - first : 0);
-    const int h0 = blockIdx.y * heads_per_block, h1 = min(p.g.kv_heads, h0 + heads_per_block);
+    const int h0 = blockIdx.y * heads_per_block, h1 = min(p.g.kv_heads, h0 + heads_per_block), heads = h1 - h0;
+    // tokens a .. b - 1 of the run are new
+    const int a = max(0, first - base), b = min(kRun, q.kv - base);
 
-    const Role mine = role_of(p.form, 8 * c);
-    // (kVector: the lane's eight dims have one role)
-    const int partner_at = PART == kVector ? mine.partner : 8 * c;
     const __nv_bfloat16* kr = p.K + row * p.k_stride;
-    const __nv_bfloat16* vr = p.V + row * p.v_stride + c * 8;
-    uint4 kw = make_uint4(0, 0, 0, 0), vw = kw, pw = kw;
+    const __nv_bfloat16* vr = p.V + row * p.v_stride;
+    uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
     auto fetch = [&](int h) {
         kw = ldg_nc_na_v4(kr + static_cast<size_t>(h) * D + c * 8);
-        if (PART == kVector) pw = __ldg(reinterpret_cast<const uint4*>(kr + static_cast<size_t>(h) * D + partner_at));
-        vw = ldg_nc_na_v4(vr + static_cast<size_t>(h) * D);
+        vw = ldg_nc_na_v4(vr + static_cast<size_t>(h) * D + c * 8);
     };
     if (live) fetch(h0);
 
-    // the tokens' g (cos, sin) at 2^-8.  A sine of 0 says that nothing is rounded: where it is 0 only in fp32, it gets
-    // its value, the angle itself
+    // the tokens' g (cos, sin) at 2^-8, by the lanes that have the token's row.  A sine of 0 says that nothing is rounded:
+    // where it is 0 only in fp32, it gets its value, the angle itself
     const float g = p.form.gain * kDown;
+    const int pairs = p.form.dims >> 1;
     {
+        constexpr int kEach = D / 2 / LANES;
         const uint64_t* turns = param_address(p.form.turns);
         const uint8_t* axis = param_address(p.form.axis);
-        const int pairs = p.form.dims >> 1;
-        for (int i = threadIdx.x; i < kRun * pairs; i += kThreads) {
-            const int t = i / pairs, k = i - t * pairs;
-            if (base + t < first || base + t >= q.kv) continue;
-            const int pos = __ldg(p.pos + axis[k] * p.pos_stride + q.q0 + base + t - first);
-            float2 cs = turn_cos_sin(pos, turns[k]);
+        int pos[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            pos[i] = live && c + LANES * i < pairs ? __ldg(p.pos + axis[c + LANES * i] * p.pos_stride + row) : 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int k = c + LANES * i;
+            if (!live || k >= pairs) continue;
+            float2 cs = turn_cos_sin(pos[i], turns[k]);
             if (cs.y == 0.f) {
-                const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns[k];
+                const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos[i])) * turns[k];
                 cs.y = cs.x * static_cast<float>(static_cast<int64_t>(frac << 1) >> 1) * 3.4061215e-19f;  // 2 pi / 2^64
             }
-            table[t * (D / 2) + k] = make_float2(g * cs.x, g * cs.y);
+            table[tok * (D / 2) + k] = make_float2(g * cs.x, g * cs.y);
         }
     }
-    __syncthreads();
-    float cs[8], sn[8];
-    uint32_t exact = 0;  // dims whose sum is exact in fp32 (with a gain that is a power of two)
+    const int page = check_page(p.g, entry) ? entry : -1;
+    if (page < 0) return;
+    const size_t at0 = static_cast<size_t>(page) * p.g.kv_heads + h0;  // of the first head
+    auto codes_of = [&](int job) {  // the first of its eight words, P / 8 words apart
+        const int hl = job / kCodeJobs, c8 = job % LANES, t0 = 8 * ((job / LANES) & 1);
+        return reinterpret_cast<uint32_t*>(p.g.vcodes + ((at0 + hl) * D + 8 * c8) * (P / 2) + (off + t0) / 2);
+    };
+    if (b - a < kRun)
+        for (int i = threadIdx.x; i < heads * kCodeJobs; i += kThreads)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cp_async4(&sold[j][i], codes_of(i) + j * (P / 8));
+    __syncwarp();
+    float2 cs[4], sn[4];
+    uint32_t partner[4] = {0, 0, 0, 0};  // kAnywhere: where in the row's 16-bit numbers, two a word
+    const bool plain = (__float_as_uint(p.form.gain) & 0x7fffffu) == 0u;  // a power of two
+    uint32_t exact = 0;  // the dims whose sums are exact in fp32, four bits each
+    const Role mine = role_of(p.form, 8 * c);
     {
-        const bool plain = (__float_as_uint(p.form.gain) & 0x7fffffu) == 0u;
+        float cc[8], ss[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+            // (kVector: the lane's eight dims have one role)
             const Role r = PART == kVector ? Role{mine.pair + j, 0, mine.turns, mine.upper} : role_of(p.form, 8 * c + j);
-            cs[j] = kDown;
-            sn[j] = 0.f;
+            cc[j] = kDown;
+            ss[j] = 0.f;
             if (r.turns && live) {
                 const float2 t = table[tok * (D / 2) + r.pair];
-                cs[j] = t.x;
-                sn[j] = r.upper ? t.y : -t.y;
+                cc[j] = t.x;
+                ss[j] = r.upper ? t.y : -t.y;
             }
-            exact |= (!r.turns || (sn[j] == 0.f && plain) ? 1u : 0u) << j;
+            if (!r.turns || (plain && ss[j] == 0.f)) exact |= 0xfu << (4 * j);
+            if (PART == kAnywhere) partner[j / 2] |= static_cast<uint32_t>(r.partner) << (16 * (j & 1));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            cs[j] = make_float2(cc[2 * j], cc[2 * j + 1]);
+            sn[j] = make_float2(ss[2 * j], ss[2 * j + 1]);
         }
     }
-    // lanes of the warp that have the token's row
-    const uint32_t row_lanes = (LANES == 16 ? 0xffffu : 0xffu) << ((threadIdx.x & 31) & ~(LANES - 1));
+    const bool some_exact = __any_sync(0xffffffffu, exact != 0u);
+    // lanes of the warp that have the token's row, and the one that has what this one's dims are paired with
+    const uint32_t row_lanes = (LANES == 16 ? 0xffffu : 0xffu) << (lane & ~(LANES - 1));
+    const int partner_lane = (lane & ~(LANES - 1)) + (PART == kVector ? mine.partner / 8 : c);
 
     for (int h = h0; h < h1; ++h) {
         const int hl = h - h0;
-        float x[8], xp[8], v[8];
+        float2 x[4], xp[4];
         open_bf16(kw, x);
-        open_bf16(vw, v);
+        const uint32_t kmost = largest_bits(kw), vmost = largest_bits(vw);
+        uint32_t pmost = kmost;  // of what the dims are paired with
         if (PART == kInLane) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) xp[j] = x[j ^ 1];
+            for (int j = 0; j < 4; ++j) xp[j] = make_float2(x[j].y, x[j].x);
         } else if (PART == kVector) {
-            open_bf16(pw, xp);
+            uint4 w;
+            w.x = __shfl_sync(0xffffffffu, kw.x, partner_lane);
+            w.y = __shfl_sync(0xffffffffu, kw.y, partner_lane);
+            w.z = __shfl_sync(0xffffffffu, kw.z, partner_lane);
+            w.w = __shfl_sync(0xffffffffu, kw.w, partner_lane);
+            open_bf16(w, xp);
+            pmost = __shfl_sync(0xffffffffu, kmost, partner_lane);
         } else {
+            __syncwarp();
+            *reinterpret_cast<uint4*>(skey + 8 * threadIdx.x) = kw;
+            __syncwarp();
+            const uint16_t* staged = skey + tok * D;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                xp[j] = live ? __bfloat162float(kr[static_cast<size_t>(h) * D + role_of(p.form, 8 * c + j).partner]) : 0.f;
+            for (int j = 0; j < 4; ++j)
+                xp[j] = make_float2(__uint_as_float(static_cast<uint32_t>(staged[partner[j] & 0xffffu]) << 16),
+                                    __uint_as_float(static_cast<uint32_t>(staged[partner[j] >> 16]) << 16));
+#pragma unroll
+            for (int o = 1; o < LANES; o <<= 1) pmost = max(pmost, __shfl_xor_sync(0xffffffffu, pmost, o));
         }
-        const bool kbad = (__ballot_sync(0xffffffffu, not_finite(kw)) & row_lanes) != 0u;
-        const bool vbad = (__ballot_sync(0xffffffffu, not_finite(vw)) & row_lanes) != 0u;
+        const bool kbad = (__ballot_sync(0xffffffffu, kmost >= kInfBits) & row_lanes) != 0u;
+        const bool vbad = (__ballot_sync(0xffffffffu, vmost >= kInfBits) & row_lanes) != 0u;
+        const uint4 vnow = vw;
         if (live && h + 1 < h1) fetch(h + 1);  // the next head is on its way
 
         // K
-        float y[8], reach = 0.f, amax = 0.f;
+        float2 y[4];
+        float amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            y[j] = fmaf(x[j], cs[j], xp[j] * sn[j]);
-            amax = fmaxf(amax, fabsf(y[j]));
-            xp[j] = (exact >> j) & 1u ? 0.f : fabsf(x[j]) + fabsf(xp[j]);  // what its error is relative to
-            reach = fmaxf(reach, xp[j]);
+        for (int j = 0; j < 4; ++j) {
+            y[j] = fma2(x[j], cs[j], mul2(xp[j], sn[j]));
+            amax = max3(amax, fabsf(y[j].x), fabsf(y[j].y));
         }
+        // A sum is within 2^-22 g (|a| + |b|) of the exact one (cos and sin half an ulp of 1 each, 2^-25, and three
+        // roundings of 2^-24), and 2^-23 more with a gain that is rounded; the quotient by the scale adds 2^-22 of itself:
+        // 2^-21 of g (|a| + |b|), or 1.25 times that.
+        const float slack = g * (plain ? 0x1p-21f : 0x1.4p-21f);
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        reach = fmaxf(reach, __shfl_xor_sync(0xffffffffu, reach, 1));
-        uint32_t kb = scale4_byte(amax);
-        // A sum is within 2^-21 g (|a| + |b|) of the exact one: cos and sin half an ulp of 1 each (2^-25), the gain and
-        // three roundings 2^-24 each; the quotient by the scale adds 2^-22 of itself.
-        const float slack = g * 0x1p-20f;
-        bool again = reach > 0.f && scale4_open(amax, reach * slack, kb);
-        const float inv = kb == 0u ? 0.f : reciprocal(scale4_value(kb) * kDown);
-        float lo[8], hi[8];
+        const float err = exact == 0xffffffffu ? 0.f : __uint_as_float(max(kmost, pmost) << 16) * (2.f * slack);  // (at most, of all)
+        float err2 = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, 1));
+        if (some_exact) {  // a block whose largest is one of its exact sums is not open
+            float most = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float w = y[j] * inv, tol = xp[j] * (slack * inv);
-            const float r = (exact >> j) & 1u ? to16bits(w) : w;
-            lo[j] = r - tol;
-            hi[j] = r + tol;
+            for (int j = 0; j < 8; ++j)
+                if (!((exact >> (4 * j)) & 1u)) most = fmaxf(most, fabsf(j & 1 ? y[j / 2].y : y[j / 2].x));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            if (most + err2 < amax) err2 = 0.f;
+        }
+        uint32_t kb = scale4_byte(amax);
+        bool open = err2 > 0.f && scale4_open(amax, err2, kb);
+        const float scale = scale4_value(kb) * kDown, inv = kb == 0u ? 0.f : reciprocal(scale);
+        float lo[8], hi[8];
+        const float reach = slack * inv;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 w = mul2(y[j], make_float2(inv, inv));
+            const float2 tol = mul2(make_float2(fabsf(x[j].x) + fabsf(xp[j].x), fabsf(x[j].y) + fabsf(xp[j].y)), make_float2(reach, reach));
+            const float2 u = add2(w, tol);
+            lo[2 * j] = w.x - tol.x;
+            lo[2 * j + 1] = w.y - tol.y;
+            hi[2 * j] = u.x;
+            hi[2 * j + 1] = u.y;
         }
         uint32_t kc = codes8(lo);
-        again = (again || kc != codes8(hi)) && live && !kbad;
-        if (__any_sync(0xffffffffu, again)) {
-            float z[8];
-            if (live && !kbad) exact_sums(p, kr + static_cast<size_t>(h) * D, row, c, z);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = 0.f;
-            amax = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(z[j]));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            kb = scale4_byte(amax);
-            kc = codes8_exactly(z, scale4_value(kb) * kDown);
+        uint32_t unsure = (kc ^ codes8(hi)) & ~exact;
+        if (some_exact) kc = (kc & ~exact) | (codes8_of_quotients(y, scale, inv) & exact);
+        if (!live || kbad) {
+            open = false;
+            unsure = 0u;
         }
+        const __nv_bfloat16* keys = kr + static_cast<size_t>(h) * D;
+        if (__any_sync(0xffffffffu, open)) {  // the scale may be another: both lanes of the block take all their sums again
+            const bool other = __shfl_xor_sync(0xffffffffu, open ? 1 : 0, 1) != 0;  // (all lanes, before anything is decided)
+            open = open || other;
+            float z[8];
+            amax = 0.f;
+            if (open) {
+#pragma unroll 1
+                for (int j = 0; j < 8; ++j) z[j] = exact_sum(p, keys, row, 8 * c + j);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(z[j]));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            if (open) {
+                kb = scale4_byte(amax);
+                kc = unsure = 0u;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) kc |= code_exactly(z[j], scale4_value(kb) * kDown) << (4 * j);
+            }
+        }
+        while (unsure != 0u) {
+            const int j = (__ffs(unsure) - 1) >> 2;
+            unsure &= ~(0xfu << (4 * j));
+            kc = (kc & ~(0xfu << (4 * j))) | code_exactly(exact_sum(p, keys, row, 8 * c + j), scale) << (4 * j);
+        }
+        __syncwarp();
         if (kbad) {
             kc = 0u;
             kb = 255u;
         }
         // V
-        amax = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] *= kDown;
-            amax = fmaxf(amax, fabsf(v[j]));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        uint32_t vb = scale4_byte(amax);
-        const float vinv = vb == 0u ? 0.f : reciprocal(scale4_value(vb) * kDown);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = to16bits(v[j] * vinv);
-        uint32_t vc = codes8(v);
+        const uint32_t vtop = max(vmost, __shfl_xor_sync(0xffffffffu, vmost, 1));
+        uint32_t vb = scale4_byte(__uint_as_float(vtop << 16) * kDown);
+        const float vscale = scale4_value(vb), vinv = vb == 0u ? 0.f : reciprocal(vscale);
+        float2 v[4];
+        open_bf16(vnow, v);
+        uint32_t vc = codes8_of_quotients(v, vscale, vinv);
         if (vbad) {
             vc = 0u;
             vb = 255u;
         }
-        if (live) {
-            const size_t at = ((static_cast<size_t>(page) * p.g.kv_heads + h) << p.g.page_shift) + off + tok;
-            *reinterpret_cast<uint32_t*>(p.g.kcodes + at * (D / 2) + 4 * c) = kc;
-        }
+        if (live) *reinterpret_cast<uint32_t*>(p.g.kcodes + (((at0 + hl) << p.g.page_shift) + off + tok) * (D / 2) + 4 * c) = kc;
         scode[hl][tok][c] = vc;
         if ((c & 1) == 0) {
             sscale[hl][0][c >> 1][tok] = static_cast<uint8_t>(kb);
             sscale[hl][1][c >> 1][tok] = static_cast<uint8_t>(vb);
         }
     }
+    cp_async_wait_all();
     __syncthreads();
-    // tokens a .. b - 1 of the run are new
-    const int a = max(0, first - base), b = min(kRun, q.kv - base);
-    const int heads = h1 - h0;
-    constexpr int kCodeJobs = 2 * LANES;  // of a head: 8 dims of 8 tokens each
     for (int i = threadIdx.x; i < heads * kCodeJobs; i += kThreads) {
         const int hl = i / kCodeJobs, c8 = i % LANES, t0 = 8 * ((i / LANES) & 1);
         const int m0 = max(a, t0) - t0, m1 = min(b, t0 + 8) - t0;  // new ones among the eight
         if (m1 <= m0) continue;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(
-            p.g.vcodes + ((static_cast<size_t>(page) * p.g.kv_heads + h0 + hl) * D + 8 * c8) * (P / 2) + (off + t0) / 2);
+        uint32_t* dst = codes_of(i);
         const int step = P / 8;  // words between dims
-        uint32_t w[8], old[8];
+        uint32_t w[8];
         const uint32_t mask = (m1 == 8 ? 0xffffffffu : (1u << (4 * m1)) - 1u) & ~((1u << (4 * m0)) - 1u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) old[j] = mask == 0xffffffffu ? 0u : dst[j * step];
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = scode[hl][t0 + j][c8];
         transpose_codes(w);
+        if (mask == 0xffffffffu) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dst[j * step] = (w[j] & mask) | (old[j] & ~mask);
+            for (int j = 0; j < 8; ++j) dst[j * step] = w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dst[j * step] = (w[j] & mask) | (sold[j][i] & ~mask);
+        }
     }
     for (int i = threadIdx.x; i < heads * 2 * NB; i += kThreads) {
         const int hl = i / (2 * NB), which = (i / NB) & 1, nb = i % NB;
-        uint8_t* dst = (which ? p.g.vscale : p.g.kscale) + ((static_cast<size_t>(page) * p.g.kv_heads + h0 + hl) * NB + nb) * P + off;
+        uint8_t* dst = (which ? p.g.vscale : p.g.kscale) + ((at0 + hl) * NB + nb) * P + off;
         const uint8_t* src = sscale[hl][which][nb];
         if (a == 0 && b == kRun)
             *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
