@@ -155,6 +155,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, AbortS
 __device__ __forceinline__ void named_barrier_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
+// Arrive at barrier `id` without waiting for it.
+__device__ __forceinline__ void named_barrier_arrive(int id, int count) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
 // The same barrier, returning the AND of `pred` over all `count` threads (every
 // participant of a barrier instance uses this form).
 __device__ __forceinline__ bool named_barrier_and(int id, int count, bool pred) {
