@@ -206,34 +206,40 @@ def _turned(x, positions, rope, out, inverse, stream, what: str, fn, turn):
         raise ValueError("x must be a [n][heads][head_dim] tensor")
     if not x.is_cuda:
         raise TypeError("x must be a CUDA tensor")
-    n, heads, dim = x.shape
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    n, heads, dim = shape = x.shape
+    dtype, device = x.dtype, x.device
+    if dtype is torch.bfloat16:
+        code, size = RC_BF16, 2
+    elif dtype is torch.float32:
+        code, size = RC_F32, 4
+    else:
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {dtype}")
     if dim != rope.head_dim:
         raise ValueError(f"x has head_dim {dim}, the plan {rope.head_dim}")
-    if torch.is_grad_enabled() and (x.requires_grad or getattr(out, "requires_grad", False)):
+    if (x.requires_grad or getattr(out, "requires_grad", False)) and torch.is_grad_enabled():
         if out is not None:
             raise RuntimeError(f"{what}: out= is not differentiable, but x or out requires a gradient")
         if stream is None:
             return _Turn.apply(x, positions, rope, inverse, turn)
-        own, current = _stream(stream, x.device), torch.cuda.current_stream(x.device)
+        own, current = _stream(stream, device), torch.cuda.current_stream(device)
         with torch.cuda.stream(own):  # (autograd runs the gradient on the stream of the turn)
             y = _Turn.apply(x, positions, rope, inverse, turn)
         y.record_stream(current)
         return y
-    xp, xs = _rows(x, x.dtype, n, heads, dim, "x", x.device)
-    if out is None:
-        out = _empty_on(stream, (n, heads, dim), x.dtype, x.device)
-    op, os_ = _rows(out, x.dtype, n, heads, dim, "out", x.device)
-    pp, ps = _positions(positions, rope.axes, n, "positions", x.device)
-    if out is not x and (xp != op or xs != os_):
-        size = x.element_size()
-        row = heads * dim
-        if op < xp + ((n - 1) * xs + row) * size and xp < op + ((n - 1) * os_ + row) * size and \
-                _rows_meet(xp, xs * size, op, os_ * size, n, row * size):
-            raise ValueError("out overlaps x without being x")
-    _call(x.device, stream, what, fn, rope._ptr, xp, xs, op, os_,
-          RC_BF16 if x.dtype == torch.bfloat16 else RC_F32, n, heads, pp, ps, 1 if inverse else 0)
+    xp, xs = _rows(x, dtype, n, heads, dim, "x", device)
+    if out is x:
+        op, os_ = xp, xs
+    else:
+        if out is None:
+            out = _empty_on(stream, shape, dtype, device)
+        op, os_ = _rows(out, dtype, n, heads, dim, "out", device)
+        if xp != op or xs != os_:
+            row = heads * dim
+            if op < xp + ((n - 1) * xs + row) * size and xp < op + ((n - 1) * os_ + row) * size and \
+                    _rows_meet(xp, xs * size, op, os_ * size, n, row * size):
+                raise ValueError("out overlaps x without being x")
+    pp, ps = _positions(positions, rope.axes, n, "positions", device)
+    _call(device, stream, what, fn, rope._ptr, xp, xs, op, os_, code, n, heads, pp, ps, 1 if inverse else 0)
     return out
 
 

@@ -88,7 +88,8 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// What a block does at a time: units k0 .. k1 - 1 of a list, KV head h of sequence s.
+// What a block does at a time: units k0 .. k1 - 1 of a list.  A list is a KV head of sequence s, or one of its row tiles:
+// number h = head x row tiles + tile.
 struct Piece {
     Seq q;
     int s, h, k0, k1;
@@ -114,8 +115,9 @@ __device__ __forceinline__ void attend_piece(const PagedAttnParams& p, RowsSmem<
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const Seq& q = pc.q;
-    const int s = pc.s, h = pc.h;
-    const int rows = q.n * p.group;  // at most 8 NR, as max_new new tokens have
+    const int s = pc.s, h = pc.h / p.row_tiles, row0 = (pc.h - h * p.row_tiles) * (8 * NR);
+    const int rows = min(8 * NR, q.n * p.group - row0);
+    if (rows <= 0) return;  // (so do the list's other parts)
     const int j0 = pc.k0 * kUnit, j1 = min(q.kv, pc.k1 * kUnit);
     uint8_t* st = sh.stages[warp];
     const int P = 1 << p.g.page_shift;
@@ -186,8 +188,8 @@ __device__ __forceinline__ void attend_piece(const PagedAttnParams& p, RowsSmem<
     int limit[NR][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-        const int rr = 8 * r + g;
-        live[r] = rr < rows;
+        const int rr = row0 + 8 * r + g;
+        live[r] = rr < row0 + rows;
         const int tok = live[r] ? rr / p.group : 0, head = h * p.group + (live[r] ? rr - tok * p.group : 0);
         qrow[r] = p.q + static_cast<int64_t>(q.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D;
         const int lim = !live[r] ? 1 << 30 : p.causal ? max(0, q.kv - q.n + tok + 1) : q.kv;
@@ -433,7 +435,7 @@ __device__ __forceinline__ void attend_piece(const PagedAttnParams& p, RowsSmem<
         }
     __syncthreads();
     auto store_out = [&](int r, int d, float4 v, float M, float L) {
-        const int tok = r / p.group, head = h * p.group + r - tok * p.group;
+        const int tok = (row0 + r) / p.group, head = h * p.group + row0 + r - tok * p.group;
         const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // a sum that is not a number stays one
         *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q.q0 + tok) * p.out_stride +
                                   static_cast<int64_t>(head) * D + d) =
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kRowsThreads, grid_blocks(NR)) paged4_rows_ker
     pc.k1 = min(units, pc.k0 + per);
     pc.parts = (units + per - 1) / per;
     pc.whole = pc.parts == 1;
-    pc.counter = pc.s * p.g.kv_heads + pc.h;
+    pc.counter = pc.s * gridDim.y + pc.h;
     pc.first = pc.counter * p.splits;
     pc.mine = pc.first + blockIdx.x;
     pc.step = 1;
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(kRowsThreads, line_blocks(NR)) paged4_line_ker
     __shared__ int64_t u_end;
     __shared__ int sums[2][kRowsWarps];
     __shared__ Piece start;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hk = p.g.kv_heads;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hk = p.g.kv_heads * p.row_tiles;  // lists of a sequence
 
     // ---- a thread sums over `per` sequences (512 at most, of 65,536 units at most)
     const int per = (p.g.seqs + kRowsThreads - 1) / kRowsThreads;
@@ -695,7 +697,8 @@ cudaError_t launch_rows(PagedAttnParams& p, cudaStream_t s) {
     static_assert(kPlaces * part_floats<D, NR>() * sizeof(float) <= (32u << 20) && kPlaces <= 16384, "places in the workspace");
     // The grid's way while all blocks are there at once with four units each at most.  (Two units stay together, but for few
     // blocks.)
-    const int64_t lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads;
+    p.row_tiles = static_cast<int>((static_cast<int64_t>(p.g.max_new) * p.group + 8 * NR - 1) / (8 * NR));
+    const int64_t lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads * p.row_tiles;
     const int64_t units = std::max(1, (p.g.max_kv + kUnit - 1) / kUnit);
     int64_t splits = std::min<int64_t>(std::max<int64_t>(kGrid / lists, 1), units);
     const int64_t least = units > 2 && lists * splits <= 2 * 152 ? 1 : 2;
@@ -704,18 +707,24 @@ cudaError_t launch_rows(PagedAttnParams& p, cudaStream_t s) {
     if (lists * splits <= kGrid && per <= 4) {
         p.split_tokens = static_cast<int>(per) * kUnit;
         p.splits = static_cast<int>(splits);
-        paged4_rows_kernel<D, NR><<<dim3(p.splits, p.g.kv_heads, p.g.seqs), kRowsThreads, 0, s>>>(p);
+        paged4_rows_kernel<D, NR><<<dim3(p.splits, p.g.kv_heads * p.row_tiles, p.g.seqs), kRowsThreads, 0, s>>>(p);
     } else {
         paged4_line_kernel<D, NR><<<kLine, kRowsThreads, 0, s>>>(p);
     }
     return cudaGetLastError();
 }
 
+// Up to 32 rows per KV head as tiles of 8 or 16 rows, which read the codes again (the second time from L2, mostly): 32
+// sequences x 8,000 tokens x 8 KV heads x 128 with 32 rows 146 us, 199 as a tile of the tcgen05 kernel, which takes as
+// long for 17 rows as for 128; 9 of 1,021 to 12,007 with 20 rows 47 and 78; 16 of 500 with 32 rows 10.4 and 15.3.  With 48
+// rows 210 us against 200.
+constexpr int kRowsFew = 32;
+
 template <int D>
 cudaError_t launch_attention_d(PagedAttnParams& p, size_t part_floats_max, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
     if (rows <= 8) return launch_rows<D, 1>(p, s);
-    if (rows <= 16) return launch_rows<D, 2>(p, s);
+    if (rows <= kRowsFew) return launch_rows<D, 2>(p, s);
     return launch_paged4_tc(p, D, part_floats_max, s);
 }
 

@@ -369,6 +369,15 @@ def test_attend_few_rows(rc, seqs, hq, hk, dim, page, causal):
     s.check_attend(bf16(s.rng, s.tokens, hq, dim), causal)
 
 
+@pytest.mark.parametrize("seqs,hq,hk", [([(4, 300), (1, 70), (0, 5), (3, 3)], 8, 1), ([(4, 5000), (2, 40), (1, 3000)], 16, 2), ([(32, 50)], 1, 1),
+                                        ([(3, 700)] * 9, 16, 2)])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (128, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_two_row_tiles(rc, seqs, hq, hk, dim, page, causal):
+    s = Setup(rc, seqs, hk, dim, page, seed=dim + page)
+    s.check_attend(bf16(s.rng, s.tokens, hq, dim), causal)
+
+
 TILE_CASES = [
     ([(17, 17)], 1, 1), ([(40, 300), (1, 129), (0, 9), (90, 90)], 2, 1), ([(130, 257)], 3, 1), ([(300, 700), (5, 1200)], 4, 2),
     ([(33, 4000)], 2, 2),
