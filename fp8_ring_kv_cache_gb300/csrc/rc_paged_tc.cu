@@ -248,7 +248,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
 
         auto unit = [&](int u) -> bool {
             const int j = tile_of(u);
-            // V of this unit and K of unit u + 2, tested now and looked at after the softmax
+            if (!warp_wait(&bars[T_S_FULL + i], (u >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
+            // V of this unit and K of unit u + 2, tested now and looked at after the softmax.  (Not before the scores are
+            // there: with one row tile K of unit u lies in the same buffer, and while it is not in place the test would
+            // answer for the phase before.)
             const int jk = tile_of(u + 2);
             const bool want_k = u + 2 < U;
             bool vk = true;
@@ -256,7 +259,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
                 vk = mbar_test(&bars[T_V_FULL + (j & 1)], (j >> 1) & 1);
                 if (want_k) vk = mbar_test(&bars[T_K_FULL + (jk & 1)], (jk >> 1) & 1) && vk;
             }
-            if (!warp_wait(&bars[T_S_FULL + i], (u >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
             tc_fence_after();
             const int room = limit - j * kTileN;  // columns the row sees
             uint32_t v[128];
