@@ -595,3 +595,192 @@ def test_a_workspace_for_both_kinds_of_cache(rc):
         s.check_attend(q, True, got=got)
         assert want is None or torch.equal(want, got[0])
         want = got[0]
+
+
+@pytest.mark.parametrize("new,hq", [(1, 6), (3, 5), (4, 8)])
+def test_a_line_of_many_lists(rc, new, hq):
+    """More sequences than a block has threads, of lengths from none to thousands, some without new tokens: equal stretches
+    of work, which begin and end anywhere.  The same twice, bit for bit."""
+    rng = np.random.default_rng(new)
+    seqs = [(int(rng.integers(0, new + 1)), int(np.exp(rng.uniform(0, np.log(2500))))) for _ in range(300)]
+    seqs[7], seqs[8], seqs[299] = (new, 0), (0, 0), (new, 3000)
+    s = Setup(rc, seqs, 2, 64, 32, seed=new)
+    q = bf16(s.rng, s.tokens, 2 * hq, 64)
+    got = s.check_attend(q, True, heads=[0, hq, 2 * hq - 1])
+    again = s.attend(q.cuda(), True)
+    assert np.array_equal(got[0], again[0].double().cpu().numpy()) and np.array_equal(got[1], again[1].double().cpu().numpy())
+
+
+@pytest.mark.parametrize("new,hq", [(1, 2), (2, 8), (5, 8)])
+def test_a_graph_over_growing_lengths(rc, new, hq):
+    """One captured call, replayed as the lengths on the device change from a few tokens to thousands and back."""
+    s = Setup(rc, [(new, 4000 + 40 * i) for i in range(40)], 2, 64, 128, seed=new, max_kv=8192)
+    s.meta["table"] = np.concatenate([s.meta["table"], np.zeros((40, 64 - s.meta["table"].shape[1]), np.int32)], 1)
+    s.upload()
+    q = bf16(s.rng, s.tokens, hq, 64)
+    qd, out, lse = q.cuda(), torch.empty(q.shape, dtype=torch.bfloat16, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+    s.cache.attend(s.batch, qd, out, lse=lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.cache.attend(s.batch, qd, out, lse=lse)
+    full = s.meta["kv_len"].copy()
+    for share in (0.0, 0.1, 1.0, 0.01):
+        s.meta["kv_len"] = np.maximum((full * share).astype(np.int32), new if share else 0)
+        s.kv_len.copy_(dev(s.meta["kv_len"]))
+        graph.replay()
+        s.cache.sync()
+        s.check_attend(q, True, got=(out, lse), heads=[0, hq - 1])
+
+
+@pytest.mark.parametrize("new,hq", [(1, 4), (3, 8), (20, 4)])
+def test_pages_far_into_a_large_pool(rc, new, hq):
+    """Codes past 2^32 bytes and scales past 2^31 of their pool."""
+    dim, page, hk = 128, 64, 1
+    s = Setup(rc, [(new, 700), (new, 90)], hk, dim, page, seed=new)
+    pages, small = (1 << 32) // (page * dim // 2) + 4096 * 900, s.pool["kcodes"].shape[0]
+    cache = rc.PagedKVCache4.empty(pages=pages, kv_heads=hk, head_dim=dim, page_tokens=page)
+    assert cache.kcodes.numel() > 1 << 34 and cache.kscale.numel() > 1 << 31
+    at = dev(np.linspace(pages - 1, pages // 2, small).astype(np.int64))
+    for k, v in s.pool.items():
+        getattr(cache, k)[at] = dev(v)
+    table = s.meta["table"]
+    far = np.where(table < 0, -1, at.cpu().numpy()[np.maximum(table, 0)]).astype(np.int32)
+    batch = rc.PagedBatch(dev(far), s.kv_len, s.q_start, tokens=s.tokens, max_new=s.max_new, max_kv=s.max_kv)
+    q = bf16(s.rng, s.tokens, hq, dim)
+    out, lse = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+    cache.attend(batch, q.cuda(), out, lse=lse)
+    cache.sync()
+    s.check_attend(q, True, got=(out, lse))
+    K, V = bf16(s.rng, s.tokens, hk, dim), bf16(s.rng, s.tokens, hk, dim)
+    cache.write(batch, K.cuda(), V.cuda())
+    cache.sync()
+    want, _ = s.want_write(K, V, None, None)
+    for k, v in want.items():
+        assert np.array_equal(getattr(cache, k)[at].cpu().numpy(), v), k
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_pages_on_a_16_byte_boundary(rc, dim):
+    """Pages whose address is a multiple of 16 bytes but not of 32 give the same bits."""
+    s = Setup(rc, [(3, 200), (150, 600)], 2, dim, 16, seed=95)
+    small = Setup(rc, [(1, 300), (2, 90)], 2, dim, 16, seed=96)
+
+    def moved(t):
+        flat = torch.zeros(t.numel() + 64, dtype=torch.uint8, device="cuda")
+        at = 16 + (-flat.data_ptr()) % 32
+        new = flat[at:at + t.numel()].view(t.shape)
+        assert new.data_ptr() % 32 == 16
+        return new.copy_(t)
+
+    for x in (s, small):
+        q, K = bf16(x.rng, x.tokens, 4, dim).cuda(), bf16(x.rng, x.tokens, 2, dim).cuda()
+        a = x.attend(q, True)
+        x.cache.write(x.batch, K, K)
+        pages = x.held()
+        x.upload()
+        x.cache = rc.PagedKVCache4(*[moved(getattr(x.cache, k)) for k in ("kcodes", "vcodes", "kscale", "vscale")])
+        b = x.attend(q, True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        x.cache.write(x.batch, K, K)
+        for k, v in x.held().items():
+            assert np.array_equal(v, pages[k])
+
+
+def test_a_wait_that_runs_out_is_reported(rc):
+    s = Setup(rc, [(200, 900), (30, 400)], 2, 128, 64, seed=11)
+    q = bf16(s.rng, s.tokens, 4, 128).cuda()
+    good = s.attend(q, True)
+    rc.rc_paged_set_wait_limit(0)
+    try:
+        s.cache.attend(s.batch, q, torch.zeros_like(q))
+        with pytest.raises(rc.RcError) as e:
+            s.cache.sync()
+    finally:
+        rc.rc_paged_set_wait_limit(2_000_000_000)
+    assert e.value.status == rc.RC_ERR_TIMEOUT
+    s.cache.sync()
+    again = s.attend(q, True)
+    assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+
+
+def test_new_tokens_that_the_length_does_not_count(rc):
+    s = Setup(rc, [(5, 4), (3, 9)], 2, 64, 16, seed=12)
+    K = bf16(s.rng, s.tokens, 2, 64)
+    before = s.held()
+    s.cache.write(s.batch, K.cuda(), K.cuda())
+    with pytest.raises(rc.RcError) as e:
+        s.cache.sync()
+    assert e.value.status == rc.RC_ERR_ARG
+    first = int(s.meta["table"][0, 0])
+    got = s.held()
+    for k in got:
+        assert np.array_equal(got[k][first], before[k][first])
+    assert not np.array_equal(got["kcodes"], before["kcodes"])  # (the other sequence's tokens are there)
+
+
+def test_refusals_of_tensors(rc):
+    s = Setup(rc, [(3, 20)], 2, 64, 16, seed=13)
+    form = rc.RopeForm(64)
+    K, q = bf16(s.rng, 3, 2, 64).cuda(), bf16(s.rng, 3, 4, 64).cuda()
+    pos, out = torch.zeros(1, 3, dtype=torch.int32, device="cuda"), torch.empty(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    c, b = s.cache, s.batch
+    for bad in (lambda: c.write(b, K, K, pos), lambda: c.write(b, K, K, pos, rc.RopeForm(128)), lambda: c.write(b, K[:2], K, pos, form),
+                lambda: c.write(b, K, K.transpose(1, 2).contiguous().transpose(1, 2), pos, form), lambda: c.write(b, K, K, pos[:, :2], form),
+                lambda: c.attend(b, q[0], out), lambda: c.attend(b, q, out[:, :2]), lambda: c.attend(b, q, out, lse=torch.empty(3, 3, device="cuda")),
+                lambda: rc.rc_rope_turn(q, pos, rc.RopeForm(128)), lambda: rc.rc_rope_turn(q, pos[0], form),
+                lambda: rc.rc_rope_turn(q[:2], pos[:, :2], form, out=q[1:]), lambda: rc.rc_rope_turn(q[0], pos, form)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: c.write(b, K, K, None, form), lambda: c.write(b, K.float(), K, pos, form), lambda: c.attend(b, q.cpu(), out),
+                lambda: c.attend(b, q, out.float()), lambda: rc.rc_rope_turn(q.half(), pos, form), lambda: rc.rc_rope_turn(q.cpu(), pos, form),
+                lambda: rc.rc_rope_turn(q, pos.long(), form), lambda: rc.PagedKVCache4(c.kcodes.cpu(), c.vcodes, c.kscale, c.vscale),
+                lambda: rc.PagedKVCache4(c.kcodes, c.vcodes.float(), c.kscale, c.vscale)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(ValueError):
+        rc.PagedKVCache4(c.kcodes, c.kcodes, c.kscale, c.vscale)
+    with pytest.raises(ValueError):
+        rc.PagedKVCache4(c.kcodes, c.vcodes, c.kscale[:, :, :2], c.vscale)
+    with pytest.raises(rc.RcError) as e:  # queries and results in one place
+        c.attend(b, q, q)
+    assert e.value.status == rc.RC_ERR_ARG
+    with pytest.raises(rc.RcError) as e:  # heads that the KV heads do not divide
+        c.attend(b, bf16(s.rng, 3, 3, 64).cuda(), torch.empty(3, 3, 64, dtype=torch.bfloat16, device="cuda"))
+    assert e.value.status == rc.RC_ERR_ARG
+    c.sync()
+
+
+def test_rope_turn_gradient_in_a_graph_and_on_another_stream(rc):
+    """Forward and backward captured together, replayed on other inputs; and recorded on a stream of the caller's."""
+    form = FORMS[3]
+    f, rng = make_form(rc, form), np.random.default_rng(20)
+    pos = rng.integers(0, 50000, (3, 12)).astype(np.int32)
+    pd, dy = dev(pos), torch.from_numpy(rng.standard_normal((12, 2, 128)).astype(np.float32))
+    leaf = torch.zeros(12, 2, 128, device="cuda", requires_grad=True)
+    dyd = dy.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            (grad,) = torch.autograd.grad(rc.rc_rope_turn(leaf, pd, f), leaf, dyd)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = rc.rc_rope_turn(leaf, pd, f)
+        (grad,) = torch.autograd.grad(y, leaf, dyd)
+    for seed in (1, 2):
+        x = torch.from_numpy(np.random.default_rng(seed).standard_normal((12, 2, 128)).astype(np.float32))
+        leaf.data.copy_(x)
+        dy = torch.from_numpy(np.random.default_rng(seed + 9).standard_normal((12, 2, 128)).astype(np.float32))
+        dyd.copy_(dy)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_turn(form, x, pos, y, 1.0)
+        check_turn(form, dy, pos, grad, -1.0)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    y = rc.rc_rope_turn(leaf, pd, f, stream=other)
+    torch.cuda.current_stream().wait_stream(other)
+    (grad,) = torch.autograd.grad(y, leaf, dyd)
+    torch.cuda.synchronize()
+    check_turn(form, dy, pos, grad, -1.0)
