@@ -44,6 +44,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // Eight codes of a word as four pairs of fp16 numbers, in order.
 __device__ __forceinline__ void codes8_f16(uint32_t w, uint32_t (&r)[4]) {
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"

@@ -25,7 +25,7 @@ namespace rc {
 namespace {
 
 constexpr int kRun = kWriteRun;
-constexpr int kMaxHeads = 4;        // of a block
+constexpr int kMaxHeads = 6;        // of a block
 constexpr float kDown = 0x1p-8f;
 
 // How a lane comes by what its dims are paired with.
@@ -159,19 +159,15 @@ __device__ __forceinline__ uint32_t largest_bits(const uint4& w) {
 }
 constexpr uint32_t kInfBits = 0x7f80u;
 
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
 template <int D, Partner PART>
-__global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(const __grid_constant__ Paged4WriteParams p, int runs, int heads_per_block) {
+__global__ void __launch_bounds__(kRun * D / 8, 384 / D) paged4_write_kernel(const __grid_constant__ Paged4WriteParams p, int runs, int heads_per_block) {
     constexpr int LANES = D / 8;  // of one token
     constexpr int kThreads = kRun * LANES;
     constexpr int NB = D / kBlock4;
-    constexpr int kCodeJobs = 2 * LANES;  // of a head: V's codes of 8 dims of 8 tokens each
+    constexpr int kCodeJobs = LANES;  // of a head: V's codes of 8 dims of the run each
     __shared__ float2 table[kRun * D / 2];
     __shared__ uint32_t scode[kMaxHeads][kRun][LANES + 1];             // V's codes
-    __shared__ uint32_t sold[8][kMaxHeads * kCodeJobs];                // the words that they go into, of a run that is not all new
+    __shared__ uint2 sold[8][kMaxHeads * kCodeJobs];                   // the words that they go into, of a run that is not all new
     __shared__ __align__(16) uint8_t sscale[kMaxHeads][2][NB][kRun];   // K's and V's scale bytes
     __shared__ uint16_t skey[PART == kAnywhere ? kThreads * 8 : 1];    // K's rows
     const int s = blockIdx.x / runs, run = blockIdx.x % runs;
@@ -196,12 +192,18 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(con
 
     const __nv_bfloat16* kr = p.K + row * p.k_stride;
     const __nv_bfloat16* vr = p.V + row * p.v_stride;
-    uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-    auto fetch = [&](int h) {
-        kw = ldg_nc_na_v4(kr + static_cast<size_t>(h) * D + c * 8);
-        vw = ldg_nc_na_v4(vr + static_cast<size_t>(h) * D + c * 8);
+    struct Words {
+        uint4 k, v;
     };
-    if (live) fetch(h0);
+    auto fetch = [&](Words& w, int h) {
+        w.k = ldg_nc_na_v4(kr + static_cast<size_t>(h) * D + c * 8);
+        w.v = ldg_nc_na_v4(vr + static_cast<size_t>(h) * D + c * 8);
+    };
+    Words even{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, odd = even;
+    if (live) {
+        fetch(even, h0);
+        if (heads > 1) fetch(odd, h0 + 1);
+    }
 
     // the tokens' g (cos, sin) at 2^-8, by the lanes that have the token's row.  A sine of 0 says that nothing is rounded:
     // where it is 0 only in fp32, it gets its value, the angle itself
@@ -230,14 +232,13 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(con
     const int page = check_page(p.g, entry) ? entry : -1;
     if (page < 0) return;
     const size_t at0 = static_cast<size_t>(page) * p.g.kv_heads + h0;  // of the first head
-    auto codes_of = [&](int job) {  // the first of its eight words, P / 8 words apart
-        const int hl = job / kCodeJobs, c8 = job % LANES, t0 = 8 * ((job / LANES) & 1);
-        return reinterpret_cast<uint32_t*>(p.g.vcodes + ((at0 + hl) * D + 8 * c8) * (P / 2) + (off + t0) / 2);
+    auto codes_of = [&](int job) {  // the first of its eight pairs of words, P / 16 pairs apart
+        return reinterpret_cast<uint2*>(p.g.vcodes + ((at0 + job / kCodeJobs) * D + 8 * (job % kCodeJobs)) * (P / 2) + off / 2);
     };
     if (b - a < kRun)
         for (int i = threadIdx.x; i < heads * kCodeJobs; i += kThreads)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) cp_async4(&sold[j][i], codes_of(i) + j * (P / 8));
+            for (int j = 0; j < 8; ++j) cp_async8(&sold[j][i], codes_of(i) + j * (P / 16));
     __syncwarp();
     float2 cs[4], sn[4];
     uint32_t partner[4] = {0, 0, 0, 0};  // kAnywhere: where in the row's 16-bit numbers, two a word
@@ -266,13 +267,14 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(con
             sn[j] = make_float2(ss[2 * j], ss[2 * j + 1]);
         }
     }
-    const bool some_exact = __any_sync(0xffffffffu, exact != 0u);
+    const bool some_exact = __any_sync(0xffffffffu, exact != 0u), all_exact = __all_sync(0xffffffffu, exact == 0xffffffffu);
     // lanes of the warp that have the token's row, and the one that has what this one's dims are paired with
     const uint32_t row_lanes = (LANES == 16 ? 0xffffu : 0xffu) << (lane & ~(LANES - 1));
     const int partner_lane = (lane & ~(LANES - 1)) + (PART == kVector ? mine.partner / 8 : c);
 
-    for (int h = h0; h < h1; ++h) {
+    auto head = [&](int h, Words& words) {
         const int hl = h - h0;
+        const uint4 kw = words.k, vw = words.v;
         float2 x[4], xp[4];
         open_bf16(kw, x);
         const uint32_t kmost = largest_bits(kw), vmost = largest_bits(vw);
@@ -302,9 +304,6 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(con
         }
         const bool kbad = (__ballot_sync(0xffffffffu, kmost >= kInfBits) & row_lanes) != 0u;
         const bool vbad = (__ballot_sync(0xffffffffu, vmost >= kInfBits) & row_lanes) != 0u;
-        const uint4 vnow = vw;
-        if (live && h + 1 < h1) fetch(h + 1);  // the next head is on its way
-
         // K
         float2 y[4];
         float amax = 0.f;
@@ -331,20 +330,23 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(con
         uint32_t kb = scale4_byte(amax);
         bool open = err2 > 0.f && scale4_open(amax, err2, kb);
         const float scale = scale4_value(kb) * kDown, inv = kb == 0u ? 0.f : reciprocal(scale);
-        float lo[8], hi[8];
-        const float reach = slack * inv;
+        uint32_t kc = 0u, unsure = 0u;
+        if (!all_exact) {
+            float lo[8], hi[8];
+            const float reach = slack * inv;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 w = mul2(y[j], make_float2(inv, inv));
-            const float2 tol = mul2(make_float2(fabsf(x[j].x) + fabsf(xp[j].x), fabsf(x[j].y) + fabsf(xp[j].y)), make_float2(reach, reach));
-            const float2 u = add2(w, tol);
-            lo[2 * j] = w.x - tol.x;
-            lo[2 * j + 1] = w.y - tol.y;
-            hi[2 * j] = u.x;
-            hi[2 * j + 1] = u.y;
+            for (int j = 0; j < 4; ++j) {
+                const float2 w = mul2(y[j], make_float2(inv, inv));
+                const float2 tol = mul2(make_float2(fabsf(x[j].x) + fabsf(xp[j].x), fabsf(x[j].y) + fabsf(xp[j].y)), make_float2(reach, reach));
+                const float2 u = add2(w, tol);
+                lo[2 * j] = w.x - tol.x;
+                lo[2 * j + 1] = w.y - tol.y;
+                hi[2 * j] = u.x;
+                hi[2 * j + 1] = u.y;
+            }
+            kc = codes8(lo);
+            unsure = (kc ^ codes8(hi)) & ~exact;
         }
-        uint32_t kc = codes8(lo);
-        uint32_t unsure = (kc ^ codes8(hi)) & ~exact;
         if (some_exact) kc = (kc & ~exact) | (codes8_of_quotients(y, scale, inv) & exact);
         if (!live || kbad) {
             open = false;
@@ -385,7 +387,8 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(con
         uint32_t vb = scale4_byte(__uint_as_float(vtop << 16) * kDown);
         const float vscale = scale4_value(vb), vinv = vb == 0u ? 0.f : reciprocal(vscale);
         float2 v[4];
-        open_bf16(vnow, v);
+        open_bf16(vw, v);
+        if (live && h + 2 < h1) fetch(words, h + 2);  // the head after the next
         uint32_t vc = codes8_of_quotients(v, vscale, vinv);
         if (vbad) {
             vc = 0u;
@@ -397,26 +400,36 @@ __global__ void __launch_bounds__(kRun * D / 8, 512 / D) paged4_write_kernel(con
             sscale[hl][0][c >> 1][tok] = static_cast<uint8_t>(kb);
             sscale[hl][1][c >> 1][tok] = static_cast<uint8_t>(vb);
         }
+    };
+#pragma unroll 1
+    for (int h = h0; h < h1; h += 2) {
+        head(h, even);
+        if (h + 1 < h1) head(h + 1, odd);
     }
     cp_async_wait_all();
     __syncthreads();
     for (int i = threadIdx.x; i < heads * kCodeJobs; i += kThreads) {
-        const int hl = i / kCodeJobs, c8 = i % LANES, t0 = 8 * ((i / LANES) & 1);
-        const int m0 = max(a, t0) - t0, m1 = min(b, t0 + 8) - t0;  // new ones among the eight
-        if (m1 <= m0) continue;
-        uint32_t* dst = codes_of(i);
-        const int step = P / 8;  // words between dims
-        uint32_t w[8];
-        const uint32_t mask = (m1 == 8 ? 0xffffffffu : (1u << (4 * m1)) - 1u) & ~((1u << (4 * m0)) - 1u);
+        const int hl = i / kCodeJobs, c8 = i % kCodeJobs;
+        uint2* dst = codes_of(i);
+        const int step = P / 16;  // pairs of words between dims
+        uint32_t w[2][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = scode[hl][t0 + j][c8];
-        transpose_codes(w);
-        if (mask == 0xffffffffu) {
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dst[j * step] = w[j];
+            for (int j = 0; j < 8; ++j) w[half][j] = scode[hl][8 * half + j][c8];
+            transpose_codes(w[half]);
+        }
+        if (b - a == kRun) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dst[j * step] = make_uint2(w[0][j], w[1][j]);
         } else {
+            const uint64_t mask = (b == kRun ? ~0ull : (1ull << (4 * b)) - 1ull) & ~((1ull << (4 * a)) - 1ull);
+            const uint32_t m0 = static_cast<uint32_t>(mask), m1 = static_cast<uint32_t>(mask >> 32);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dst[j * step] = (w[j] & mask) | (sold[j][i] & ~mask);
+            for (int j = 0; j < 8; ++j) {
+                const uint2 old = sold[j][i];
+                dst[j * step] = make_uint2((w[0][j] & m0) | (old.x & ~m0), (w[1][j] & m1) | (old.y & ~m1));
+            }
         }
     }
     for (int i = threadIdx.x; i < heads * 2 * NB; i += kThreads) {
@@ -434,7 +447,7 @@ template <int D, Partner PART>
 cudaError_t launch_part(const Paged4WriteParams& p, cudaStream_t s) {
     const int runs = static_cast<int>(paged_write_runs(p.g));
     const int64_t blocks = paged_write_blocks(p.g);
-    const int hpb = blocks * ((p.g.kv_heads + 3) / 4) >= 152 * 3 ? 4 : 2;
+    const int hpb = blocks * ((p.g.kv_heads + kMaxHeads - 1) / kMaxHeads) >= 152 * 2 ? kMaxHeads : 2;
     dim3 grid(static_cast<unsigned>(blocks), (p.g.kv_heads + hpb - 1) / hpb);
     paged4_write_kernel<D, PART><<<grid, kRun * D / 8, 0, s>>>(p, runs, hpb);
     return cudaGetLastError();
