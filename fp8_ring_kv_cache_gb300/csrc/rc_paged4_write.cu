@@ -328,7 +328,23 @@ __global__ void __launch_bounds__(kRun * D / 8, 384 / D) paged4_write_kernel(con
             if (most + err2 < amax) err2 = 0.f;
         }
         uint32_t kb = scale4_byte(amax);
-        bool open = err2 > 0.f && scale4_open(amax, err2, kb);
+        const __nv_bfloat16* keys = kr + static_cast<size_t>(h) * D;
+        bool open = live && !kbad && err2 > 0.f && scale4_open(amax, err2, kb);
+        if (__any_sync(0xffffffffu, open)) {  // the scale may be another: the sums that may be the block's largest, taken again
+            const bool other = __shfl_xor_sync(0xffffffffu, open ? 1 : 0, 1) != 0;  // (all lanes, before anything is decided)
+            open = open || other;
+            uint32_t may = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) may |= (fabsf(j & 1 ? y[j / 2].y : y[j / 2].x) >= amax - 2.f * err2 ? 1u : 0u) << j;
+            float most = 0.f;
+            while (open && may != 0u) {
+                most = fmaxf(most, fabsf(exact_sum(p, keys, row, 8 * c + __ffs(may) - 1)));
+                may &= may - 1;
+            }
+            __syncwarp();
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            if (open) kb = scale4_byte(most);
+        }
         const float scale = scale4_value(kb) * kDown, inv = kb == 0u ? 0.f : reciprocal(scale);
         uint32_t kc = 0u, unsure = 0u;
         if (!all_exact) {
@@ -348,30 +364,7 @@ __global__ void __launch_bounds__(kRun * D / 8, 384 / D) paged4_write_kernel(con
             unsure = (kc ^ codes8(hi)) & ~exact;
         }
         if (some_exact) kc = (kc & ~exact) | (codes8_of_quotients(y, scale, inv) & exact);
-        if (!live || kbad) {
-            open = false;
-            unsure = 0u;
-        }
-        const __nv_bfloat16* keys = kr + static_cast<size_t>(h) * D;
-        if (__any_sync(0xffffffffu, open)) {  // the scale may be another: both lanes of the block take all their sums again
-            const bool other = __shfl_xor_sync(0xffffffffu, open ? 1 : 0, 1) != 0;  // (all lanes, before anything is decided)
-            open = open || other;
-            float z[8];
-            amax = 0.f;
-            if (open) {
-#pragma unroll 1
-                for (int j = 0; j < 8; ++j) z[j] = exact_sum(p, keys, row, 8 * c + j);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(z[j]));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            if (open) {
-                kb = scale4_byte(amax);
-                kc = unsure = 0u;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) kc |= code_exactly(z[j], scale4_value(kb) * kDown) << (4 * j);
-            }
-        }
+        if (!live || kbad) unsure = 0u;
         while (unsure != 0u) {
             const int j = (__ffs(unsure) - 1) >> 2;
             unsure &= ~(0xfu << (4 * j));
