@@ -297,7 +297,7 @@ struct PagedAttnParams {
     float sm_log2;     // log2(e) / sqrt(head_dim)
     int split_tokens;  // cached tokens of one split (a multiple of 256)
     int splits;        // splits of a sequence of max_kv tokens
-    int row_tiles;     // tcgen05 kernel: row tiles of a sequence of max_new tokens
+    int row_tiles;     // kernels with row tiles: those of a sequence of max_new tokens
     float* part;       // workspace: partial results
     int* counters;     // workspace: arrivals of the splits, all zero between calls
     uint64_t wait_ns;

@@ -27,6 +27,12 @@
 // looks which group is ready: 119 us; units of 64 tokens with two places of scores a group,
 // so that scores are always ahead: 138 us, as products of 64 columns take as long as
 // those of 128.)
+// 757 queries x 5,788 tokens x 48 heads x 128: 87.3 us, 1.23 PFLOP/s, 0.65 of what a
+// library product of bf16 matrices reaches; the tensor cores work 55 % of the time.  A
+// tile takes 3,500 cycles for both groups, 1,750 each for products of 1,024.  By
+// arithmetic shared memory explains that (not measured by itself): a score product reads
+// 8 KB in 64 cycles, all that 128 bytes a cycle give, and the converters' stores, 64 KB a
+// tile, come in between.
 // A row sees the cached tokens from the first on, so a token whose V is not a number is
 // remembered by the first such one's number: the row has it if it sees that far.
 #include "rc_paged4.cuh"
