@@ -182,6 +182,10 @@ class RopeAxes:
                                      RC_ROPE_SHARED_FREQS if shared_freqs else 0), "rc_rope_plan_init")
         self._ptr = ctypes.addressof(self.plan)
 
+    def __setstate__(self, state):  # (a deep copy, or one from another process, has numbers of its own)
+        self.__dict__.update(state)
+        self._ptr = ctypes.addressof(self.plan)
+
 
 class _Turn(torch.autograd.Function):
     """The turn with its gradient, the turn back."""

@@ -86,6 +86,10 @@ class RopeForm:
         self.gain = self.form.gain
         self._ptr = ctypes.addressof(self.form)
 
+    def __setstate__(self, state):  # (a deep copy, or one from another process, has numbers of its own)
+        self.__dict__.update(state)
+        self._ptr = ctypes.addressof(self.form)
+
 
 def rc_rope_turn(x, positions, form: RopeForm, out=None, back: bool = False, stream=None):
     """x [n][heads][head_dim] (bf16 or fp32) turned at positions (int32 [axes][n]) in the form's manner, times its gain;

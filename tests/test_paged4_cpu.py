@@ -1,7 +1,9 @@
 """The rotary forms and the 4-bit paged cache without a GPU: the forms' numbers, and every refusal of the C ABI's argument
 checks, which come before any device work (the addresses here are never read)."""
+import copy
 import ctypes
 import functools
+import pickle
 from fractions import Fraction
 
 import numpy as np
@@ -227,3 +229,15 @@ def test_the_tests_own_definitions():
     import torch
     every = torch.from_numpy(pu.E2M1[:, None] * pu.SCALES[None, :pu.TOP + 1])
     assert torch.equal(every.to(torch.bfloat16).double(), every) and torch.equal(every.half().double(), every)
+
+
+@pytest.mark.parametrize("make", [lambda rc: rc.RopeForm(128, layout="halves", gain=1.25), lambda rc: rc.RopeAxes((22, 21, 21))])
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda f: pickle.loads(pickle.dumps(f))])
+def test_a_copy_of_a_form_has_numbers_of_its_own(rc, make, how):
+    """What a call is given is the address of numbers that live as long as the copy, whatever happens to the original."""
+    form = make(rc)
+    numbers = lambda f: f.form if hasattr(f, "form") else f.plan
+    want = bytes(numbers(form))
+    other = how(form)
+    assert other._ptr == ctypes.addressof(numbers(other))
+    assert bytes(numbers(other)) == want
