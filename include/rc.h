@@ -655,7 +655,9 @@ typedef struct rc_paged4_view {
  * Write each sequence's new tokens into its pages: K turned at the tokens'
  * positions (as rc_rope_turn, unrounded), K and V quantised as above.  Arguments and errors as
  * rc_paged_write, with a form of the cache's head_dim; form NULL: K is stored as it comes, and
- * positions are not read (may be NULL).
+ * positions are not read (may be NULL).  A page that gets new tokens belongs to one sequence
+ * and stands once in the part of its row that is written: V's words hold 16 tokens and
+ * are written whole, older tokens with the bits that they have.
  */
 int rc_paged4_write(const rc_paged4_view *view, const rc_paged_batch *batch, const void *K_bf16, int64_t k_stride,
                     const void *V_bf16, int64_t v_stride, const int32_t *positions, int64_t pos_stride,
