@@ -297,7 +297,9 @@ struct PagedAttnParams {
     float sm_log2;     // log2(e) / sqrt(head_dim)
     int split_tokens;  // cached tokens of one split (a multiple of 256)
     int splits;        // splits of a sequence of max_kv tokens
-    int row_tiles;     // kernels with row tiles: those of a sequence of max_new tokens
+    int row_tiles;     // kernels with row tiles: those of the longest sequence that they take
+    int few;           // tcgen05 kernels: sequences with up to so many rows a KV head are another kernel's (0: none is)
+    int most;          // 4-bit kernels of few rows: so are those with more than so many
     float* part;       // workspace: partial results
     int* counters;     // workspace: arrivals of the splits, all zero between calls
     uint64_t wait_ns;

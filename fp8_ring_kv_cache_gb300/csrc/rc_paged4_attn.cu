@@ -55,6 +55,13 @@ constexpr int part_floats() {
 // log2 units; -inf: the partial saw nothing).
 __device__ __forceinline__ float join_weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
 
+// Sequence s, without new tokens if it has more rows than this kernel takes.
+__device__ __forceinline__ Seq rows_seq(const PagedAttnParams& p, int s) {
+    Seq q = load_seq(p.g, s);
+    if (q.n * p.group > p.most) q.n = 0;
+    return q;
+}
+
 // Units of a sequence, for one KV head: none without new tokens, one at least with some.
 __device__ __forceinline__ int units_of(const Seq& q) { return q.n == 0 ? 0 : max(1, (q.kv + kUnit - 1) / kUnit); }
 
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(kRowsThreads, grid_blocks(NR)) paged4_rows_ker
     Piece pc;
     pc.s = blockIdx.z;
     pc.h = blockIdx.y;
-    pc.q = load_seq(p.g, pc.s);
+    pc.q = rows_seq(p, pc.s);
     const int units = units_of(pc.q), per = p.split_tokens / kUnit;
     pc.k0 = blockIdx.x * per;
     if (pc.k0 >= units) return;
@@ -592,7 +599,7 @@ __global__ void __launch_bounds__(kRowsThreads, line_blocks(NR)) paged4_line_ker
     const int s_first = min(p.g.seqs, tid * per), s_end = min(p.g.seqs, s_first + per);
     int units = 0, lists = 0;
     for (int s = s_first; s < s_end; ++s) {
-        const int n = units_of(load_seq(p.g, s));
+        const int n = units_of(rows_seq(p, s));
         units += n;
         lists += n > 0;
     }
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(kRowsThreads, line_blocks(NR)) paged4_line_ker
         }
         if (before <= u && u < before + (units + static_cast<int64_t>(l.gap) * lists) * hk) {  // one thread: the place of u
             for (int s = s_first; s < s_end; ++s) {
-                const Seq q = load_seq(p.g, s);
+                const Seq q = rows_seq(p, s);
                 const int n = units_of(q) + l.gap;
                 const int64_t all = q.n == 0 ? 0 : static_cast<int64_t>(n) * hk;
                 if (u < before + all) {
@@ -684,22 +691,24 @@ __global__ void __launch_bounds__(kRowsThreads, line_blocks(NR)) paged4_line_ker
         if (++pc.h == hk) {
             pc.h = 0;
             do {  // (u is in the line: there is one)
-                pc.q = load_seq(p.g, ++pc.s);
+                pc.q = rows_seq(p, ++pc.s);
             } while (pc.q.n == 0 && pc.s + 1 < p.g.seqs);
         }
         __syncthreads();
     }
 }
 
+// Of the sequences with `rows` rows a KV head at most.
 template <int D, int NR>
-cudaError_t launch_rows(PagedAttnParams& p, cudaStream_t s) {
+cudaError_t launch_rows(PagedAttnParams& p, int64_t rows, cudaStream_t s) {
     constexpr int kGrid = 152 * grid_blocks(NR), kLine = 152 * line_blocks(NR);  // blocks at once
     constexpr int kPlaces = kGrid > 2 * kLine ? kGrid : 2 * kLine;
     static_assert(kPlaces * part_floats<D, NR>() * sizeof(float) <= (32u << 20) && kPlaces <= 16384, "places in the workspace");
     // The grid's way while all blocks are there at once with four units each at most: 64 sequences x 1,000 tokens x 8 heads
     // 19.9 us, 25.6 as a line; 8 x 2,000 12.4 and 15.2; one of 4,000 8.4 and 11.5; one of 337 x 2 heads x 64 5.3 and 6.6.
     // (Two units stay together, but for few blocks.)
-    p.row_tiles = static_cast<int>((static_cast<int64_t>(p.g.max_new) * p.group + 8 * NR - 1) / (8 * NR));
+    p.most = static_cast<int>(rows);
+    p.row_tiles = static_cast<int>((rows + 8 * NR - 1) / (8 * NR));
     const int64_t lists = static_cast<int64_t>(p.g.seqs) * p.g.kv_heads * p.row_tiles;
     const int64_t units = std::max(1, (p.g.max_kv + kUnit - 1) / kUnit);
     int64_t splits = std::min<int64_t>(std::max<int64_t>(kGrid / lists, 1), units);
@@ -725,8 +734,18 @@ constexpr int kRowsFew = 32;
 template <int D>
 cudaError_t launch_attention_d(PagedAttnParams& p, size_t part_floats_max, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
-    if (rows <= 8) return launch_rows<D, 1>(p, s);
-    if (rows <= kRowsFew) return launch_rows<D, 2>(p, s);
+    if (rows <= 8) return launch_rows<D, 1>(p, rows, s);
+    if (rows <= kRowsFew) return launch_rows<D, 2>(p, rows, s);
+    // With long sequences in the call, those of a token or a few (what fills the row tiles that one token needs) have a
+    // launch of their own, if as many as half of the sequences can be such.
+    if (p.group <= kRowsFew) {
+        const int one = p.group <= 8 ? 8 : (p.group + 15) / 16 * 16, few = one / p.group;
+        if (p.g.seqs > 1 && 2 * static_cast<int64_t>(p.g.tokens) <= static_cast<int64_t>(p.g.seqs) * (p.g.max_new + few)) {
+            const cudaError_t e = one == 8 ? launch_rows<D, 1>(p, one, s) : launch_rows<D, 2>(p, one, s);
+            if (e != cudaSuccess) return e;
+            p.few = one;
+        }
+    }
     return launch_paged4_tc(p, D, part_floats_max, s);
 }
 

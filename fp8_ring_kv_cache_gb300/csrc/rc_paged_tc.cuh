@@ -31,13 +31,14 @@ __device__ __forceinline__ uint4 cut16(uint4 v, int left) {
 
 // Cached tokens that the rows of a tile see, and how they are split.
 struct TileWork {
-    int rows;    // rows of the sequence's KV head
+    int rows;    // rows of the sequence's KV head (0: none, or another kernel's)
     int seen;    // tokens that the tile's last row sees
     int nsplit;  // splits with work (at least 1)
 };
 __device__ __forceinline__ TileWork tile_work(const PagedAttnParams& p, const Seq& q, int tile) {
     TileWork w;
     w.rows = q.n * p.group;
+    if (w.rows <= p.few) w.rows = 0;
     const int last_new = min(q.n - 1, (tile * kRowsTc + kRowsTc - 1) / p.group);
     w.seen = p.causal ? max(0, q.kv - q.n + last_new + 1) : q.kv;
     w.nsplit = max(1, (w.seen + p.split_tokens - 1) / p.split_tokens);

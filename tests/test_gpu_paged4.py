@@ -784,3 +784,45 @@ def test_rope_turn_gradient_in_a_graph_and_on_another_stream(rc):
     (grad,) = torch.autograd.grad(y, leaf, dyd)
     torch.cuda.synchronize()
     check_turn(form, dy, pos, grad, -1.0)
+
+
+MIXED = [  # single and few new tokens next to long ones; rows at, one under and one over what a single token's tile holds
+    ([(1, 900)] * 5 + [(130, 400)], 6, 1), ([(300, 300)] + [(1, 2000), (2, 50), (3, 70), (0, 4), (1, 0)] * 2, 8, 2),
+    ([(8, 600), (9, 600), (7, 33), (1, 1), (60, 90), (2, 0)], 1, 1), ([(1, 500), (2, 300), (1, 5000), (40, 41)], 16, 1),
+    ([(1, 500), (2, 300), (1, 600), (40, 100)], 17, 1), ([(1, 300), (1, 90), (9, 300)], 33, 1), ([(1, 6000), (20, 6000)], 8, 4),
+    ([(1, 700)] * 70 + [(64, 3000)] + [(1, 40)] * 70, 4, 1),
+]
+
+
+@pytest.mark.parametrize("seqs,hq,hk", MIXED)
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_short_and_long_sequences_in_one_call(rc, seqs, hq, hk, dim, page, causal):
+    s = Setup(rc, seqs, hk, dim, page, seed=dim + len(seqs))
+    q = bf16(s.rng, s.tokens, hq, dim)
+    first = s.check_attend(q, causal)
+    again = s.attend(q.cuda(), causal)
+    assert np.array_equal(first[0], again[0].double().cpu().numpy(), equal_nan=True)
+    assert np.array_equal(first[1], again[1].double().cpu().numpy(), equal_nan=True)
+
+
+def test_a_graph_in_which_sequences_become_short_and_long(rc):
+    """One captured call over 9 sequences whose new tokens change on the device: all short, mixed, and rows of nobody."""
+    s = Setup(rc, [(1, 700 + 90 * i) for i in range(8)] + [(40, 1500)], 2, 64, 32, seed=11, tokens=120, max_new=40)
+    q = bf16(s.rng, 120, 12, 64)
+    qd = q.cuda()
+    out, lse = torch.empty((120, 12, 64), dtype=torch.bfloat16, device="cuda"), torch.empty((120, 12), device="cuda")
+    s.cache.attend(s.batch, qd, out, lse=lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.cache.attend(s.batch, qd, out, lse=lse)
+    for new in ([1] * 9, [1] * 8 + [40], [40, 1, 0, 2, 1, 1, 40, 0, 1], [13] * 9):
+        s.meta["q_start"] = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        s.q_start.copy_(dev(s.meta["q_start"]))
+        n = sum(new)
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        s.cache.sync()
+        s.check_attend(q, True, got=(out, lse), heads=[0, 11])
+        assert (out[n:] == 7.0).all() and (lse[n:] == 7.0).all()
