@@ -94,7 +94,9 @@ __device__ __forceinline__ uint2 ldg_early_v2(const void* p) {
     return r;
 }
 
-template <int D>
+// NUMBERED: the blocks are numbered over the tiles that there are.  (A form of its own: the sum over the lengths that finds a
+// tile made the other one 1 % slower, 486 -> 491 us for 4 prompts of 259 to 2,701 new tokens.)
+template <int D, bool NUMBERED>
 __global__ void __launch_bounds__(kTcThreads, 1) paged4_tc_kernel(PagedAttnParams p) {
     using Lay = Tc4Layout<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -107,7 +109,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged4_tc_kernel(PagedAttnParam
     int b = blockIdx.x;
     const int h = b % p.g.kv_heads;
     b /= p.g.kv_heads;
-    const int s = b % p.g.seqs, tile = p.row_tiles - 1 - b / p.g.seqs, split = blockIdx.y;
+    const int split = blockIdx.y;
+    int s = b % p.g.seqs, tile = p.row_tiles - 1 - b / p.g.seqs;
+    if constexpr (NUMBERED) {
+        s = tile_place(p, b, tile, reinterpret_cast<int*>(smem));
+        if (s < 0) return;
+    }
     const Seq q = load_seq(p.g, s);
     const TileWork tw = tile_work(p, q, tile);
     const int row0 = tile * kRowsTc;
@@ -625,10 +632,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged4_tc_kernel(PagedAttnParam
 
 template <int D>
 cudaError_t launch_d(PagedAttnParams& p, size_t part_floats_max, cudaStream_t s) {
-    static std::atomic<uint64_t> configured{0};
+    static std::atomic<uint64_t> configured[2]{};
     constexpr uint32_t smem = Tc4Layout<D>::kAlloc;
     static_assert(smem <= 227 * 1024, "shared memory over the sm_103 limit");
-    return launch_tiles<D>(paged4_tc_kernel<D>, smem, configured, p, part_floats_max, s);
+    return launch_tiles<D>({paged4_tc_kernel<D, false>, configured[0]}, {paged4_tc_kernel<D, true>, configured[1]}, smem, p, part_floats_max, s);
 }
 
 }  // namespace

@@ -586,7 +586,8 @@ cudaError_t launch_d(PagedAttnParams& p, size_t part_floats_max, cudaStream_t s)
     static std::atomic<uint64_t> configured{0};
     constexpr uint32_t smem = TcLayout<D>::kAlloc;
     static_assert(smem <= 227 * 1024, "shared memory over the sm_103 limit");
-    return launch_tiles<D>(paged_tc_kernel<D>, smem, configured, p, part_floats_max, s);
+    const TilesKernel kernel{paged_tc_kernel<D>, configured};
+    return launch_tiles<D>(kernel, kernel, smem, p, part_floats_max, s);  // (few is 0: never by number)
 }
 
 }  // namespace

@@ -45,6 +45,54 @@ __device__ __forceinline__ TileWork tile_work(const PagedAttnParams& p, const Se
     return w;
 }
 
+// Tile number `number` among the tiles of all sequences (each sequence's last one first): its sequence, or -1 if there are
+// fewer.  By the whole block, with some of its shared memory.
+__device__ __forceinline__ int tile_place(const PagedAttnParams& p, int number, int& tile, int* smem) {
+    constexpr int kWarps = kTcThreads / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (p.g.seqs + kTcThreads - 1) / kTcThreads;
+    const int first = min(p.g.seqs, tid * per), end = min(p.g.seqs, first + per);
+    auto tiles_of = [&](int s) {
+        const int rows = load_seq(p.g, s).n * p.group;
+        return rows <= p.few ? 0 : (rows + kRowsTc - 1) / kRowsTc;
+    };
+    int mine = 0;
+    for (int s = first; s < end; ++s) mine += tiles_of(s);
+    int to = mine;  // up to and with the thread's, of the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, to, o);
+        if (lane >= o) to += x;
+    }
+    if (lane == 31) smem[warp] = to;
+    if (tid == 0) smem[kWarps] = -1;  // (lengths that contradict each other may leave the number to nobody)
+    __syncthreads();
+    int before = to - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int n = smem[w];
+        if (w < warp) before += n;
+        all += n;
+    }
+    if (number >= all) return -1;
+    if (before <= number && number < before + mine) {  // one thread
+        for (int s = first; s < end; ++s) {
+            const int n = tiles_of(s);
+            if (number < before + n) {
+                smem[kWarps] = s;
+                smem[kWarps + 1] = n - 1 - (number - before);
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    const int s = smem[kWarps];
+    tile = smem[kWarps + 1];
+    __syncthreads();
+    return s;
+}
+
 // Joins the splits of each row, in split order: a warp a row.
 template <int D>
 __global__ void __launch_bounds__(256) paged_tc_join_kernel(PagedAttnParams p) {
@@ -111,11 +159,16 @@ __global__ void __launch_bounds__(256) paged_tc_join_kernel(PagedAttnParams p) {
             L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-template <int D, typename Kernel>
-cudaError_t launch_tiles(Kernel* kernel, uint32_t smem, std::atomic<uint64_t>& configured, PagedAttnParams& p, size_t part_floats_max,
+// A kernel, and the devices where its shared memory's limit is set.
+struct TilesKernel {
+    void (*kernel)(PagedAttnParams);
+    std::atomic<uint64_t>& configured;
+};
+
+// numbered: the kernel whose blocks are numbered over the tiles that there are; only for p.few > 0.
+template <int D>
+cudaError_t launch_tiles(const TilesKernel& padded, const TilesKernel& numbered, uint32_t smem, PagedAttnParams& p, size_t part_floats_max,
                          cudaStream_t s) {
-    cudaError_t e = smem_limit_once(kernel, smem, configured);
-    if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(p.g.max_new) * p.group;
     p.row_tiles = static_cast<int>((rows + kRowsTc - 1) / kRowsTc);
     const int64_t blocks = paged_attend_blocks(p.g, rows);
@@ -130,7 +183,21 @@ cudaError_t launch_tiles(Kernel* kernel, uint32_t smem, std::atomic<uint64_t>& c
     const int per = static_cast<int>((p.g.max_kv + want - 1) / want);
     p.split_tokens = std::max(kTileN, (per + kTileN - 1) / kTileN * kTileN);
     p.splits = std::max(1, (p.g.max_kv + p.split_tokens - 1) / p.split_tokens);
-    kernel<<<dim3(static_cast<unsigned>(blocks), p.splits), kTcThreads, smem, s>>>(p);
+    // Where short sequences are another kernel's, most places of the padded grid are empty: unsplit, a block finds its tile
+    // by its number among those that there are.  So many at most: the whole ones of all tokens, and one of each sequence.
+    // (63 single tokens and a chunk of 512 in one call, all with 8,000 cached, 8 x 6 heads x 128: 768 tiles of a KV head in
+    // the padded grid, 286 us in all; 77 numbered ones, 222.)
+    int64_t grid = blocks;
+    const bool by_number = p.few > 0 && p.splits == 1;
+    if (by_number) {
+        const int64_t tokens = p.g.tokens, longer = std::min<int64_t>(p.g.seqs, tokens / (p.few / p.group + 1));
+        grid = std::min(tokens * p.group / kRowsTc + longer, blocks / p.g.kv_heads) * p.g.kv_heads;
+        if (grid == 0) return cudaSuccess;
+    }
+    const TilesKernel& k = by_number ? numbered : padded;
+    cudaError_t e = smem_limit_once(k.kernel, smem, k.configured);
+    if (e != cudaSuccess) return e;
+    k.kernel<<<dim3(static_cast<unsigned>(grid), p.splits), kTcThreads, smem, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
     const int64_t joins = (rows + 7) / 8 * p.g.seqs * p.g.kv_heads;

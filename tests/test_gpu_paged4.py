@@ -826,3 +826,25 @@ def test_a_graph_in_which_sequences_become_short_and_long(rc):
         s.cache.sync()
         s.check_attend(q, True, got=(out, lse), heads=[0, 11])
         assert (out[n:] == 7.0).all() and (lse[n:] == 7.0).all()
+
+
+def test_many_short_and_long_sequences_in_one_call(rc):
+    """More sequences than a block of the tiles' kernel has threads, tiles of lengths that end anywhere, a bad length among them
+    (which is left out and reported; the others are as they were)."""
+    rng = np.random.default_rng(5)
+    seqs = [(1, int(rng.integers(1, 200))) for _ in range(700)]
+    for i in (0, 13, 14, 333, 639, 640, 699):
+        seqs[i] = (int(rng.integers(60, 400)), int(rng.integers(1, 500)))
+    seqs[20], seqs[641] = (0, 3), (1, 0)
+    s = Setup(rc, seqs, 1, 64, 16, seed=6)
+    q = bf16(s.rng, s.tokens, 5, 64)
+    s.check_attend(q, True, heads=[0, 4])
+    good, _ = s.attend(q.cuda(), True)
+    s.kv_len[333] = s.max_kv + 1
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    s.cache.attend(s.batch, q.cuda(), out)
+    with pytest.raises(rc.RcError):
+        s.cache.sync()
+    a, b = int(s.meta["q_start"][333]), int(s.meta["q_start"][334])
+    assert (out[a:b] == 7.0).all()
+    assert torch.equal(out[:a], good[:a]) and torch.equal(out[b:], good[b:])
