@@ -223,10 +223,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged4_tc_kernel(PagedAttnParam
             for (int w = 0; w < 2 && w < n_all; ++w) {
                 if (w == 0 || !two_u) ok = ok && warp_wait(&bars[F_K_FULL + w], 0, ab, kDevTimeoutMma);
                 tc_fence_after();
-                if (ok && elect_one()) issue_qk(w, two_u ? 0 : w);
+                if (elect_one()) {
+                    if (ok)
+                        issue_qk(w, two_u ? 0 : w);
+                    else
+                        mbar_arrive(&bars[F_S_FULL + w]);
+                }
                 __syncwarp();
             }
-            // every half is waited for, also after an abort, so that all stay in step
+            // Every half is waited for, also after an abort, and then the next scores are announced without products: a
+            // group hands over nothing of a tile before they are, so no warp of it can be at a barrier for the second
+            // time while another, or this one, has yet to come there for the first.
 #pragma unroll 1
             for (int w = 0; w < n_all; ++w) {
                 const int i = w & 1, j = two_u ? w >> 1 : w;
@@ -239,10 +246,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged4_tc_kernel(PagedAttnParam
                 __syncwarp();
                 named_barrier_sync(kNbHalf + 2 * i + 1, kNbHalfThreads);
                 tc_fence_after();
-                if (ok && elect_one()) {
-                    issue_pv(i, j, 1, true);
-                    if (!two_u || i == 1) mma_commit(&bars[F_V_EMPTY + (j & 1)]);
-                    if (more) issue_qk(i, two_u ? j + 1 : j + 2);
+                if (elect_one()) {
+                    if (ok) {
+                        issue_pv(i, j, 1, true);
+                        if (!two_u || i == 1) mma_commit(&bars[F_V_EMPTY + (j & 1)]);
+                        if (more) issue_qk(i, two_u ? j + 1 : j + 2);
+                    } else if (more) {
+                        mbar_arrive(&bars[F_S_FULL + i]);
+                    }
                 }
                 __syncwarp();
             }
@@ -285,9 +296,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged4_tc_kernel(PagedAttnParam
         for (int u = 0; u < units; ++u) {
             const int j = two ? u : 2 * u + i;
             if (ok) ok = warp_wait(&bars[F_S_FULL + i], u & 1, ab, kDevTimeoutSoftmax);
-            if (!ok) {  // after an abort: the halves are handed over still, one by one
-                named_barrier_sync(kNbHalf + 2 * i, kNbHalfThreads);
-                named_barrier_sync(kNbHalf + 2 * i + 1, kNbHalfThreads);
+            if (!ok) {
+                // after an abort: the halves are handed over still, and not before their turn, which the scores announce
+                // (the product warp always comes to that; the bound is for what nobody thought of)
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(&bars[F_S_FULL + i], u & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
+                }
+                hand_over(0);
+                hand_over(1);
                 continue;
             }
             // V of this tile and K of the group's next, tested now and looked at after the exponentials.  (Not before the

@@ -703,6 +703,31 @@ def test_a_wait_that_runs_out_is_reported(rc):
     assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
 
 
+@pytest.mark.parametrize("seqs,hq,hk", [([(200, 900), (30, 400)], 4, 2), ([(40, 3000)], 2, 1), ([(300, 2500)], 2, 2), ([(33, 1100)] * 40, 2, 2)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_waits_that_run_out_at_any_time(rc, seqs, hq, hk, dim):
+    """Limits from nothing to what a call takes: a wait runs out early, late, at some warps only or nowhere.  Each call ends,
+    says so if one did, has its result if none did, and leaves nothing behind for the next."""
+    s = Setup(rc, seqs, hk, dim, 64, seed=dim + hq)
+    q = bf16(s.rng, s.tokens, hq, dim).cuda()
+    good = s.attend(q, False)
+    for limit in [0, 1, 100, 300, 1000, 2000, 4000, 8000, 16000, 32000] * 4:
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+        rc.rc_paged_set_wait_limit(limit)
+        try:
+            s.cache.attend(s.batch, q, out, lse=lse, causal=False)
+        finally:
+            rc.rc_paged_set_wait_limit(2_000_000_000)
+        try:
+            s.cache.sync()
+        except rc.RcError as e:
+            assert e.status == rc.RC_ERR_TIMEOUT
+        else:
+            assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+    again = s.attend(q, False)
+    assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+
+
 def test_new_tokens_that_the_length_does_not_count(rc):
     s = Setup(rc, [(5, 4), (3, 9)], 2, 64, 16, seed=12)
     K = bf16(s.rng, s.tokens, 2, 64)
