@@ -11,6 +11,15 @@ namespace rc {
 constexpr int kBlock4 = 16;              // dims of a scale
 constexpr uint32_t kTopScale4 = 226u;    // 10,240: the largest scale that a row gets
 constexpr uint32_t kFirstNan4 = 248u;    // infinity, and NaN above it
+// Where a row's running maximum (in log2 units) is this large, scores are rounded before it is subtracted, and a maximum is
+// kept as it is: its own weight is 1.  Below, a weight is exp2 of one multiply-add of the score with a maximum kept
+// some units lower, where rounding moves the exponent by 2^-5 at most; far above, that would be more than fp16 weights allow.
+constexpr float kLargeScore4 = 0x1p20f;
+// That is looked at where a query row's largest value is 16 or more (its power of two in query_tile_f16 2^-10 then): of others
+// no score is over 16 x 128 x 61,440 x log2(e) / sqrt(128) < 2^24, where the exponent moves by 2^-1 and weights still fit.
+// (32 x 8,000 tokens with 16 rows: 81.4 us without the question, 82.4 so, 83.2 if all rows are asked; a prefill 489, 491 and
+// 496, with queries of 64 times the size 556 without and 564 with it.)
+constexpr float kLargeQuery4 = 0x1p-10f;
 
 __device__ __forceinline__ float scale4_value(uint32_t b) { return __half2float(__ushort_as_half(static_cast<unsigned short>(b << 7))); }
 

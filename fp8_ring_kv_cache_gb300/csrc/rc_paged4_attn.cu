@@ -16,7 +16,7 @@
 //                    held in the same order.  Rows of Q are scaled to fp16's range.
 //   P = exp2(S - max + 14), online, rounded to fp16 (2^-12 of each weight; weights down
 //                    to 2^-28 of the largest keep all their bits, the row sums are
-//                    not rounded); an 8 x 8 transpose of the accumulators makes them
+//                    not rounded; scores from 2^20 on: kLargeScore4); an 8 x 8 transpose of the accumulators makes them
 //                    the B operand of
 //   O^T += V^T P^T   whose A operand is an 8-byte piece of a V row: 16 tokens of one dim.
 //                    The tokens of S's rows are chosen to match.
@@ -32,6 +32,7 @@
 // arithmetic alone 54: neither hides the other wholly.  (Codes straight into registers, a
 // block a fixed split: 76 us.)
 #include <algorithm>
+#include <type_traits>
 
 #include "rc_paged4.cuh"
 
@@ -216,6 +217,12 @@ __device__ __forceinline__ void attend_piece(const PagedAttnParams& p, RowsSmem<
         cp_async_commit();
     }
     query_tile_f16<D, NR, D / 4>(qrow, live, p.sm_log2, qb, qscale);
+    bool may_be_large = false;  // (rows of zeros are taken for such, but for those past the end)
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) may_be_large |= limit[r][x] != 1 << 30 && qscale[r][x] >= p.sm_log2 * kLargeQuery4;
+    may_be_large = __any_sync(0xffffffffu, may_be_large);
     // what every row sees
     const int least = min(j1, p.causal ? max(0, q.kv - q.n + 1) : q.kv);
 
@@ -308,32 +315,41 @@ __device__ __forceinline__ void attend_piece(const PagedAttnParams& p, RowsSmem<
         }
         bool moved = false;
         float alpha[NR][2];
+        auto softmax = [&](auto large) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
+            for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float mx = -INFINITY;
+                for (int x = 0; x < 2; ++x) {
+                    float mx = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mx = max3(mx, sc[r][i][x], sc[r][i][2 + x]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const float m_new = fmaxf(m_run[r][x], mx * qscale[r][x] - kWeightShift);
-                const float base = m_new == -INFINITY ? 0.f : m_new;
-                alpha[r][x] = ex2(m_run[r][x] - base);  // 0 while nothing was seen
-                m_run[r][x] = m_new;
-                moved |= alpha[r][x] != 1.f;
-                float sum = 0.f;
+                    for (int i = 0; i < 4; ++i) mx = max3(mx, sc[r][i][x], sc[r][i][2 + x]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    float m_new = fmaxf(m_run[r][x], fmaf(mx, qscale[r][x], -kWeightShift));
+                    const bool far = large && m_new != -INFINITY && fabsf(m_new) >= kLargeScore4;
+                    if (far) m_new = fmaxf(m_run[r][x], __fmul_rn(mx, qscale[r][x]));
+                    const float base = m_new == -INFINITY ? 0.f : m_new;
+                    alpha[r][x] = ex2(m_run[r][x] - base);  // 0 while nothing was seen
+                    m_run[r][x] = m_new;
+                    moved |= alpha[r][x] != 1.f;
+                    float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        const float w = ex2(fmaf(sc[r][i][2 * a + x], qscale[r][x], -base));
-                        sc[r][i][2 * a + x] = w;
-                        sum += w;
-                    }
-                l_run[r][x] = l_run[r][x] * alpha[r][x] + sum;
-            }
+                        for (int a = 0; a < 2; ++a) {
+                            const float v = sc[r][i][2 * a + x];
+                            const float w = ex2(far ? __fadd_rn(__fmul_rn(v, qscale[r][x]), -base) : fmaf(v, qscale[r][x], -base));
+                            sc[r][i][2 * a + x] = w;
+                            sum += w;
+                        }
+                    l_run[r][x] = l_run[r][x] * alpha[r][x] + sum;
+                }
+        };
+        if (may_be_large)
+            softmax(std::true_type{});
+        else
+            softmax(std::false_type{});
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
             for (int r = 0; r < NR; ++r)

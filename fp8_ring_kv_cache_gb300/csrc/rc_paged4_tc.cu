@@ -13,7 +13,7 @@
 // operands: rows of Q are brought to fp16's range by a power of two, which multiplies
 // their scores in the softmax, and P has 11 bits; it is kept 2^7 larger (and the
 // running maximum 7 lower), so that a weight of 2^-21 of the largest still has all of
-// them.
+// them.  (Scores from 2^20 on: kLargeScore4.)
 // The work of a group is a chain of KV tiles: S = Q K^T into TMEM; softmax of a row by
 // its thread: P to fp16, over S; O += P V with P read from TMEM.  With more than 128
 // rows group i has rows [128 i, 128 i + 128) and both groups take each tile; with fewer
@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged4_tc_kernel(PagedAttnParam
         const int limit = (!live || !p.causal ? j1 : min(j1, max(0, q.kv - q.n + tok + 1))) - j0;
         const float a = reinterpret_cast<const float*>(smem + Lay::kQScale)[(two ? kTileM * i : 0) + r];
         const float2 a2 = make_float2(a, a);
+        const bool may_be_large = __any_sync(0xffffffffu, live && a >= p.sm_log2 * kLargeQuery4);
         constexpr float kBelow = 7.f;  // of the running maximum
         float m_run = -INFINITY, l_run = 0.f;
         bool ok = true;
@@ -331,48 +332,78 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged4_tc_kernel(PagedAttnParam
                 for (int k = 8; k < kTileN; k += 8)
                     mx[c] = max3(mx[c], __uint_as_float(x[k + c]), __uint_as_float(x[k + 4 + c]));
             }
-            const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a - kBelow;
+            const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float m_tile = fmaf(most, a, -kBelow);
             // the running max moves only when a tile raises it by more than 2^8 of
             // weight: fp16 (up to 2^15) and fp32 hold the larger weights as well
             const bool bump = (m_run == -INFINITY) || (m_tile > m_run + 8.f);
-            const float m_new = bump ? fmaxf(m_run, m_tile) : m_run;
-            const float base = (m_new == -INFINITY) ? 0.f : m_new;
-            const float alpha = bump ? ex2(m_run - base) : 1.f;
+            float m_new = bump ? fmaxf(m_run, m_tile) : m_run;
+            float base = (m_new == -INFINITY) ? 0.f : m_new;
+            float alpha = bump ? ex2(m_run - base) : 1.f;
             // rescale the running output when the max moved (the products of the tile before have finished: the scores
             // came after them)
-            if (__any_sync(0xffffffffu, u > 0 && alpha != 1.f)) {
+            auto rescale = [&](float by) {
+                if (!__any_sync(0xffffffffu, u > 0 && by != 1.f)) return;
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t y[16];
                     tmem_ld16(o_tm + 16 * c, y);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * alpha);
+                    for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * by);
                     tmem_st16(o_tm + 16 * c, y);
                 }
                 tmem_st_wait();
-            }
-            const float2 n2 = make_float2(-base, -base);
+            };
+            rescale(alpha);
             float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int k = 0; k < kHalfN; k += 4) {
-                    const uint32_t* w = x + kHalfN * half + k;
-                    const float2 x0 = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), a2, n2);
-                    const float2 x1 = fma2(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), a2, n2);
-                    const float2 q0 = make_float2(ex2(x0.x), ex2(x0.y));
-                    const float2 q1 = make_float2(ex2(x1.x), ex2(x1.y));
-                    ls0 = add2(ls0, q0);
-                    ls1 = add2(ls1, q1);
-                    pk[k / 2] = pack_f16(q0.x, q0.y);
-                    pk[k / 2 + 1] = pack_f16(q1.x, q1.y);
-                }
-                tmem_st32(s_tm + kHalfN * half, pk);
+            auto give = [&](int half) {
                 tmem_st_wait();
                 if (watcher && half == 0 && !v_in) ok = mbar_wait(&bars[F_V_FULL + (j & 1)], (j >> 1) & 1, ab, kDevTimeoutSoftmax);
                 if (watcher && half == 1 && !k_in) ok = mbar_wait(&bars[F_K_FULL + (jk & 1)], (jk >> 1) & 1, ab, kDevTimeoutSoftmax) && ok;
                 hand_over(half);
+            };
+            if (may_be_large && __any_sync(0xffffffffu, fabsf(base) >= kLargeScore4)) {
+                if (fabsf(base) >= kLargeScore4) m_new = fmaxf(base, __fmul_rn(most, a));
+                const float by = m_new == -INFINITY ? 1.f : ex2(base - m_new);
+                rescale(by);
+                alpha *= by;
+                base = m_new == -INFINITY ? 0.f : m_new;
+                // (a few columns at a time, so that this costs the other way no registers)
+#pragma unroll 1
+                for (int c = 0; c < kTileN / 32; ++c) {
+                    uint32_t y[32], pk[16];
+                    tmem_ld32(s_tm + 32 * c, y);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float2 w;
+                        w.x = ex2(32 * c + k < room ? __fadd_rn(__fmul_rn(__uint_as_float(y[k]), a), -base) : -INFINITY);
+                        w.y = ex2(32 * c + k + 1 < room ? __fadd_rn(__fmul_rn(__uint_as_float(y[k + 1]), a), -base) : -INFINITY);
+                        ls0 = add2(ls0, w);
+                        pk[k / 2] = pack_f16(w.x, w.y);
+                    }
+                    tmem_st16(s_tm + 16 * (c & 1) + kHalfN * (c >> 1), pk);
+                    if (c & 1) give(c >> 1);
+                }
+            } else {
+                const float2 n2 = make_float2(-base, -base);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int k = 0; k < kHalfN; k += 4) {
+                        const uint32_t* w = x + kHalfN * half + k;
+                        const float2 x0 = fma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), a2, n2);
+                        const float2 x1 = fma2(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), a2, n2);
+                        const float2 q0 = make_float2(ex2(x0.x), ex2(x0.y));
+                        const float2 q1 = make_float2(ex2(x1.x), ex2(x1.y));
+                        ls0 = add2(ls0, q0);
+                        ls1 = add2(ls1, q1);
+                        pk[k / 2] = pack_f16(q0.x, q0.y);
+                        pk[k / 2 + 1] = pack_f16(q1.x, q1.y);
+                    }
+                    tmem_st32(s_tm + kHalfN * half, pk);
+                    give(half);
+                }
             }
             ok = __all_sync(0xffffffffu, ok);
             l_run = l_run * alpha + ((ls0.x + ls0.y) + (ls1.x + ls1.y));

@@ -666,7 +666,8 @@ int rc_paged4_write(const rc_paged4_view *view, const rc_paged_batch *batch, con
 /*
  * Attention of each sequence's new tokens over its pages; arguments and errors
  * as rc_paged_attend.  A row of Q is held in fp16 relative to its largest value: what lies under
- * 2^-32 of that loses bits.
+ * 2^-32 of that loses bits.  Scores are fp32: a row with one of 2^126 or more in magnitude reads as some
+ * number, infinity or NaN.
  */
 int rc_paged4_attend(const rc_paged4_view *view, const rc_paged_batch *batch, const void *Q_bf16, int64_t q_stride,
                      int heads, void *out_bf16, int64_t out_stride, float *lse, int causal, void *stream);

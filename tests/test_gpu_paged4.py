@@ -403,6 +403,62 @@ def test_attend_spread_of_sizes(rc, seqs, hq, hk, dim):
     s.check_attend(q, True)
 
 
+@pytest.mark.parametrize("seqs,hq,hk", [([(1, 90), (1, 1), (1, 1500)], 4, 1), ([(3, 700), (1, 2)], 12, 2), ([(1, 20000)], 8, 1), ([(30, 500), (1, 1)], 3, 1),
+                                        ([(200, 1000), (90, 90)], 4, 2)])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("size", [2.0 ** 16, 2.0 ** 20, 2.0 ** 24, 2.0 ** 27, 2.0 ** 32, 2.0 ** 60, 2.0 ** 110, -(2.0 ** 26), 2.0])
+def test_attend_large_scores(rc, seqs, hq, hk, dim, page, size):
+    """Scores far over what weights can be told apart by (size 2: rows of Q under 16, K with the largest scale): every result is finite, and where the largest score leads the others
+    by 30 and more than what rounding may be (2^-17 (1 + b) each), it is that token's V and its score; with two tokens of the
+    same K it is the mean of both their V."""
+    s = Setup(rc, seqs, hk, dim, page, seed=dim + page, spread=0.3)
+    if size == 2.0:
+        s.pool["kscale"][:] = pu.TOP
+    for i, (new, kv) in enumerate(seqs):  # the last token's K is the first one's too
+        first, last = (s.meta["table"][i, j // page] for j in (0, kv - 1))
+        s.pool["kcodes"][first, :, 0] = s.pool["kcodes"][last, :, (kv - 1) % page]
+        s.pool["kscale"][first, :, :, 0] = s.pool["kscale"][last, :, :, (kv - 1) % page]
+    s.upload()
+    q = bf16(s.rng, s.tokens, hq, dim) * size
+    for t in s.meta["q_start"][1:] - 1:  # the last query of a sequence looks for its last token
+        i = int(np.searchsorted(s.meta["q_start"], t, side="right")) - 1
+        kv = int(s.meta["kv_len"][i])
+        for head in range(hq):
+            k = pu.tokens_of(s.pool, "k", s.meta["table"][i], head * hk // hq, kv)[-1]
+            q[t, head] = torch.from_numpy((7.96 * k / np.abs(k).max()).astype(np.float32)).to(torch.bfloat16) * size
+    out, lse = s.attend(q.cuda(), True)
+    out, lse, qn = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().numpy()
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    sure = twice = 0
+    for i, (new, kv) in enumerate(seqs):
+        q0 = s.meta["q_start"][i]
+        for head in range(hq):
+            k, v = (pu.tokens_of(s.pool, x, s.meta["table"][i], head * hk // hq, kv) for x in "kv")
+            for t in range(new):
+                see = kv - new + t + 1
+                x = k[:see] @ qn[q0 + t, head] / np.sqrt(dim)
+                off = 2.0 ** -17 * (1 + (np.abs(k[:see]) @ np.abs(qn[q0 + t, head]) / np.sqrt(dim)).max())
+                top = x.max()
+                lead = np.nonzero(x >= top - 2 * off - 30)[0]
+                g, tol = out[q0 + t, head], off + 2.0 ** -20 * abs(top)
+                # (what is behind has weights under e^-30 each)
+                if len(lead) == 1:
+                    sure += 1
+                    assert (np.abs(g - v[lead[0]]) <= 2.0 ** -8 * np.abs(v[lead[0]]) + see * np.exp(-30.0) * np.abs(v[:see]).max()).all(), (i, head, t)
+                    assert abs(lse[q0 + t, head] - top) <= tol + see * np.exp(-30.0)
+                elif len(lead) == 2 and lead[0] == 0 and lead[1] == kv - 1 == see - 1:
+                    twice += 1
+                    want = (v[0] + v[-1]) / 2
+                    # (two weights rounded to fp16 each, the result to bf16)
+                    assert (np.abs(g - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + see * np.exp(-30.0)) * np.abs(v[:see]).max()).all(), (i, head, t)
+                    assert abs(lse[q0 + t, head] - top - np.log(2.0)) <= tol + see * np.exp(-30.0)
+                else:
+                    low, high = v[lead].min(0), v[lead].max(0)
+                    reach = 2.0 ** -8 * np.abs(g) + (2.0 ** -10 + see * np.exp(-30.0)) * np.abs(v[:see]).max()
+                    assert (g >= low - reach).all() and (g <= high + reach).all(), (i, head, t)
+    assert sure + twice > 0 and (size < 2.0 ** 20 or twice > 0) and (size != 2.0 or np.abs(qn).max() < 16.0)
+
+
 @pytest.mark.parametrize("rows", [1, 5, 40])
 def test_attend_rows_that_see_nothing(rc, rows):
     """More new tokens than cached ones: the first rows see no token; a sequence without any."""
