@@ -25,6 +25,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from ._binding import _check, lib
 
@@ -187,21 +188,35 @@ class RopeAxes:
         self._ptr = ctypes.addressof(self.plan)
 
 
+def _packed(dy):
+    """dy as rows that the kernel takes (a broadcast gradient or tangent has no such strides)."""
+    dy = dy.contiguous()
+    return dy.clone() if dy.data_ptr() % 16 else dy
+
+
 class _Turn(torch.autograd.Function):
-    """The turn with its gradient, the turn back."""
+    """The turn with its gradient, the turn back, and its tangent, the turn of x's."""
 
     @staticmethod
     def forward(ctx, x, positions, rope, inverse, turn):
         ctx.rope, ctx.inverse, ctx.turn = rope, inverse, turn
         ctx.save_for_backward(positions)
+        ctx.save_for_forward(positions)
         return turn(x.detach(), positions, rope, None, inverse)
 
     @staticmethod
     def backward(ctx, dy):
-        dy = dy.contiguous()  # (a broadcast gradient has no strides that the kernel takes)
-        if dy.data_ptr() % 16:
-            dy = dy.clone()
-        return ctx.turn(dy, ctx.saved_tensors[0], ctx.rope, None, not ctx.inverse), None, None, None, None
+        return ctx.turn(_packed(dy), ctx.saved_tensors[0], ctx.rope, None, not ctx.inverse), None, None, None, None
+
+    @staticmethod
+    def jvp(ctx, dx, *_):
+        return ctx.turn(_packed(dx), ctx.saved_tensors[0], ctx.rope, None, ctx.inverse)
+
+
+def _has_tangent(x) -> bool:
+    # (outside of a dual level nothing has one: that is asked first, in 0.1 us where unpack_dual takes 0.4)
+    return getattr(forward_ad, "_current_level", 0) >= 0 and isinstance(x, torch.Tensor) and \
+        forward_ad.unpack_dual(x).tangent is not None
 
 
 def _turned(x, positions, rope, out, inverse, stream, what: str, fn, turn):
@@ -220,15 +235,18 @@ def _turned(x, positions, rope, out, inverse, stream, what: str, fn, turn):
         raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {dtype}")
     if dim != rope.head_dim:
         raise ValueError(f"x has head_dim {dim}, the plan {rope.head_dim}")
-    if (x.requires_grad or getattr(out, "requires_grad", False)) and torch.is_grad_enabled():
+    dual = _has_tangent(x) or _has_tangent(out)
+    if dual or ((x.requires_grad or getattr(out, "requires_grad", False)) and torch.is_grad_enabled()):
         if out is not None:
-            raise RuntimeError(f"{what}: out= is not differentiable, but x or out requires a gradient")
+            raise RuntimeError(f"{what}: out= is not differentiable, but x or out requires a gradient or has a tangent")
         if stream is None:
             return _Turn.apply(x, positions, rope, inverse, turn)
         own, current = _stream(stream, device), torch.cuda.current_stream(device)
         with torch.cuda.stream(own):  # (autograd runs the gradient on the stream of the turn)
             y = _Turn.apply(x, positions, rope, inverse, turn)
         y.record_stream(current)
+        if dual:
+            forward_ad.unpack_dual(y).tangent.record_stream(current)
         return y
     xp, xs = _rows(x, dtype, n, heads, dim, "x", device)
     if out is x:
@@ -250,8 +268,8 @@ def _turned(x, positions, rope, out, inverse, stream, what: str, fn, turn):
 def rc_rope_axes(x, positions, rope: RopeAxes, out=None, inverse: bool = False, stream=None):
     """x [n][heads][head_dim] (bf16 or fp32) turned at positions (int32 [axes][n]); inverse turns back, which is also
     the gradient: dx = rc_rope_axes(dy, positions, rope, inverse=True).  out defaults to a new tensor (of the call's
-    stream, kept from reuse for the current one too) and may be x.  Autograd records the call if x requires a gradient;
-    as with torch's own functions, not with out=, which is refused then."""
+    stream, kept from reuse for the current one too) and may be x.  Autograd records the call if x requires a gradient,
+    and the result has a tangent if x has one; as with torch's own functions, not with out=, which is refused then."""
     return _turned(x, positions, rope, out, inverse, stream, "rc_rope_axes", lib.rc_rope_axes, rc_rope_axes)
 
 
