@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kRun * D / 8, 384 / D) paged4_write_kernel(con
     __shared__ uint32_t scode[kMaxHeads][kRun][LANES + 1];             // V's codes
     __shared__ uint2 sold[8][kMaxHeads * kCodeJobs];                   // the words that they go into, of a run that is not all new
     __shared__ __align__(16) uint8_t sscale[kMaxHeads][2][NB][kRun];   // K's and V's scale bytes
-    __shared__ uint16_t skey[PART == kAnywhere ? kThreads * 8 : 1];    // K's rows
+    __shared__ __align__(16) uint16_t skey[PART == kAnywhere ? kThreads * 8 : 1];  // K's rows
     const int s = blockIdx.x / runs, run = blockIdx.x % runs;
     const Seq q = load_seq(p.g, s);
     if (q.n == 0) return;

@@ -3,7 +3,9 @@ checks, which come before any device work (the addresses here are never read).""
 import copy
 import ctypes
 import functools
+import os
 import pickle
+import re
 from fractions import Fraction
 
 import numpy as np
@@ -241,3 +243,19 @@ def test_a_copy_of_a_form_has_numbers_of_its_own(rc, make, how):
     other = how(form)
     assert other._ptr == ctypes.addressof(numbers(other))
     assert bytes(numbers(other)) == want
+
+
+def test_shared_arrays_lie_on_the_boundaries_of_their_accesses():
+    """Shared arrays that the kernels' sources read or write as vectors are declared with the vectors' alignment."""
+    here = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "fp8_ring_kv_cache_gb300", "csrc")
+    size = {"uint2": 8, "float2": 8, "uint4": 16, "float4": 16, "int4": 16}
+    checked = 0
+    for name in sorted(os.listdir(here)):
+        with open(os.path.join(here, name)) as f:
+            text = f.read()
+        for align, kind, array in re.findall(r"__shared__\s+(?:__align__\((\d+)\)\s+)?(\w+)\s+(\w+)\s*\[", text):
+            for access in re.findall(r"reinterpret_cast<(?:const )?(\w+)\s*\*>\(\s*&?" + array + r"\b", text):
+                if access in size:
+                    checked += 1
+                    assert max(int(align or 1), size.get(kind, 1)) >= size[access], (name, array, access)
+    assert checked >= 2
