@@ -60,7 +60,9 @@ class RopeForm:
     """A form of rotary positions: dims first .. first + dims - 1 of a head turn (dims: the rest of the head, or twice the
     sum of `sections`), as neighbouring "pairs" or as "halves" of that part; sections: pairs of each axis (one axis by
     default).  scaling: None, "linear", "base" or "parts", by `factor`; "parts" also reads context, low and high, the
-    turns in `context` positions between which a frequency goes over from stretched to kept.  gain multiplies what turns."""
+    turns in `context` positions between which a frequency goes over from stretched to kept, evenly over the turns (a model
+    that was trained with the same evenly over the pairs' numbers, or with factors of its own for each pair, has other
+    frequencies, which this class does not make).  gain multiplies what turns."""
 
     def __init__(self, head_dim: int, sections=None, dims=None, first: int = 0, layout: str = "pairs", base: float = 10000.0,
                  shared_freqs: bool = False, scaling=None, factor: float = 1.0, context: float = 0.0, low: float = 1.0,

@@ -28,9 +28,10 @@
 // from when its products are.  V's scales are made fp16 once a chunk by one lane each,
 // and read by all.
 // 32 single tokens (sequences of 61 to 16,381 tokens, 8 KV heads x 6 query heads x 128):
-// 62 us for 304 MB, 0.73 of the rate of a copy.  The copies alone take 55 us, the
+// 62.5 us for 304 MB, 0.73 of the rate of a copy.  The copies alone take 55 us, the
 // arithmetic alone 54: neither hides the other wholly.  (Codes straight into registers, a
-// block a fixed split: 76 us.)
+// block a fixed split: 76 us.  Looking for large scores is in the 62.5 with 0.6 us; the
+// times at the rules below were taken without it.)
 #include <algorithm>
 #include <type_traits>
 
@@ -132,8 +133,8 @@ __device__ __forceinline__ void attend_piece(const PagedAttnParams& p, RowsSmem<
     const int P = 1 << p.g.page_shift;
 
     // ---- the copies of a chunk of 64 tokens.  Lane l's page is that of the chunk's block l % 4, looked up a chunk ahead.  A
-    // block behind the sequence's end, or on a bad page, is read from page 0 instead, and its tokens are cut off (K) or given
-    // the scale 0 (V).
+    // block behind the sequence's end, or on a bad page, is read from page 0 instead.  Tokens behind the end are cut off (K)
+    // and given the scale 0 (V); those on a bad page have page 0's scores and the scale 0: that call's results are void.
     const uint32_t* pages =
         reinterpret_cast<const uint32_t*>(p.g.page_table + static_cast<size_t>(s) * p.g.table_pages);
     auto entry = [&](int jc) {

@@ -27,12 +27,14 @@
 // looks which group is ready: 119 us; units of 64 tokens with two places of scores a group,
 // so that scores are always ahead: 138 us, as products of 64 columns take as long as
 // those of 128.)
-// 757 queries x 5,788 tokens x 48 heads x 128: 87.3 us, 1.23 PFLOP/s, 0.65 of what a
-// library product of bf16 matrices reaches; the tensor cores work 55 % of the time.  A
-// tile takes 3,500 cycles for both groups, 1,750 each for products of 1,024.  By
-// arithmetic shared memory explains that (not measured by itself): a score product reads
-// 8 KB in 64 cycles, all that 128 bytes a cycle give, and the converters' stores, 64 KB a
-// tile, come in between.
+// 757 queries x 5,788 tokens x 48 heads x 128: 87.4 us, 1.23 PFLOP/s, 0.65 of what a
+// library product of bf16 matrices reaches; the tensor cores work 52 to 55 % of the time
+// of the SMs that have a block.  A tile takes 3,500 cycles for both groups, 1,750 each for
+// products of 1,024.  What the rest is, is not known: by arithmetic the products' operands
+// and the converters' stores are 2,048 cycles of shared memory a tile, the counters show
+// its banks read in 21 % of the cycles and written in 9 % (conflicts are 3 % of the stores),
+// and issue slots are used in 54 %.  A trace shows 200 to 250 cycles between the hand-over
+// of a half and its products.
 // A row sees the cached tokens from the first on, so a token whose V is not a number is
 // remembered by the first such one's number: the row has it if it sees that far.
 #include "rc_paged4.cuh"
@@ -518,8 +520,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged4_tc_kernel(PagedAttnParam
         // while it waits for a free buffer.  Lane l < 8 of a warp looks up where
         // the tile's tokens [16 l, 16 l + 16) are: the number of their block of
         // 16 among the pool's (page, head, 16 tokens).  Blocks behind the end of
-        // the sequence, or on a bad page, read block 0 instead: the softmax cuts
-        // K's columns, and V's get the scale 0, as P is 0 there.
+        // the sequence, or on a bad page, read block 0 instead.  Behind the end the
+        // softmax cuts K's columns, and V's get the scale 0, as P is 0 there; a bad
+        // page's tokens have block 0's scores and V, and the call's results are void.
         regs_dec<56>();
         const int ct = tid & 127;
         const int pb = p.g.page_shift - 4;  // blocks of a page: 1 << pb

@@ -121,8 +121,9 @@ __global__ void __launch_bounds__(kRowsThreads, NR == 1 ? 3 : 2) paged_rows_kern
     for (int jc = j0 + warp * kChunk; jc < j1; jc += kStride) {
         // The lane reads K rows and scales of the 16-token block g >> 1 and V
         // pieces and scales of block t.  A block behind the sequence's end, or on
-        // a bad page, is read from page 0 instead, and its tokens are cut off (K)
-        // or given the factor 0 (V).
+        // a bad page, is read from page 0 instead.  Tokens behind the end are cut off
+        // (K) and given the factor 0 (V); those on a bad page have page 0's scores
+        // and the factor 0, and the call's results are void.
         const int vblk = jc + 16 * t, kblk = jc + 16 * (g >> 1);
         const bool vok = vblk < q.kv && check_page(p.g, ahead);
         const uint32_t mine = static_cast<uint32_t>(vok ? ahead : 0);

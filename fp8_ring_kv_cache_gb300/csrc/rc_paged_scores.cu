@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, NR == 1 ? 7 : D == 64 ? 5 : 
     int jc = j0 + warp * kFewChunk;
     int ahead = entry(jc);
     for (; jc < end; jc += kStride) {
-        // (a block of 16 tokens behind the end, or on a bad page: page 0 is read, its tokens are cut off)
+        // (a block of 16 tokens behind the end, or on a bad page: page 0 is read; tokens behind the end are cut off, with a bad
+        // page the results are void)
         const int blk = jc + 16 * t;
         const uint32_t mine = static_cast<uint32_t>(blk < q.kv && check_page(p.g, ahead) ? ahead : 0);
         const size_t kph = static_cast<size_t>(__shfl_sync(0xffffffffu, mine, g >> 1)) * p.g.kv_heads + h;

@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(kStThreads, 1) paged_scores_tc_kernel(PagedSco
         };
         uint4 k[NB];
         uint32_t scale;
-        // pieces c, c + 1 of the row (tokens behind the end, or on a bad page, read the first token of page 0: their sums are not used)
+        // pieces c, c + 1 of the row (tokens behind the end, or on a bad page, read the first token of page 0: behind the end the
+        // sums are not used, with a bad page the results are void)
         auto row_of = [&](const Step& x, int page) {
             const int t = j0 + x.i * kStTile + ct;
             const bool have = x.rb < w.blocks && t < q.kv && check_page(p.g, page);

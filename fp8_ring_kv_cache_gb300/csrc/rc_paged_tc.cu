@@ -29,7 +29,7 @@
 // that order is kept along the summed dims (Q is stored in it) and along the
 // cached tokens (P is packed in it).
 //
-// 757 queries x 5,788 tokens x 48 heads x 128: 105 us, 1.03 PFLOP/s, 0.54 of what
+// 757 queries x 5,788 tokens x 48 heads x 128: 102 us, 1.05 PFLOP/s, 0.56 of what
 // a library product of bf16 matrices reaches; the tensor cores work 47 % of the
 // time.  What bounds it is the chain of a unit (scores to registers, maximum,
 // exponentials, P back, the hand-over to the products), which two groups do not
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
             if (!warp_wait(&bars[T_S_FULL + i], (u >> 1) & 1, ab, kDevTimeoutSoftmax)) return false;
             // V of this unit and K of unit u + 2, tested now and looked at after the softmax.  (Not before the scores are
             // there: with one row tile K of unit u lies in the same buffer, and while it is not in place the test would
-            // answer for the phase before.)
+            // answer for the phase before.  Nor is it faster, where it can be done: 104.1 us for the chunk above.)
             const int jk = tile_of(u + 2);
             const bool want_k = u + 2 < U;
             bool vk = true;
@@ -440,8 +440,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(PagedAttnParams
         // while it waits for a free buffer.  Lane l < 8 of a warp looks up where
         // the tile's tokens [16 l, 16 l + 16) are: the number of their block of
         // 16 among the pool's (page, head, 16 tokens).  Blocks behind the end of
-        // the sequence, or on a bad page, read block 0 instead: the softmax cuts
-        // K's columns, and V's get the scale byte 0 (a finite factor), as P is 0 there.
+        // the sequence, or on a bad page, read block 0 instead.  Behind the end the
+        // softmax cuts K's columns, and V's get the scale byte 0 (a finite factor), as
+        // P is 0 there; a bad page's tokens have block 0's, and the results are void.
         // Neighbouring groups of four lanes have neighbouring rows, whose
         // swizzles differ in the lowest bit: the stores meet no bank conflict.
         regs_dec<56>();

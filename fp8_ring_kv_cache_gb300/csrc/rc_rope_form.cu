@@ -1,4 +1,4 @@
-// rc_rope_form.cu -- rotary positions in the forms that models have
+// rc_rope_form.cu -- rotary positions in other forms than rc_rope_axes'
 // (rc_rope_turn): neighbouring pairs or halves, a part of the head, a gain;
 // forward, or back (the gradient: the turn's transpose with the same gain).
 //   (a, b) -> g (a cos - b sin, a sin + b cos) per pair, the other dims copied

@@ -409,7 +409,7 @@ int rc_rope_axes(const rc_rope_plan *plan, const void *x, int64_t x_stride, void
 
 /* ---- rotary positions in other forms ---------------------------------------- */
 /*
- * The forms that rotary embeddings have beside the one above: the turned pairs
+ * Forms of rotary embeddings beside the one above: the turned pairs
  * are neighbours or lie half a part apart, a part of the head turns, frequencies
  * are stretched for contexts longer than a model was trained for, and what is
  * turned is multiplied by a gain.  Dims first .. first + dims - 1 of a head turn,
@@ -427,6 +427,11 @@ int rc_rope_axes(const rc_rope_plan *plan, const void *x, int64_t x_stride, void
  *   RC_ROPE_SCALE_PARTS   theta (k + (1 - k) / factor), where k goes from 0 to 1
  *                         as the pair's turns in `context` positions,
  *                         context theta / 2 pi, go from low to high
+ * A model has to be run with the frequencies that it was trained with: those that
+ * go from stretched to kept evenly over the pairs' NUMBERS (between two pairs that
+ * turns give, rounded or not) differ from RC_ROPE_SCALE_PARTS by tens of percent
+ * for some pairs, and neither they nor a table of factors for each pair are among
+ * these forms.
  * One token at one axis with RC_ROPE_PAIRS, the whole head and a gain of 1 is
  * what rc_rope_axes does.
  */
@@ -508,9 +513,10 @@ int rc_rope_turn(const rc_rope_form *form, const void *x, int64_t x_stride, void
  * that takes more than 2^31 - 1 blocks (seqs x max_new / 16 of a write, seqs x
  * kv_heads x a KV head's query rows / 256 of an attention) a call is refused
  * (RC_ERR_UNSUPPORTED).  Metadata out of these bounds (or a page id that
- * is not one of the pool's) is found on the device: the sequence (or page) is
- * left out, nothing is read or written out of bounds, and rc_paged_status
- * reports RC_ERR_ARG; that call's results are not valid.
+ * is not one of the pool's) is found on the device: the sequence is left out, such
+ * a page is not written, and where it would be read page 0 is; nothing is read or
+ * written out of bounds, and rc_paged_status reports RC_ERR_ARG; that call's
+ * results are not valid.
  *
  * workspace: device memory of RC_PAGED_WORKSPACE_BYTES, 256-byte aligned,
  * zeroed once by the caller before its first use.  It holds the status word
